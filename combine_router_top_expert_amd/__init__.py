@@ -24,14 +24,16 @@ MAX_SOURCES = 64
 
 STATUS = {
     0: "MOK_OK", -1: "MOK_EINVAL", -2: "MOK_ESHAPE", -3: "MOK_EDEVICE", -4: "MOK_ECAPACITY",
-    -5: "MOK_ETIMEOUT", -6: "MOK_EROUTE", -7: "MOK_ESCRATCH",
+    -5: "MOK_ETIMEOUT", -6: "MOK_EROUTE", -7: "MOK_ESCRATCH", -8: "MOK_EGROUP",
 }
 
 # every symbol include/mok.h declares
 EXPORTS = ("mok_workspace_bytes", "mok_route", "mok_layout", "mok_dispatch", "mok_expert_ffn",
            "mok_combine", "mok_layer_fwd", "mok_layer_bwd", "mok_mx_quantize", "mok_tune_fwd",
            "mok_ring_layout", "mok_hbm_stream", "mok_layer_fwd_noalloc", "mok_layer_fwd_macro",
-           "mok_prepare_bwd", "mok_mx_quantize_f32", "mok_mfma_probe", "mok_version")
+           "mok_prepare_bwd", "mok_mx_quantize_f32", "mok_mfma_probe", "mok_route_logits",
+           "mok_balance_ws_bytes", "mok_balance_fwd", "mok_balance_bwd", "mok_router_bwd_ws_bytes",
+           "mok_router_bwd", "mok_grad_norm_ws_bytes", "mok_grad_norm", "mok_adamw", "mok_version")
 
 
 class MokError(RuntimeError):
@@ -187,13 +189,35 @@ class mok_fwd_state(ctypes.Structure):
     _fields_ = [("topk_idx", ctypes.c_void_p), ("topk_gate", ctypes.c_void_p),
                 ("counts", ctypes.c_void_p), ("offsets", ctypes.c_void_p),
                 ("row_src", ctypes.c_void_p), ("dest_row", ctypes.c_void_p),
-                ("h", ctypes.c_void_p), ("ab", ctypes.c_void_p), ("h_scale", ctypes.c_void_p)]
+                ("h", ctypes.c_void_p), ("ab", ctypes.c_void_p), ("h_scale", ctypes.c_void_p),
+                ("logits", ctypes.c_void_p)]
 
 
 class mok_layer_call(ctypes.Structure):
     _fields_ = [("own_lo", ctypes.c_int32), ("own_n", ctypes.c_int32),
                 ("src_x", ctypes.c_void_p), ("st", ctypes.POINTER(mok_fwd_state)),
                 ("staging", ctypes.c_void_p), ("out", ctypes.c_void_p)]
+
+
+class mok_balance(ctypes.Structure):
+    _fields_ = [("alpha", ctypes.c_float), ("beta", ctypes.c_float), ("G", ctypes.c_int32),
+                ("group_offsets", ctypes.c_void_p), ("token_mask", ctypes.c_void_p)]
+
+
+class mok_param(ctypes.Structure):
+    _fields_ = [("p", ctypes.c_void_p), ("g", ctypes.c_void_p), ("master", ctypes.c_void_p),
+                ("m", ctypes.c_void_p), ("v", ctypes.c_void_p), ("m_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("n", ctypes.c_int64), ("p_type", ctypes.c_int32),
+                ("g_type", ctypes.c_int32), ("state_bits", ctypes.c_int32),
+                ("weight_decay", ctypes.c_float)]
+
+
+class mok_adamw_args(ctypes.Structure):
+    _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
+                ("eps", ctypes.c_double), ("step", ctypes.c_int64), ("seed", ctypes.c_uint64),
+                ("grad_scale", ctypes.c_float), ("random_params", ctypes.c_int32),
+                ("dev_scale", ctypes.c_void_p), ("dev_lr", ctypes.c_void_p),
+                ("dev_step", ctypes.c_void_p)]
 
 
 MAX_CALLS = 8
@@ -239,10 +263,21 @@ def lib():
                                           ctypes.POINTER(mok_expert_weights), P, P, P]
         L.mok_prepare_bwd.argtypes = [cfgp, P, P, P, P, P, P, P, P]
         L.mok_mx_quantize_f32.argtypes = [I64, I64, P, P, P, P]
+        balp, parp = ctypes.POINTER(mok_balance), ctypes.POINTER(mok_param)
+        L.mok_route_logits.argtypes = [cfgp, I32, P, P, P, P, P, P, P]
+        L.mok_balance_ws_bytes.argtypes = [cfgp, I32, balp]
+        L.mok_balance_fwd.argtypes = [cfgp, I32, balp, P, P, P, P, P, P, P, P, P]
+        L.mok_balance_bwd.argtypes = [cfgp, I32, balp, P, P, P, P, P, P, P]
+        L.mok_router_bwd_ws_bytes.argtypes = [cfgp, I32]
+        L.mok_router_bwd.argtypes = [cfgp, I32, I32, P, P, P, P, P, P, I32, P, P]
+        L.mok_grad_norm_ws_bytes.argtypes = [I32, parp]
+        L.mok_grad_norm.argtypes = [I32, parp, ctypes.c_float, P, P, P]
+        L.mok_adamw.argtypes = [I32, parp, ctypes.POINTER(mok_adamw_args), P]
         L.mok_version.argtypes = []
         L.mok_version.restype = ctypes.c_char_p
-        for name in EXPORTS[1:-1]:
-            getattr(L, name).restype = ctypes.c_int
+        for name in EXPORTS[:-1]:
+            getattr(L, name).restype = (ctypes.c_size_t if name.endswith("_bytes")
+                                        else ctypes.c_int)
         _lib = L
     return _lib
 
@@ -291,9 +326,61 @@ def make_weights(w_gate, w_up, w_down, s_gate=None, s_up=None, s_down=None, wt_d
 
 
 def make_state(topk_idx, topk_gate, counts, offsets, row_src, dest_row, h, ab,
-               h_scale=None) -> mok_fwd_state:
+               h_scale=None, logits=None) -> mok_fwd_state:
     return mok_fwd_state(_ptr(topk_idx), _ptr(topk_gate), _ptr(counts), _ptr(offsets),
-                         _ptr(row_src), _ptr(dest_row), _ptr(h), _ptr(ab), _ptr(h_scale))
+                         _ptr(row_src), _ptr(dest_row), _ptr(h), _ptr(ab), _ptr(h_scale),
+                         _ptr(logits))
+
+
+def make_balance(alpha, beta=0.0, groups=0, group_offsets=None, token_mask=None) -> mok_balance:
+    """groups 0: all rows are one group.  The caller keeps the tensors alive."""
+    return mok_balance(alpha, beta, groups, _ptr(group_offsets), _ptr(token_mask))
+
+
+def _type(t) -> int:
+    """MOK_F32 or MOK_BF16 of a tensor (anything else is refused)."""
+    import torch
+    if t is None or t.dtype == torch.float32:
+        return MOK_F32
+    if t.dtype == torch.bfloat16:
+        return MOK_BF16
+    raise TypeError(f"float32 or bfloat16 expected, got {t.dtype}")
+
+
+def make_param(p=None, g=None, m=None, v=None, master=None, m_scale=None, v_scale=None,
+               weight_decay=0.0) -> mok_param:
+    """Descriptor of one tensor of mok_adamw / mok_grad_norm (which needs g
+    only).  Tensors are contiguous; 8-bit moments are told by their scales."""
+    for t in (p, g, m, v, master, m_scale, v_scale):
+        if t is not None and not t.is_contiguous():
+            raise ValueError("tensors of an optimizer step must be contiguous")
+    import torch
+    n = (g if g is not None else p).numel()
+    if any(t.numel() != n for t in (p, m, v, master) if t is not None):
+        raise ValueError("tensors of one parameter differ in size")
+    if (m_scale is None) != (v_scale is None):
+        raise ValueError("8-bit moments need both scales")
+    if any(t.numel() != (n + 31) // 32 for t in (m_scale, v_scale) if t is not None):
+        raise ValueError("one scale per 32 elements")
+    code = torch.float32 if m_scale is None else torch.uint8
+    for t, want in ((m, code), (v, code), (master, torch.float32), (m_scale, torch.uint8),
+                    (v_scale, torch.uint8)):
+        if t is not None and t.dtype != want:
+            raise TypeError(f"{want} expected, got {t.dtype}")
+    return mok_param(_ptr(p), _ptr(g), _ptr(master), _ptr(m), _ptr(v), _ptr(m_scale),
+                     _ptr(v_scale), n, _type(p), _type(g), 32 if m_scale is None else 8,
+                     weight_decay)
+
+
+def make_params(params: Sequence[mok_param]) -> ctypes.Array:
+    return (mok_param * len(params))(*params)
+
+
+def make_adamw(lr, beta1=0.9, beta2=0.999, eps=1e-8, step=1, seed=0, grad_scale=1.0,
+               random_params=False, dev_scale=None, dev_lr=None, dev_step=None) -> mok_adamw_args:
+    """dev_scale fp32, dev_lr fp64 and dev_step int64 device tensors, or None."""
+    return mok_adamw_args(lr, beta1, beta2, eps, step, seed & 0xFFFFFFFFFFFFFFFF, grad_scale,
+                          int(random_params), _ptr(dev_scale), _ptr(dev_lr), _ptr(dev_step))
 
 
 # ------------------------------------------------------------------ entry points
@@ -448,3 +535,57 @@ def mok_layer_fwd_macro(cfg, calls, w_router, bias, expert_to_local, weights: mo
     _check("mok_layer_fwd_macro", lib().mok_layer_fwd_macro(
         ctypes.byref(cfg), len(calls), arr, _ptr(w_router), _ptr(bias), _ptr(expert_to_local),
         ctypes.byref(weights), _ptr(ws), _ptr(dev_status), _stream(stream)))
+
+
+# ------------------------------------------------------------------ training
+def mok_route_logits(cfg, T, x, w_router, bias, topk_idx, topk_gate, logits, stream=None):
+    _check("mok_route_logits", lib().mok_route_logits(
+        ctypes.byref(cfg), T, _ptr(x), _ptr(w_router), _ptr(bias), _ptr(topk_idx),
+        _ptr(topk_gate), _ptr(logits), _stream(stream)))
+
+
+def mok_balance_ws_bytes(cfg, T, bal: mok_balance) -> int:
+    return int(lib().mok_balance_ws_bytes(ctypes.byref(cfg), T, ctypes.byref(bal)))
+
+
+def mok_balance_fwd(cfg, T, bal: mok_balance, logits, topk_idx, counts, prob, n_tok, loss, ws,
+                    dev_status, stream=None):
+    _check("mok_balance_fwd", lib().mok_balance_fwd(
+        ctypes.byref(cfg), T, ctypes.byref(bal), _ptr(logits), _ptr(topk_idx), _ptr(counts),
+        _ptr(prob), _ptr(n_tok), _ptr(loss), _ptr(ws), _ptr(dev_status), _stream(stream)))
+
+
+def mok_balance_bwd(cfg, T, bal: mok_balance, logits, counts, n_tok, d_loss, d_logits, dev_status,
+                    stream=None):
+    _check("mok_balance_bwd", lib().mok_balance_bwd(
+        ctypes.byref(cfg), T, ctypes.byref(bal), _ptr(logits), _ptr(counts), _ptr(n_tok),
+        _ptr(d_loss), _ptr(d_logits), _ptr(dev_status), _stream(stream)))
+
+
+def mok_router_bwd_ws_bytes(cfg, own_n) -> int:
+    return int(lib().mok_router_bwd_ws_bytes(ctypes.byref(cfg), own_n))
+
+
+def mok_router_bwd(cfg, own_lo, own_n, d_logits, src_x, w_router, d_x, dw_router, d_bias,
+                   accumulate, ws, stream=None):
+    """src_x, d_x: one entry per source (own entries used); d_x, dw_router,
+    d_bias may be None."""
+    _check("mok_router_bwd", lib().mok_router_bwd(
+        ctypes.byref(cfg), own_lo, own_n, _ptr(d_logits),
+        _table(src_x) if src_x is not None else None, _ptr(w_router),
+        _table(d_x) if d_x is not None else None, _ptr(dw_router), _ptr(d_bias), int(accumulate),
+        _ptr(ws), _stream(stream)))
+
+
+def mok_grad_norm_ws_bytes(params) -> int:
+    return int(lib().mok_grad_norm_ws_bytes(len(params), params))
+
+
+def mok_grad_norm(params, max_norm, out, ws, stream=None):
+    """out [2] fp32: the norm and the clip factor."""
+    _check("mok_grad_norm", lib().mok_grad_norm(len(params), params, max_norm, _ptr(out), _ptr(ws),
+                                                _stream(stream)))
+
+
+def mok_adamw(params, args: mok_adamw_args, stream=None):
+    _check("mok_adamw", lib().mok_adamw(len(params), params, ctypes.byref(args), _stream(stream)))

@@ -179,8 +179,9 @@ size_t mok_workspace_bytes(const mok_config* cfg) {
   return ws_layout(cfg).total;
 }
 
-mok_status mok_route(const mok_config* cfg, int32_t T, const void* x, const void* w_router,
-                     const float* bias, int32_t* topk_idx, float* topk_gate, void* stream) {
+mok_status mok_route_logits(const mok_config* cfg, int32_t T, const void* x, const void* w_router,
+                            const float* bias, int32_t* topk_idx, float* topk_gate, float* logits,
+                            void* stream) {
   if (!valid_cfg(cfg) || T < 0) return MOK_EINVAL;
   if (T > 0 && (!x || !w_router || !topk_idx || !topk_gate)) return MOK_EINVAL;
   trace_mark(cfg->trace, "start", (hipStream_t)stream);
@@ -189,7 +190,12 @@ mok_status mok_route(const mok_config* cfg, int32_t T, const void* x, const void
   src.p[0] = x;
   const int rprec = cfg->prec == MOK_F32 ? MOK_F32 : MOK_BF16;
   return launch_route(rprec, src, 0, T > 0 ? T : 1, T, cfg->d, cfg->E, cfg->k, w_router, bias,
-                      topk_idx, topk_gate, (hipStream_t)stream, cfg->trace);
+                      topk_idx, topk_gate, (hipStream_t)stream, cfg->trace, logits);
+}
+
+mok_status mok_route(const mok_config* cfg, int32_t T, const void* x, const void* w_router,
+                     const float* bias, int32_t* topk_idx, float* topk_gate, void* stream) {
+  return mok_route_logits(cfg, T, x, w_router, bias, topk_idx, topk_gate, nullptr, stream);
 }
 
 mok_status mok_layout(const mok_config* cfg, const int32_t* topk_idx_all,
@@ -307,7 +313,9 @@ mok_status route_and_layout(const mok_config* cfg, int32_t own_lo, int32_t own_n
   fill_table(&src, src_x, cfg->S);
   mok_status rc = launch_route(rprec, src, own_lo, cfg->T_src, own_n * cfg->T_src, cfg->d, cfg->E,
                                cfg->k, w_router, bias, st->topk_idx + own_lo * per_src,
-                               st->topk_gate + own_lo * per_src, sm, tr);
+                               st->topk_gate + own_lo * per_src, sm, tr,
+                               st->logits ? st->logits + (int64_t)own_lo * cfg->T_src * cfg->E
+                                          : nullptr);
   if (rc != MOK_OK) return rc;
   return launch_layout((int64_t)cfg->S * cfg->T_src * cfg->k, cfg->E, cfg->E_local, cfg->R_cap,
                        st->topk_idx, expert_to_local, st->counts, st->offsets, st->row_src,
@@ -856,6 +864,147 @@ mok_status mok_mx_quantize_f32(int64_t rows, int64_t K, const float* src, uint8_
   if (!src || !codes || !scales) return MOK_EINVAL;
   if ((uintptr_t)src % 16 != 0 || (uintptr_t)codes % 8 != 0) return MOK_EINVAL;
   return launch_mx_quantize(rows, K, src, codes, scales, (hipStream_t)stream, true);
+}
+
+}  // extern "C"
+
+// ------------------------------------------------------------------ training
+namespace {
+
+int balance_groups(const mok_balance* b) { return b->G > 0 ? b->G : 1; }
+
+bool valid_balance(const mok_config* cfg, int32_t T, const mok_balance* b) {
+  if (!valid_cfg(cfg) || T < 0 || !b || b->G < 0) return false;
+  if (b->G > 0 && !b->group_offsets) return false;
+  // counts are int32, group rows of the outputs are indexed by int32
+  if ((int64_t)T * cfg->k > 0x7FFFFFFF || (int64_t)b->G * cfg->E > 0x7FFFFFFF) return false;
+  return true;
+}
+
+bool aligned(const void* p, int n) { return (uintptr_t)p % n == 0; }
+
+bool valid_type(int t) { return t == MOK_F32 || t == MOK_BF16; }
+int type_bytes(int t) { return t == MOK_F32 ? 4 : 2; }
+
+bool valid_grads(int32_t n, const mok_param* q) {
+  if (n < 0 || (n > 0 && !q)) return false;
+  for (int i = 0; i < n; ++i) {
+    if (q[i].n < 0 || !valid_type(q[i].g_type)) return false;
+    if (q[i].n > 0 && (!q[i].g || !aligned(q[i].g, type_bytes(q[i].g_type)))) return false;
+  }
+  return true;
+}
+
+bool valid_params(int32_t n, const mok_param* q) {
+  if (!valid_grads(n, q)) return false;
+  for (int i = 0; i < n; ++i) {
+    if (!valid_type(q[i].p_type) || (q[i].state_bits != 32 && q[i].state_bits != 8)) return false;
+    if (q[i].master && q[i].p_type != MOK_BF16) return false;
+    if (q[i].n == 0) continue;
+    if (!q[i].p || !q[i].m || !q[i].v) return false;
+    if (!aligned(q[i].p, type_bytes(q[i].p_type)) || !aligned(q[i].master, 4)) return false;
+    if (q[i].state_bits == 8 && (!q[i].m_scale || !q[i].v_scale)) return false;
+    if (q[i].state_bits == 32 && (!aligned(q[i].m, 4) || !aligned(q[i].v, 4))) return false;
+  }
+  return true;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t mok_balance_ws_bytes(const mok_config* cfg, int32_t T, const mok_balance* bal) {
+  if (!valid_balance(cfg, T, bal)) return 0;
+  return balance_ws_bytes(T, cfg->E, balance_groups(bal));
+}
+
+mok_status mok_balance_fwd(const mok_config* cfg, int32_t T, const mok_balance* bal,
+                           const float* logits, const int32_t* topk_idx, int32_t* counts,
+                           float* prob, int32_t* n_tok, float* loss, void* ws,
+                           int32_t* dev_status, void* stream) {
+  if (!valid_balance(cfg, T, bal)) return MOK_EINVAL;
+  if (T > 0 && (!logits || !topk_idx)) return MOK_EINVAL;
+  if (!counts || !prob || !n_tok || !loss || !ws || !aligned(ws, 8)) return MOK_EINVAL;
+  trace_mark(cfg->trace, "start", (hipStream_t)stream);
+  return launch_balance_fwd(T, cfg->E, cfg->k, balance_groups(bal), *bal, logits, topk_idx, counts,
+                            prob, n_tok, loss, ws, dev_status, (hipStream_t)stream, cfg->trace);
+}
+
+mok_status mok_balance_bwd(const mok_config* cfg, int32_t T, const mok_balance* bal,
+                           const float* logits, const int32_t* counts, const int32_t* n_tok,
+                           const float* d_loss, float* d_logits, int32_t* dev_status,
+                           void* stream) {
+  if (!valid_balance(cfg, T, bal)) return MOK_EINVAL;
+  if (T == 0) return MOK_OK;
+  if (!logits || !counts || !n_tok || !d_logits) return MOK_EINVAL;
+  trace_mark(cfg->trace, "start", (hipStream_t)stream);
+  return launch_balance_bwd(T, cfg->E, cfg->k, balance_groups(bal), *bal, logits, counts, n_tok,
+                            d_loss, d_logits, dev_status, (hipStream_t)stream, cfg->trace);
+}
+
+size_t mok_router_bwd_ws_bytes(const mok_config* cfg, int32_t own_n) {
+  if (!valid_cfg(cfg) || own_n < 0 || own_n > cfg->S) return 0;
+  return router_bwd_ws_bytes(cfg->prec, (int64_t)own_n * cfg->T_src, cfg->d, cfg->E);
+}
+
+mok_status mok_router_bwd(const mok_config* cfg, int32_t own_lo, int32_t own_n,
+                          const float* d_logits, const void* const* src_x, const void* w_router,
+                          void* const* d_x, float* dw_router, float* d_bias, int32_t accumulate,
+                          void* ws, void* stream) {
+  if (!valid_cfg(cfg) || !own_range_ok(cfg, own_lo, own_n)) return MOK_EINVAL;
+  const int64_t T = (int64_t)own_n * cfg->T_src;
+  if (T > 0 && (!d_logits || !aligned(d_logits, 4))) return MOK_EINVAL;
+  if (!ws || !aligned(ws, 16) || !aligned(dw_router, 16) || !aligned(d_bias, 4)) return MOK_EINVAL;
+  RouterBwdPlan p;
+  memset(&p, 0, sizeof(p));
+  p.want_dx = d_x != nullptr && T > 0;
+  if (p.want_dx && (!w_router || !aligned(w_router, 16))) return MOK_EINVAL;
+  if (p.want_dx && !own_sources_set((const void* const*)d_x, own_lo, own_n, cfg->T_src))
+    return MOK_EINVAL;
+  if (dw_router && !own_sources_set(src_x, own_lo, own_n, cfg->T_src)) return MOK_EINVAL;
+  for (int s = own_lo; T > 0 && s < own_lo + own_n; ++s) {
+    if (p.want_dx) {
+      if (!aligned(d_x[s], 16)) return MOK_EINVAL;
+      p.d_x.p[s] = d_x[s];
+    }
+    if (dw_router) {
+      if (!aligned(src_x[s], 16)) return MOK_EINVAL;
+      p.x.p[s] = src_x[s];
+    }
+  }
+  p.prec = cfg->prec == MOK_F32 ? MOK_F32 : MOK_BF16;
+  p.T = (int)T, p.T_src = cfg->T_src, p.d = cfg->d, p.E = cfg->E, p.own_lo = own_lo;
+  p.dz = d_logits;
+  p.w = w_router;
+  p.dw = dw_router;
+  p.db = d_bias;
+  p.add = accumulate != 0;
+  p.ws = ws;
+  p.tr = cfg->trace;
+  trace_mark(cfg->trace, "start", (hipStream_t)stream);
+  return launch_router_bwd(p, (hipStream_t)stream);
+}
+
+size_t mok_grad_norm_ws_bytes(int32_t n_params, const mok_param* params) {
+  if (!valid_grads(n_params, params)) return 0;
+  return grad_norm_ws_bytes(n_params, params);
+}
+
+mok_status mok_grad_norm(int32_t n_params, const mok_param* params, float max_norm, float* out,
+                         void* ws, void* stream) {
+  if (!valid_grads(n_params, params) || !out || !ws || !aligned(ws, 8)) return MOK_EINVAL;
+  return launch_grad_norm(n_params, params, max_norm, out, ws, (hipStream_t)stream);
+}
+
+mok_status mok_adamw(int32_t n_params, const mok_param* params, const mok_adamw_args* args,
+                     void* stream) {
+  if (!valid_params(n_params, params) || !args) return MOK_EINVAL;
+  if (!(args->beta1 >= 0.0 && args->beta1 < 1.0) || !(args->beta2 >= 0.0 && args->beta2 < 1.0) ||
+      !(args->eps >= 0.0) || !(args->lr >= 0.0))
+    return MOK_EINVAL;
+  if (!args->dev_step && args->step < 1) return MOK_EINVAL;
+  if (args->random_params != 0 && args->random_params != 1) return MOK_EINVAL;
+  return launch_adamw(n_params, params, *args, (hipStream_t)stream);
 }
 
 }  // extern "C"

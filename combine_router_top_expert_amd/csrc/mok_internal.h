@@ -12,7 +12,8 @@ size_t route_smem_bytes(int E, int T);
 // of T_src tokens each, contiguous in the table).
 mok_status launch_route(int prec, const SrcTable& src, int src_lo, int T_src, int T, int d,
                         int E, int k, const void* w, const float* bias, int32_t* topk_idx,
-                        float* topk_gate, hipStream_t stream, mok_trace* tr = nullptr);
+                        float* topk_gate, hipStream_t stream, mok_trace* tr = nullptr,
+                        float* logits = nullptr);
 
 size_t layout_ws_bytes(int64_t N, int E_local);
 mok_status launch_layout(int64_t N, int E, int E_local, int R_cap, const int32_t* topk,
@@ -201,5 +202,43 @@ mok_status launch_prepare_bwd_bf16(int E_local, int d, int I, const void* w_gate
 bool bwd_ring_geometry(int64_t ring_bytes, int d, int I, int E_local, int mb, int R_cap,
                        int* slots, int* rows, int64_t* cols, int* n_win);
 size_t wgrad_partial_bytes(int R_cap, int d, int I);
+
+// Balance loss and its gradient (mok_balance.hip); G >= 1 groups, offsets
+// null = one group of all T rows.
+size_t balance_ws_bytes(int T, int E, int G);
+mok_status launch_balance_fwd(int T, int E, int k, int G, const mok_balance& b, const float* logits,
+                              const int32_t* topk, int32_t* counts, float* prob, int32_t* n_tok,
+                              float* loss, void* ws, int32_t* status, hipStream_t stream,
+                              mok_trace* tr);
+mok_status launch_balance_bwd(int T, int E, int k, int G, const mok_balance& b, const float* logits,
+                              const int32_t* counts, const int32_t* n_tok, const float* d_loss,
+                              float* d_logits, int32_t* status, hipStream_t stream, mok_trace* tr);
+
+// Backward of the router projection for dense logit gradients
+// (mok_router_bwd.hip).
+struct RouterBwdPlan {
+  int prec;               // MOK_F32 or MOK_BF16
+  int T, T_src, d, E;     // T = own rows
+  int own_lo;
+  SrcTable x;
+  DstTable d_x;
+  bool want_dx;
+  const float* dz;        // [T, E]
+  const void* w;          // [E, d]
+  float* dw;              // [E, d] or null
+  float* db;              // [E] or null
+  bool add;
+  void* ws;
+  mok_trace* tr;
+};
+size_t router_bwd_ws_bytes(int prec, int64_t T, int d, int E);
+mok_status launch_router_bwd(const RouterBwdPlan& p, hipStream_t stream);
+
+// Optimizer (mok_optim.hip).
+size_t grad_norm_ws_bytes(int n_params, const mok_param* params);
+mok_status launch_grad_norm(int n_params, const mok_param* params, float max_norm, float* out,
+                            void* ws, hipStream_t stream);
+mok_status launch_adamw(int n_params, const mok_param* params, const mok_adamw_args& a,
+                        hipStream_t stream);
 
 }  // namespace mok

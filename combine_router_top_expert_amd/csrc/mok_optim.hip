@@ -1,0 +1,410 @@
+// Optimizer step over many tensors: global gradient norm with the clip
+// factor, and AdamW with moments in 32 or 8 bits.
+//
+// Tensors come as descriptors in the kernel arguments (kBatch per launch; no
+// device table to keep), cut into pieces of kPiece elements; a workgroup
+// finds its tensor by a search over the pieces' prefix sums.  A lane takes 8
+// consecutive elements at a time (32 bytes of fp32, 16 of bf16, 8 of codes);
+// four lanes hold a 32-element block of an 8-bit moment, so its largest
+// magnitude is two quad exchanges away.
+#include "mok_internal.h"
+#include "mok_lanes.h"
+
+namespace mok {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kLane = 8;                       // elements per lane at a time
+constexpr int kStep = kThreads * kLane;        // elements per workgroup step
+constexpr int kPiece = 4 * kStep;              // elements per workgroup
+constexpr int kBatch = 40;                     // tensors per launch
+
+struct Desc {
+  void* p;
+  const void* g;
+  float* master;
+  void* m;
+  void* v;
+  uint8_t* ms;
+  uint8_t* vs;
+  int64_t n;
+  float wd;
+  uint32_t flags;
+  uint32_t index;   // place in the caller's array: the seed of its random words
+};
+enum : uint32_t { kPBf16 = 1, kGBf16 = 2, kEight = 4, kWide = 8 };
+
+struct Batch {
+  Desc d[kBatch];
+  uint32_t first[kBatch + 1];   // pieces before tensor i
+  int count;
+};
+
+struct AdamArgs {
+  float lr, b1, c1, b2, c2, eps;   // c = 1 - b
+  double beta1, beta2;
+  float inv_bc1, inv_sqrt_bc2;     // of the host's step
+  float grad_scale;
+  int64_t step;
+  uint64_t seed;
+  const float* dev_scale;
+  const double* dev_lr;
+  const int64_t* dev_step;
+  int random_params;
+};
+
+__device__ __forceinline__ int find_tensor(const Batch& b, uint32_t piece) {
+  int lo = 0, hi = b.count - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (b.first[mid] <= piece) lo = mid;
+    else hi = mid - 1;
+  }
+  return lo;
+}
+
+// 8 elements from element i of an fp32 or bf16 tensor; elements past n are 0.
+__device__ __forceinline__ void load8_f32(const float* p, int64_t i, int64_t n, bool wide, float (&v)[8]) {
+  if (wide && i + 8 <= n) {
+    const float4 a = *reinterpret_cast<const float4*>(p + i), b = *reinterpret_cast<const float4*>(p + i + 4);
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = i + j < n ? p[i + j] : 0.0f;
+  }
+}
+__device__ __forceinline__ void load8_bf16(const bf16_t* p, int64_t i, int64_t n, bool wide, float (&v)[8]) {
+  if (wide && i + 8 <= n) {
+    const uint4 u = ld16(p + i);
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      v[2 * j] = __uint_as_float(w[j] << 16);
+      v[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = i + j < n ? bf16_to_f32(p[i + j]) : 0.0f;
+  }
+}
+__device__ __forceinline__ void store8_f32(float* p, int64_t i, int64_t n, bool wide, const float (&v)[8]) {
+  if (wide && i + 8 <= n) {
+    *reinterpret_cast<float4*>(p + i) = make_float4(v[0], v[1], v[2], v[3]);
+    *reinterpret_cast<float4*>(p + i + 4) = make_float4(v[4], v[5], v[6], v[7]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (i + j < n) p[i + j] = v[j];
+  }
+}
+__device__ __forceinline__ void store8_u16(bf16_t* p, int64_t i, int64_t n, bool wide, const uint32_t (&w)[4]) {
+  if (wide && i + 8 <= n) {
+    st16(p + i, make_uint4(w[0], w[1], w[2], w[3]));
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (i + j < n) p[i + j] = (bf16_t)(w[j >> 1] >> (16 * (j & 1)));
+  }
+}
+__device__ __forceinline__ void load8_u8(const uint8_t* p, int64_t i, int64_t n, bool wide, uint32_t (&w)[2]) {
+  if (wide && i + 8 <= n) {
+    const uint2 u = *reinterpret_cast<const uint2*>(p + i);
+    w[0] = u.x, w[1] = u.y;
+  } else {
+    w[0] = w[1] = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (i + j < n) w[j >> 2] |= (uint32_t)p[i + j] << (8 * (j & 3));
+  }
+}
+__device__ __forceinline__ void store8_u8(uint8_t* p, int64_t i, int64_t n, bool wide, const uint32_t (&w)[2]) {
+  if (wide && i + 8 <= n) {
+    *reinterpret_cast<uint2*>(p + i) = make_uint2(w[0], w[1]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (i + j < n) p[i + j] = (uint8_t)(w[j >> 2] >> (8 * (j & 3)));
+  }
+}
+
+// ------------------------------------------------------------------ norm
+// Squares summed in 64 bits (fp32 squares would overflow from 1.8e19 on and
+// vanish below 1e-23): per lane, wave and workgroup in a fixed order, one
+// partial sum per piece.
+__global__ __launch_bounds__(kThreads) void norm_kernel(Batch b, double* part) {
+  __shared__ double s_w[kThreads / 64];
+  const int ti = find_tensor(b, blockIdx.x);
+  const Desc& d = b.d[ti];
+  const int64_t base = (int64_t)(blockIdx.x - b.first[ti]) * kPiece;
+  const bool wide = d.flags & kWide;
+  double s = 0.0;
+  for (int it = 0; it < kPiece / kStep; ++it) {
+    const int64_t i = base + (int64_t)it * kStep + threadIdx.x * kLane;
+    if (i >= d.n) break;
+    float g[8];
+    if (d.flags & kGBf16) load8_bf16((const bf16_t*)d.g, i, d.n, wide, g);
+    else load8_f32((const float*)d.g, i, d.n, wide, g);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) s = __builtin_fma((double)g[j], (double)g[j], s);
+  }
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) s += __shfl_xor(s, o, 64);
+  if ((threadIdx.x & 63) == 0) s_w[threadIdx.x >> 6] = s;
+  __syncthreads();
+  if (threadIdx.x == 0) part[blockIdx.x] = (s_w[0] + s_w[1]) + (s_w[2] + s_w[3]);
+}
+
+__global__ __launch_bounds__(1024) void norm_total_kernel(const double* part, int64_t n, float max_norm, float* out) {
+  __shared__ double s_w[16];
+  double s = 0.0;
+  for (int64_t i = threadIdx.x; i < n; i += 1024) s += part[i];
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) s += __shfl_xor(s, o, 64);
+  if ((threadIdx.x & 63) == 0) s_w[threadIdx.x >> 6] = s;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    s = 0.0;
+    for (int i = 0; i < 16; ++i) s += s_w[i];
+    const double norm = sqrt(s);
+    const float f = (float)norm;
+    out[0] = f;
+    const double c = max_norm > 0.0f ? max_norm / (norm + 1e-6) : 1.0;
+    out[1] = __builtin_isfinite(f) ? (float)(c < 1.0 ? c : 1.0) : __builtin_nanf("");
+  }
+}
+
+// ------------------------------------------------------------------ AdamW
+// The 64-bit finaliser of SplitMix64 (Steele, Lea and Flood, OOPSLA 2014).
+constexpr uint64_t kGold = 0x9E3779B97F4A7C15ull;
+__device__ __forceinline__ uint64_t mix64(uint64_t z) {
+  z = (z ^ (z >> 30)) * 0xBF58476D1CE4E5B9ull;
+  z = (z ^ (z >> 27)) * 0x94D049BB133111EBull;
+  return z ^ (z >> 31);
+}
+
+// Smallest s with amax <= 448 2^s (448 = 1.75 2^8), from the bits: adding
+// what is missing from 1.75 to 2 in the mantissa carries into the exponent
+// exactly where the mantissa is above 1.75.  Clamped to E8M0's range.
+__device__ __forceinline__ int block_scale(float amax) {
+  const int s = (int)((__float_as_uint(amax) + 0x1FFFFFu) >> 23) - 127 - 8;
+  return s < -127 ? -127 : (s > 127 ? 127 : s);
+}
+
+// E4M3 code of |x| 2^-s rounded up or down by 16 random bits (bits 4..19 of
+// rnd).  |x| 2^(-s-120) has the code's exponent field (bias 127 - 120 = 7),
+// so its bits from 20 on are the code, subnormals included; adding below bit
+// 20 and cutting off rounds at random.  Not finite: the NaN code.
+__device__ __forceinline__ uint32_t e4m3_random(float x, int s, uint32_t rnd) {
+  const float y = __builtin_amdgcn_ldexpf(__builtin_fabsf(x), -s - 120);
+  const uint32_t c = (__float_as_uint(y) + rnd) >> 20;
+  return __builtin_isfinite(x) ? (c < 0x7Eu ? c : 0x7Eu) : 0x7Fu;
+}
+
+__device__ __forceinline__ float quad_max(float x) { return group_reduce<4, OpMax>(x); }
+
+template <bool EIGHT>
+__device__ __forceinline__ void adam_step(const Desc& d, const AdamArgs& a, int64_t i, float scale, float lr,
+                                          float inv_bc1, float inv_sbc2, uint64_t key) {
+  const bool wide = d.flags & kWide, pb = d.flags & kPBf16;
+  float g[8], p[8], m[8], v[8];
+  const int64_t n = d.n;
+  if (d.flags & kGBf16) load8_bf16((const bf16_t*)d.g, i, n, wide, g);
+  else load8_f32((const float*)d.g, i, n, wide, g);
+  if (d.master) load8_f32(d.master, i, n, wide, p);
+  else if (pb) load8_bf16((const bf16_t*)d.p, i, n, wide, p);
+  else load8_f32((const float*)d.p, i, n, wide, p);
+  if constexpr (EIGHT) {
+    uint32_t mc[2], vc[2];
+    load8_u8((const uint8_t*)d.m, i, n, wide, mc);
+    load8_u8((const uint8_t*)d.v, i, n, wide, vc);
+    const bool there = i < n;
+    const int sm = there ? (int)d.ms[i >> 5] - 127 : 0, sv = there ? (int)d.vs[i >> 5] - 127 : 0;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const auto m0 = __builtin_amdgcn_cvt_pk_f32_fp8((int)mc[h], false), m1 = __builtin_amdgcn_cvt_pk_f32_fp8((int)mc[h], true);
+      const auto v0 = __builtin_amdgcn_cvt_pk_f32_fp8((int)vc[h], false), v1 = __builtin_amdgcn_cvt_pk_f32_fp8((int)vc[h], true);
+      m[4 * h] = m0[0], m[4 * h + 1] = m0[1], m[4 * h + 2] = m1[0], m[4 * h + 3] = m1[1];
+      v[4 * h] = v0[0], v[4 * h + 1] = v0[1], v[4 * h + 2] = v1[0], v[4 * h + 3] = v1[1];
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      m[j] = __builtin_amdgcn_ldexpf(m[j], sm);
+      v[j] = __builtin_amdgcn_ldexpf(v[j], sv);
+      v[j] *= v[j];
+    }
+  } else {
+    load8_f32((const float*)d.m, i, n, wide, m);
+    load8_f32((const float*)d.v, i, n, wide, v);
+  }
+  const float decay = 1.0f - lr * d.wd, rate = lr * inv_bc1;
+  float r[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const float gj = g[j] * scale;
+    m[j] = __builtin_fmaf(a.b1, m[j], a.c1 * gj);
+    v[j] = __builtin_fmaf(a.b2, v[j], a.c2 * (gj * gj));
+    r[j] = sqrtf(v[j]);
+    p[j] = __builtin_fmaf(-rate, m[j] / __builtin_fmaf(r[j], inv_sbc2, a.eps), p[j] * decay);
+  }
+  uint32_t w0 = 0, w1 = 0;
+  if (EIGHT || a.random_params) {
+    const uint64_t z = mix64(key + ((uint64_t)(i >> 3) + 1) * kGold);
+    w0 = (uint32_t)z, w1 = (uint32_t)(z >> 32);
+  }
+  if constexpr (EIGHT) {
+    // finite magnitudes only: one bad element must not take its block along
+    float am = 0.0f, ar = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      am = __builtin_fmaxf(am, __builtin_isfinite(m[j]) ? __builtin_fabsf(m[j]) : 0.0f);
+      ar = __builtin_fmaxf(ar, __builtin_isfinite(r[j]) ? r[j] : 0.0f);
+    }
+    const int sm = block_scale(quad_max(am)), sr = block_scale(quad_max(ar));
+    uint32_t mc[2] = {0, 0}, vc[2] = {0, 0};
+    uint32_t w = w0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j, w += w1) {
+      const uint32_t cm = e4m3_random(m[j], sm, (w & 0xFFFFu) << 4) | ((__float_as_uint(m[j]) >> 24) & 0x80u);
+      uint32_t cv = e4m3_random(r[j], sr, (w >> 16) << 4);
+      if (cv == 0 && r[j] > 0.0f) cv = 1;   // a divisor of zero would throw the next step
+      if (cv == 0x7Fu) cv = 0x7Eu;
+      mc[j >> 2] |= cm << (8 * (j & 3));
+      vc[j >> 2] |= cv << (8 * (j & 3));
+    }
+    store8_u8((uint8_t*)d.m, i, n, wide, mc);
+    store8_u8((uint8_t*)d.v, i, n, wide, vc);
+    if ((threadIdx.x & 3) == 0 && i < n) {
+      d.ms[i >> 5] = (uint8_t)(sm + 127);
+      d.vs[i >> 5] = (uint8_t)(sr + 127);
+    }
+  } else {
+    store8_f32((float*)d.m, i, n, wide, m);
+    store8_f32((float*)d.v, i, n, wide, v);
+  }
+  if (d.master) store8_f32(d.master, i, n, wide, p);
+  if (pb) {
+    uint32_t o[4];
+    if (a.random_params && !d.master) {
+      uint32_t w = w1, b[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j, w += w0) b[j] = __float_as_uint(p[j]) + (__builtin_isfinite(p[j]) ? w >> 16 : 0u);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) o[j] = (b[2 * j] >> 16) | (b[2 * j + 1] & 0xFFFF0000u);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) o[j] = pack2_bf16(p[2 * j], p[2 * j + 1]);
+    }
+    store8_u16((bf16_t*)d.p, i, n, wide, o);
+  } else {
+    store8_f32((float*)d.p, i, n, wide, p);
+  }
+}
+
+__global__ __launch_bounds__(kThreads) void adamw_kernel(Batch b, AdamArgs a) {
+  float scale = a.grad_scale;
+  if (a.dev_scale) {
+    const float s = *a.dev_scale;
+    if (__builtin_isnan(s)) return;   // the whole step is left out
+    scale *= s;
+  }
+  float lr = a.lr, inv_bc1 = a.inv_bc1, inv_sbc2 = a.inv_sqrt_bc2;
+  int64_t step = a.step;
+  if (a.dev_lr) lr = (float)*a.dev_lr;
+  if (a.dev_step) {
+    step = *a.dev_step;
+    inv_bc1 = (float)(1.0 / (1.0 - pow(a.beta1, (double)step)));
+    inv_sbc2 = (float)(1.0 / sqrt(1.0 - pow(a.beta2, (double)step)));
+  }
+  const int ti = find_tensor(b, blockIdx.x);
+  const Desc& d = b.d[ti];
+  const int64_t base = (int64_t)(blockIdx.x - b.first[ti]) * kPiece;
+  const uint64_t key = mix64(mix64(a.seed + d.index) + (uint64_t)step * kGold);
+  for (int it = 0; it < kPiece / kStep; ++it) {
+    const int64_t at = base + (int64_t)it * kStep;
+    if (at >= d.n) break;
+    const int64_t i = at + threadIdx.x * kLane;
+    if (d.flags & kEight) adam_step<true>(d, a, i, scale, lr, inv_bc1, inv_sbc2, key);
+    else adam_step<false>(d, a, i, scale, lr, inv_bc1, inv_sbc2, key);
+  }
+}
+
+int64_t pieces_of(int64_t n) { return (n + kPiece - 1) / kPiece; }
+
+// Calls f(batch, pieces) for batches of at most kBatch non-empty tensors and
+// at most 2^30 pieces each; a tensor never splits over batches.
+template <class F>
+bool each_batch(int n_params, const mok_param* params, F f) {
+  Batch b = {};
+  uint64_t pieces = 0;
+  for (int t = 0; t < n_params; ++t) {
+    const mok_param& q = params[t];
+    if (q.n == 0) continue;
+    const uint64_t k = (uint64_t)pieces_of(q.n);
+    if (b.count == kBatch || (b.count && pieces + k > (1u << 30))) {
+      if (!f(b, (uint32_t)pieces)) return false;
+      b.count = 0;
+      pieces = 0;
+    }
+    Desc& d = b.d[b.count];
+    d.p = q.p, d.g = q.g, d.master = q.master, d.m = q.m, d.v = q.v, d.ms = q.m_scale, d.vs = q.v_scale;
+    d.n = q.n;
+    d.wd = q.weight_decay;
+    d.index = (uint32_t)t;
+    const uintptr_t all = (uintptr_t)q.p | (uintptr_t)q.g | (uintptr_t)q.master | (uintptr_t)q.m | (uintptr_t)q.v;
+    d.flags = (q.p_type == MOK_BF16 ? kPBf16 : 0) | (q.g_type == MOK_BF16 ? kGBf16 : 0) |
+              (q.state_bits == 8 ? kEight : 0) | (all % 16 == 0 ? kWide : 0);
+    b.first[b.count] = (uint32_t)pieces;
+    pieces += k;
+    b.first[++b.count] = (uint32_t)pieces;
+  }
+  return b.count == 0 || f(b, (uint32_t)pieces);
+}
+
+}  // namespace
+
+size_t grad_norm_ws_bytes(int n_params, const mok_param* params) {
+  uint64_t pieces = 0;
+  for (int t = 0; t < n_params; ++t) pieces += (uint64_t)pieces_of(params[t].n);
+  return (size_t)(pieces + 1) * sizeof(double);
+}
+
+mok_status launch_grad_norm(int n_params, const mok_param* params, float max_norm, float* out, void* ws,
+                            hipStream_t stream) {
+  double* part = (double*)ws;
+  int64_t done = 0;
+  // only the gradients are read: their alignment alone decides the width
+  auto run = [&](Batch& b, uint32_t pieces) {
+    for (int i = 0; i < b.count; ++i)
+      b.d[i].flags = (b.d[i].flags & ~(uint32_t)kWide) | ((uintptr_t)b.d[i].g % 16 == 0 ? kWide : 0);
+    hipLaunchKernelGGL(norm_kernel, dim3(pieces), dim3(kThreads), 0, stream, b, part + done);
+    done += pieces;
+    return hipGetLastError() == hipSuccess;
+  };
+  if (!each_batch(n_params, params, run)) return MOK_EDEVICE;
+  hipLaunchKernelGGL(norm_total_kernel, dim3(1), dim3(1024), 0, stream, part, done, max_norm, out);
+  return hipGetLastError() == hipSuccess ? MOK_OK : MOK_EDEVICE;
+}
+
+mok_status launch_adamw(int n_params, const mok_param* params, const mok_adamw_args& h, hipStream_t stream) {
+  AdamArgs a = {};
+  a.lr = (float)h.lr;
+  a.b1 = (float)h.beta1, a.c1 = (float)(1.0 - h.beta1);
+  a.b2 = (float)h.beta2, a.c2 = (float)(1.0 - h.beta2);
+  a.eps = (float)h.eps;
+  a.beta1 = h.beta1, a.beta2 = h.beta2;
+  a.inv_bc1 = (float)(1.0 / (1.0 - pow(h.beta1, (double)h.step)));
+  a.inv_sqrt_bc2 = (float)(1.0 / sqrt(1.0 - pow(h.beta2, (double)h.step)));
+  a.grad_scale = h.grad_scale;
+  a.step = h.step;
+  a.seed = h.seed;
+  a.dev_scale = h.dev_scale, a.dev_lr = h.dev_lr, a.dev_step = h.dev_step;
+  a.random_params = h.random_params;
+  auto run = [&](Batch& b, uint32_t pieces) {
+    hipLaunchKernelGGL(adamw_kernel, dim3(pieces), dim3(kThreads), 0, stream, b, a);
+    return hipGetLastError() == hipSuccess;
+  };
+  return each_batch(n_params, params, run) ? MOK_OK : MOK_EDEVICE;
+}
+
+}  // namespace mok

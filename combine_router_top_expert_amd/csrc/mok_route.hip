@@ -26,6 +26,7 @@ struct RouteArgs {
   const float* bias;
   int32_t* topk_idx;  // [T, k] for the launch's tokens, in order
   float* topk_gate;
+  float* logits;      // [T, E] in the same order, or null
   int T, d, E, k;
   int EL;           // expert lanes per wave (each lane: 4 experts)
   int ESETS;        // sets of 4 * EL experts
@@ -289,6 +290,11 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteArgs a) {
     }
   }
   __syncthreads();
+  if (a.logits) {  // a block's rows are one contiguous piece of [T, E]
+    const int n = min(TB, a.T - t0) * a.E;
+    float* out = a.logits + (size_t)t0 * a.E;
+    for (int i = tid; i < n; i += kRouteThreads) out[i] = zs[(i / a.E) * zp + i % a.E];
+  }
 
   // selection: LP lanes per token (the power of two covering E, at most 64)
   const int LPS = a.E >= 64 ? 6 : (a.E <= 1 ? 0 : 32 - __builtin_clz(a.E - 1));  // log2 LP
@@ -336,9 +342,10 @@ size_t route_smem_bytes(int E, int T) {
 
 mok_status launch_route(int prec, const SrcTable& src, int src_lo, int T_src, int T, int d,
                         int E, int k, const void* w, const float* bias, int32_t* topk_idx,
-                        float* topk_gate, hipStream_t stream, mok_trace* tr) {
+                        float* topk_gate, hipStream_t stream, mok_trace* tr, float* logits) {
   if (T == 0) return MOK_OK;
   RouteArgs a;
+  a.logits = logits;
   a.src = src;
   a.src_lo = src_lo;
   a.T_src = T_src;

@@ -2,8 +2,9 @@
 
 ``MoELayer`` owns the caller-side memory the C ABI expects (configuration,
 weights, forward state, staging rows, outputs, gradients, workspace, device
-status word) and calls ``mok_layer_fwd`` / ``mok_layer_bwd``.  It does no
-arithmetic of its own.
+status word) and calls ``mok_layer_fwd`` / ``mok_layer_bwd``, and for training the
+balance loss (``mok_balance_fwd`` / ``mok_balance_bwd``) with the router
+projection's backward (``mok_router_bwd``).  It does no arithmetic of its own.
 """
 from __future__ import annotations
 
@@ -12,8 +13,10 @@ from typing import List, Optional
 import numpy as np
 import torch
 
-from . import (MAX_SOURCES, AuxStream, make_config, make_state, make_weights, mok_layer_bwd, mok_layer_fwd,
-               mok_prepare_bwd, mok_mx_quantize, mok_tune_fwd, mok_workspace_bytes, STATUS)
+from . import (MAX_SOURCES, AuxStream, make_balance, make_config, make_state, make_weights,
+               mok_balance_bwd, mok_balance_fwd, mok_balance_ws_bytes, mok_layer_bwd, mok_layer_fwd,
+               mok_prepare_bwd, mok_mx_quantize, mok_router_bwd, mok_router_bwd_ws_bytes,
+               mok_tune_fwd, mok_workspace_bytes, STATUS)
 
 
 def _dt(prec: str):
@@ -30,7 +33,8 @@ def to_device(a: np.ndarray, prec: str, device) -> torch.Tensor:
 class MoELayer:
     def __init__(self, S, T_src, d, E, k, I, E_local, prec, R_cap, own_lo, own_n, device="cuda",
                  ring_bytes=0, minibatch_rows=256, comm_wgs=0, gemm_wgs=0, with_bwd=True,
-                 wait_limit_us=0, two_streams=True, bwd_ring_bytes=0, transposed_weights=True):
+                 wait_limit_us=0, two_streams=True, bwd_ring_bytes=0, transposed_weights=True,
+                 keep_logits=False):
         assert S <= MAX_SOURCES
         self.S, self.T_src, self.d, self.E, self.k, self.I = S, T_src, d, E, k, I
         self.E_local, self.prec, self.R_cap = E_local, prec, R_cap
@@ -67,8 +71,12 @@ class MoELayer:
         # MXFP8: h holds E4M3 codes; its scales are kept for the backward
         self.h_scale = (torch.zeros(max(R_cap, 1) * I // 32, dtype=torch.uint8, device=dev)
                         if prec == "mxfp8" and with_bwd else None)
+        # the router's logits, for the balance loss (balance_loss)
+        self.logits = (torch.zeros(max(S * T_src, 1), E, dtype=torch.float32, device=dev)
+                       if keep_logits else None)
         self.state = make_state(self.topk_idx, self.topk_gate, self.counts, self.offsets,
-                                self.row_src, self.dest_row, self.h, self.ab, self.h_scale)
+                                self.row_src, self.dest_row, self.h, self.ab, self.h_scale,
+                                self.logits)
         self.with_bwd = with_bwd
         # bf16 backward: the weights also transposed (mok_prepare_bwd), so dh
         # and dx read them k-contiguous (bit-identical either way)
@@ -106,7 +114,7 @@ class MoELayer:
             E, d, I = self.E_local, self.d, self.I
             self.wt = [torch.empty(E * I * d, dtype=torch.bfloat16, device=self.device),
                        torch.empty(E * d * 2 * I, dtype=torch.bfloat16, device=self.device)]
-            mok_prepare_bwd(self.cfg, w_gate, w_up, w_down, self.wt[0], None, self.wt[1], None)
+            self.update_weights()
             self.weights = make_weights(w_gate, w_up, w_down, wt_down=self.wt[0],
                                         wt_gu=self.wt[1])
         else:
@@ -125,17 +133,26 @@ class MoELayer:
             if dx is not None:
                 self.dx_stage[s].copy_(dx)
 
+    def update_weights(self, stream=None):
+        """After the expert weights were written in place (an optimizer step):
+        forms what the layer keeps beside them again -- the backward's
+        transposed copies, the MX codes -- in the same buffers.  A layer in
+        fp32, or in bf16 without transposed weights, keeps nothing."""
+        w = (self.w_gate, self.w_up, self.w_down)
+        if self.prec == "mxfp8":
+            for t, (codes, scales) in zip(w, self.wq):
+                mok_mx_quantize(t.numel() // t.shape[-1], t.shape[-1], t, codes, scales, stream)
+            if self.with_bwd:
+                mok_prepare_bwd(self.cfg, *w, *self.wt, stream)
+        elif self.prec == "bf16" and self.with_bwd and self.transposed_weights:
+            mok_prepare_bwd(self.cfg, *w, self.wt[0], None, self.wt[1], None, stream)
+
     def _quantize_weights(self):
-        """MX-quantise the expert weights once (off the timed path)."""
-        q = []
-        for w in (self.w_gate, self.w_up, self.w_down):
-            rows = w.numel() // w.shape[-1]
-            K = w.shape[-1]
-            codes = torch.empty(w.numel(), dtype=torch.uint8, device=self.device)
-            scales = torch.empty(w.numel() // 32, dtype=torch.uint8, device=self.device)
-            mok_mx_quantize(rows, K, w, codes, scales)
-            q.append((codes, scales))
-        self.wq = q
+        """MX-quantise the expert weights (off the timed path)."""
+        self.wq = [(torch.empty(w.numel(), dtype=torch.uint8, device=self.device),
+                    torch.empty(w.numel() // 32, dtype=torch.uint8, device=self.device))
+                   for w in (self.w_gate, self.w_up, self.w_down)]
+        q = self.wq
         t = [None] * 4
         if self.with_bwd:
             # the backward's transposed operands: W_down^T and [W_gate; W_up]^T
@@ -144,8 +161,8 @@ class MoELayer:
                  torch.empty(E * I * d // 32, dtype=torch.uint8, device=self.device),
                  torch.empty(E * d * 2 * I, dtype=torch.uint8, device=self.device),
                  torch.empty(E * d * 2 * I // 32, dtype=torch.uint8, device=self.device)]
-            mok_prepare_bwd(self.cfg, self.w_gate, self.w_up, self.w_down, *t)
         self.wt = t
+        self.update_weights()
         self.weights = make_weights(q[0][0], q[1][0], q[2][0], q[0][1], q[1][1], q[2][1], *t)
 
     # ---------------------------------------------------------------- passes
@@ -181,6 +198,52 @@ class MoELayer:
                       self.weights, self.state, self.staging, self.d_gate, self.dx_stage, self.d_x,
                       self.dw_gate, self.dw_up, self.dw_down,
                       self.dw_router if router_grad else None, self.ws, self.status, stream)
+
+    def balance_loss(self, alpha, beta=0.0, group_offsets=None, token_mask=None, stream=None):
+        """Balance loss and z-loss of the last forward's own tokens (fp32 [2]
+        on the device; needs keep_logits).  group_offsets: int32 [G+1] over
+        the own rows (sequences), None = one group; token_mask: uint8 [own
+        rows] or None.  Leaves counts_all [G, E], prob [G, E] and n_tok
+        [G+2]."""
+        if self.logits is None:
+            raise RuntimeError("balance_loss needs MoELayer(keep_logits=True)")
+        T, dev = self.own_n * self.T_src, self.device
+        G = 0 if group_offsets is None else group_offsets.numel() - 1
+        for t, dt, n in ((group_offsets, torch.int32, None), (token_mask, torch.uint8, T)):
+            if t is not None and (t.dtype != dt or not t.is_contiguous() or t.device.type != dev.type
+                                  or (n is not None and t.numel() != n) or t.numel() < 1):
+                raise ValueError(f"contiguous {dt} tensor on {dev} expected, got {t.dtype} {tuple(t.shape)}")
+        if group_offsets is not None and G < 1:
+            raise ValueError("group_offsets needs at least two entries")
+        self._bal = make_balance(alpha, beta, G, group_offsets, token_mask)
+        self._bal_keep = (group_offsets, token_mask)
+        rows = max(G, 1)
+        if getattr(self, "n_tok", None) is None or self.n_tok.numel() != rows + 2:
+            self.counts_all = torch.zeros(rows, self.E, dtype=torch.int32, device=dev)
+            self.prob = torch.zeros(rows, self.E, dtype=torch.float32, device=dev)
+            self.n_tok = torch.zeros(rows + 2, dtype=torch.int32, device=dev)
+            self.loss = torch.zeros(2, dtype=torch.float32, device=dev)
+            self.ws_bal = torch.zeros(mok_balance_ws_bytes(self.cfg, T, self._bal),
+                                      dtype=torch.uint8, device=dev)
+        lo = self.own_lo * self.T_src
+        mok_balance_fwd(self.cfg, T, self._bal, self.logits[lo:], self.topk_idx[lo * self.k:],
+                        self.counts_all, self.prob, self.n_tok, self.loss, self.ws_bal,
+                        self.status, stream)
+        return self.loss
+
+    def balance_backward(self, d_loss=None, stream=None):
+        """Adds the gradient of d_loss[0] * balance loss + d_loss[1] * z-loss
+        (d_loss fp32 [2] on the device, None = ones) to d_x and dw_router,
+        after backward()."""
+        T, lo = self.own_n * self.T_src, self.own_lo * self.T_src
+        if getattr(self, "d_logits", None) is None:
+            self.d_logits = torch.zeros(max(T, 1), self.E, dtype=torch.float32, device=self.device)
+            self.ws_router = torch.zeros(mok_router_bwd_ws_bytes(self.cfg, self.own_n),
+                                         dtype=torch.uint8, device=self.device)
+        mok_balance_bwd(self.cfg, T, self._bal, self.logits[lo:], self.counts_all, self.n_tok,
+                        d_loss, self.d_logits, self.status, stream)
+        mok_router_bwd(self.cfg, self.own_lo, self.own_n, self.d_logits, self.xs, self.w_router,
+                       self.d_x, self.dw_router, None, True, self.ws_router, stream)
 
     def check_status(self):
         st = int(self.status.item())

@@ -1,0 +1,114 @@
+"""AdamW over the tensors of a model, through ``mok_grad_norm`` and ``mok_adamw``.
+
+``AdamW`` owns what the C ABI expects from its caller: the moments (fp32, or
+MX blocks of E4M3 codes with E8M0 scales), fp32 copies behind bf16 parameters,
+the descriptors, the workspace.  It does no arithmetic of its own: one step is
+the norm's launches (with ``max_norm``) and the update's.
+"""
+from __future__ import annotations
+
+from typing import Optional, Sequence, Union
+
+import torch
+
+from . import (make_adamw, make_param, make_params, mok_adamw, mok_grad_norm,
+               mok_grad_norm_ws_bytes)
+
+
+class AdamW:
+    """params: contiguous fp32 or bf16 tensors of one device, updated in place.
+
+    weight_decay, state_bits: one value, or one per tensor.  state_bits 32 or 8
+    (moments of a tensor in fp32, or in 8 bits).  master: keep fp32 copies of
+    bf16 parameters; without them a bf16 parameter is rounded to nearest, or at
+    random with random_params.  max_norm: clip the global gradient norm; a step
+    whose norm is not finite is left out.  capturable: the step number (and the
+    learning rate, see set_lr) live on the device, so a step captured in a
+    graph advances at every replay; the number counts left-out steps too.
+    """
+
+    def __init__(self, params: Sequence[torch.Tensor], lr: float = 1e-3, betas=(0.9, 0.999),
+                 eps: float = 1e-8, weight_decay: Union[float, Sequence[float]] = 0.01,
+                 state_bits: Union[int, Sequence[int]] = 32, master: bool = True,
+                 random_params: bool = False, max_norm: Optional[float] = None, seed: int = 0,
+                 capturable: bool = False):
+        self.params = list(params)
+        if not self.params:
+            raise ValueError("no parameters")
+        dev = self.params[0].device
+        per = lambda v: list(v) if isinstance(v, (list, tuple)) else [v] * len(self.params)  # noqa: E731
+        self.weight_decay, self.state_bits = per(weight_decay), per(state_bits)
+        if len(self.weight_decay) != len(self.params) or len(self.state_bits) != len(self.params):
+            raise ValueError("one weight_decay and state_bits per parameter")
+        for p, bits in zip(self.params, self.state_bits):
+            if p.device != dev or not p.is_contiguous():
+                raise ValueError("parameters must be contiguous and on one device")
+            if p.dtype not in (torch.float32, torch.bfloat16):
+                raise TypeError(f"float32 or bfloat16 expected, got {p.dtype}")
+            if bits not in (8, 32):
+                raise ValueError(f"state_bits 8 or 32 expected, got {bits}")
+        self.device, self.max_norm = dev, max_norm
+        self.step_count = 0
+        self.master = [p.float() if master and p.dtype == torch.bfloat16 else None
+                       for p in self.params]
+        z = lambda n, t: torch.zeros(n, dtype=t, device=dev)  # noqa: E731
+        self.m, self.v, self.m_scale, self.v_scale = [], [], [], []
+        for p, bits in zip(self.params, self.state_bits):
+            n, t = p.numel(), torch.float32 if bits == 32 else torch.uint8
+            self.m.append(z(n, t))
+            self.v.append(z(n, t))
+            self.m_scale.append(None if bits == 32 else z((n + 31) // 32, torch.uint8))
+            self.v_scale.append(None if bits == 32 else z((n + 31) // 32, torch.uint8))
+        self.norm = z(2, torch.float32)      # norm and clip factor of the last step
+        self.dev_step = z(1, torch.int64) if capturable else None
+        self.dev_lr = torch.full((1,), lr, dtype=torch.float64, device=dev) if capturable else None
+        self.args = make_adamw(lr, betas[0], betas[1], eps, seed=seed, random_params=random_params,
+                               dev_scale=self.norm[1:] if max_norm is not None else None,
+                               dev_lr=self.dev_lr, dev_step=self.dev_step)
+        self._grads = None
+
+    def set_lr(self, lr: float):
+        self.args.lr = lr
+        if self.dev_lr is not None:
+            self.dev_lr.fill_(lr)
+
+    def bind(self, grads: Sequence[torch.Tensor]):
+        """Descriptors for these gradient tensors (kept: step() without
+        arguments reads them again)."""
+        grads = list(grads)
+        if len(grads) != len(self.params):
+            raise ValueError("one gradient per parameter")
+        for p, g in zip(self.params, grads):
+            if g.device != self.device:
+                raise ValueError(f"gradient on {g.device}, parameters on {self.device}")
+        flat = lambda t: None if t is None else t.view(-1)  # noqa: E731
+        self._desc = make_params([
+            make_param(p=flat(p), g=flat(g), m=m, v=v, master=flat(w), m_scale=ms, v_scale=vs,
+                       weight_decay=wd)
+            for p, g, m, v, w, ms, vs, wd in zip(self.params, grads, self.m, self.v, self.master,
+                                                 self.m_scale, self.v_scale, self.weight_decay)])
+        self._grads = grads
+        if self.max_norm is not None:
+            self._ws = torch.zeros(mok_grad_norm_ws_bytes(self._desc), dtype=torch.uint8,
+                                   device=self.device)
+
+    def step(self, grads: Optional[Sequence[torch.Tensor]] = None, grad_scale: float = 1.0,
+             stream=None):
+        """One step on `stream` (None: the device's current stream).  grads:
+        gradients to bind, or None for those bound before.  Gradients are
+        multiplied by grad_scale (the norm is taken before)."""
+        if grads is not None:
+            self.bind(grads)
+        if self._grads is None:
+            raise RuntimeError("step() before any gradients were bound")
+        with torch.cuda.device(self.device):
+            s = torch.cuda.current_stream() if stream is None else stream
+            if self.max_norm is not None:
+                mok_grad_norm(self._desc, self.max_norm / grad_scale, self.norm, self._ws, s)
+            self.step_count += 1
+            self.args.step = self.step_count
+            self.args.grad_scale = grad_scale
+            if self.dev_step is not None:
+                with torch.cuda.stream(s):
+                    self.dev_step.add_(1)
+            mok_adamw(self._desc, self.args, s)

@@ -78,7 +78,8 @@ typedef enum {
   MOK_ECAPACITY = -4,  /* device-latched: routed rows exceed R_cap */
   MOK_ETIMEOUT = -5,   /* device-latched: a bounded wait in the fused kernel ran out */
   MOK_EROUTE = -6,     /* device-latched: an expert id outside [0, E) in routing input */
-  MOK_ESCRATCH = -7    /* mok_layer_fwd_noalloc: cfg needs more than its static scratch */
+  MOK_ESCRATCH = -7,   /* mok_layer_fwd_noalloc: cfg needs more than its static scratch */
+  MOK_EGROUP = -8      /* device-latched: group offsets that do not ascend within [0, T] */
 } mok_status;
 
 typedef enum {
@@ -194,6 +195,8 @@ typedef struct mok_fwd_state {
   uint8_t* h_scale;    /* MOK_MXFP8: [R_cap, I/32] E8M0 scales of h (h holds its E4M3
                           codes), kept for the backward; NULL = the forward keeps them in
                           its workspace only.  Unused otherwise. */
+  float* logits;       /* [S*T_src*E] router logits z (bias included), written by the forward
+                          for the own sources only; NULL = not kept */
 } mok_fwd_state;
 
 /* Bytes of device workspace the calls below need for `cfg` (256-byte aligned
@@ -209,6 +212,13 @@ size_t mok_workspace_bytes(const mok_config* cfg);
  * renormalised over the chosen k (= softmax of the chosen logits), fp32. */
 mok_status mok_route(const mok_config* cfg, int32_t T, const void* x, const void* w_router,
                      const float* bias, int32_t* topk_idx, float* topk_gate, void* stream);
+
+/* mok_route that also keeps the logits z (bias included): logits [T, E] fp32.
+ * topk_idx and topk_gate are those of mok_route, bit for bit.  logits may be
+ * NULL. */
+mok_status mok_route_logits(const mok_config* cfg, int32_t T, const void* x, const void* w_router,
+                            const float* bias, int32_t* topk_idx, float* topk_gate, float* logits,
+                            void* stream);
 
 /* Expert-contiguous layout [K01 count / place / group; K02 receiver-chosen
  * placement ordered by local expert].  Input: routing of all S sources
@@ -380,6 +390,143 @@ mok_status mok_layer_bwd(const mok_config* cfg, int32_t own_lo, int32_t own_n,
 mok_status mok_prepare_bwd(const mok_config* cfg, const void* w_gate, const void* w_up,
                            const void* w_down, void* wt_down, uint8_t* st_down, void* wt_gu,
                            uint8_t* st_gu, void* stream);
+
+/* Balance loss of the router and its gradient, for training.  The T tokens
+ * come in G groups of consecutive rows (the sequences of a batch, or one
+ * group); rows outside [group_offsets[0], group_offsets[G]) belong to no
+ * group.  A row counts if its mask byte is nonzero and not all of its logits
+ * are -inf.  With p = softmax(z) of a counted row, N_g the counted rows of
+ * group g, c_ge its chosen slots that name expert e, G+ the groups with
+ * N_g > 0, N = sum N_g and lse = log sum_e exp(z_e):
+ *   L_balance = alpha / G+ sum_g sum_e (E c_ge / (k N_g)) (sum_t p_te / N_g)
+ *   L_z       = beta / N sum_t lse_t^2
+ * (each 0 where nothing counts).  c_ge is constant in the gradient. */
+typedef struct mok_balance {
+  float alpha;                   /* weight of the balance loss */
+  float beta;                    /* weight of the z-loss */
+  int32_t G;                     /* groups; 0 = the T rows are one group */
+  const int32_t* group_offsets;  /* [G+1] ascending, device; unused (may be NULL) with G = 0 */
+  const uint8_t* token_mask;     /* [T], device, or NULL = every row counts */
+} mok_balance;
+
+/* Bytes of device workspace mok_balance_fwd needs for T rows (0 on a bad
+ * argument); uses cfg->E and cfg->k. */
+size_t mok_balance_ws_bytes(const mok_config* cfg, int32_t T, const mok_balance* bal);
+
+/* Both losses, the counts and the mean probabilities.  logits [T, E] fp32
+ * (mok_route_logits, or the own rows of mok_fwd_state.logits), topk_idx
+ * [T, k].  Outputs, overwritten (G = 0 counts as one group): counts [G, E],
+ * prob [G, E] the mean of p over the group's counted rows (0 for an empty
+ * group), n_tok [G+2] = N_g of every group, then N, then G+; loss [2] =
+ * L_balance, L_z.  An id outside [0, E) latches MOK_EROUTE and is not
+ * counted; offsets that do not ascend within [0, T] latch MOK_EGROUP and the
+ * group counts nothing.  NaN logits of counted rows reach the losses; values
+ * of rows that do not count are never used. */
+mok_status mok_balance_fwd(const mok_config* cfg, int32_t T, const mok_balance* bal,
+                           const float* logits, const int32_t* topk_idx, int32_t* counts,
+                           float* prob, int32_t* n_tok, float* loss, void* ws,
+                           int32_t* dev_status, void* stream);
+
+/* Gradient of d_loss[0] L_balance + d_loss[1] L_z with respect to the logits:
+ *   d_logits[t][e] = p_te (w_ge - sum_i p_ti w_gi) + p_te 2 beta d_loss[1] lse_t / N,
+ *   w_ge = alpha d_loss[0] E c_ge / (k N_g^2 G+),
+ * [T, E] fp32, overwritten: zero in rows of a group that do not count; rows
+ * outside every group are left as they are.  counts and n_tok as the forward
+ * wrote them; d_loss [2] fp32 on the device, or NULL = {1, 1}.  d_logits may
+ * be logits itself. */
+mok_status mok_balance_bwd(const mok_config* cfg, int32_t T, const mok_balance* bal,
+                           const float* logits, const int32_t* counts, const int32_t* n_tok,
+                           const float* d_loss, float* d_logits, int32_t* dev_status,
+                           void* stream);
+
+/* Bytes of device workspace mok_router_bwd needs for own_n sources of cfg (0
+ * on a bad argument). */
+size_t mok_router_bwd_ws_bytes(const mok_config* cfg, int32_t own_n);
+
+/* Backward of the router projection z = x W^T + bias for a dense gradient of
+ * the logits (mok_layer_bwd handles the chosen slots only): with d_logits
+ * [own_n*T_src, E] fp32 for the own sources [own_lo, own_lo+own_n) in order,
+ *   d_x[s]    = d_logits W_router       ([T_src, d], activation dtype; host
+ *               array of S device pointers, own entries used, or NULL)
+ *   dw_router = d_logits^T x            ([E, d] fp32, or NULL)
+ *   d_bias    = sum_t d_logits          ([E] fp32, or NULL)
+ * overwritten, or with accumulate != 0 added to what the buffers hold (after
+ * mok_layer_bwd; d_x is then rounded once more, from the fp32 sum).  Sums in
+ * fp32 at least, in a fixed order.  src_x is needed for dw_router, w_router
+ * for d_x; fp32 for MOK_F32, else bf16, 16-byte aligned like the outputs.
+ * own rows of zero overwrite (or leave) dw_router and d_bias with zeros. */
+mok_status mok_router_bwd(const mok_config* cfg, int32_t own_lo, int32_t own_n,
+                          const float* d_logits, const void* const* src_x, const void* w_router,
+                          void* const* d_x, float* dw_router, float* d_bias, int32_t accumulate,
+                          void* ws, void* stream);
+
+/* One tensor of an optimizer step: n contiguous elements (any n >= 0, any
+ * element alignment; 16-byte aligned pointers are faster).  Types are
+ * MOK_F32 or MOK_BF16.  master: fp32 values behind a bf16 p (p is then
+ * written as master rounded to nearest), or NULL.  Moments: state_bits 32:
+ * m, v fp32 [n], zero before the first step.  state_bits 8: m and v hold
+ * E4M3 codes [n] of m and of sqrt(v), in blocks of MOK_MX_BLOCK consecutive
+ * elements with E8M0 scales m_scale, v_scale [ceil(n / 32)]; all zero before
+ * the first step.  No two tensors of a call may overlap. */
+typedef struct mok_param {
+  void* p;
+  const void* g;
+  float* master;
+  void* m;
+  void* v;
+  uint8_t* m_scale;
+  uint8_t* v_scale;
+  int64_t n;
+  int32_t p_type;
+  int32_t g_type;
+  int32_t state_bits;   /* 32 or 8 */
+  float weight_decay;
+} mok_param;
+
+/* Bytes of device workspace mok_grad_norm needs (0 on a bad argument). */
+size_t mok_grad_norm_ws_bytes(int32_t n_params, const mok_param* params);
+
+/* Global L2 norm of the gradients (g, g_type, n of every tensor; the other
+ * fields are not used) and the factor that clips it:
+ *   out[0] = norm = sqrt(sum g^2), out[1] = min(1, max_norm / (norm + 1e-6))
+ * fp32 on the device; out[1] is 1 for max_norm <= 0 and NaN if the norm is
+ * not finite.  The squares are summed in 64 bits in a fixed order. */
+mok_status mok_grad_norm(int32_t n_params, const mok_param* params, float max_norm, float* out,
+                         void* ws, void* stream);
+
+/* Step constants of mok_adamw. */
+typedef struct mok_adamw_args {
+  double lr, beta1, beta2, eps;
+  int64_t step;              /* number of this step, 1 for the first */
+  uint64_t seed;             /* of the random rounding */
+  float grad_scale;          /* gradients are multiplied by grad_scale * *dev_scale */
+  int32_t random_params;     /* bf16 p without master: 0 = round to nearest, 1 = at random */
+  const float* dev_scale;    /* device, or NULL = 1 (out + 1 of mok_grad_norm); NaN: the call
+                                leaves every tensor as it is */
+  const double* dev_lr;      /* device, or NULL = lr: read when the step runs, for captured steps */
+  const int64_t* dev_step;   /* device, or NULL = step */
+} mok_adamw_args;
+
+/* One AdamW step over n_params tensors (host array; the call reads it before
+ * it returns).  With g' = g grad_scale *dev_scale and t the step number:
+ *   m = beta1 m + (1 - beta1) g';  v = beta2 v + (1 - beta2) g'^2
+ *   p = p (1 - lr weight_decay)
+ *       - lr / (1 - beta1^t) m / (sqrt(v) / sqrt(1 - beta2^t) + eps)
+ * in fp32 from the stored values, p from the new moments before those are
+ * rounded.  8-bit moments: the scale of a block is the smallest power of two
+ * that takes the block's largest magnitude to at most 448; a value is then
+ * rounded to one of its two E4M3 neighbours at random, up with the
+ * probability of its distance from the lower one (a slowly moving average
+ * would otherwise never leave its code), and a sqrt(v) above zero stays
+ * above zero.  Random words: SplitMix64's finaliser of a counter, element i
+ * of tensor t (its place in the array) takes w = a + (i % 8) b mod 2^32 for
+ * the moments (low half m, high half v) and the high half of b + (i % 8) a
+ * for p, where a, b are the halves of mix(key + (i / 8 + 1) G), key =
+ * mix(mix(seed + t) + step G), G = 0x9E3779B97F4A7C15; the same inputs give
+ * the same bytes.  Non-finite gradients make the element's m, v and p
+ * non-finite (E4M3 NaN; sqrt(v) saturates). */
+mok_status mok_adamw(int32_t n_params, const mok_param* params, const mok_adamw_args* args,
+                     void* stream);
 
 /* Tuner of the fused path's minibatch size and workgroup split [K02: the
  * split of SMs between the communication and compute sides is set directly,
