@@ -3,9 +3,25 @@
 //   dx[t][n] = sum_e dz[t][e] W[e][n]      (contraction over the experts)
 //   dW[e][n] = sum_t dz[t][e] x[t][n]      (contraction over the tokens)
 //   db[e]    = sum_t dz[t][e]
-// dz stays fp32: both products run on the fp32 matrix cores
+//
+// fp32 layers: both products on the fp32 matrix cores
 // (v_mfma_f32_32x32x2_f32), whose operands hold one k per lane, so operands
 // that are strided along k need no transpose.
+//
+// bf16 layers: x and W are bf16, dz is fp32.  A fp32 value is the sum of
+// three bf16 parts (hi = bf16(v), mid = bf16(v - hi), lo = bf16(v - hi -
+// mid): 8 bits each, exact in between), so the products run on the bf16
+// matrix cores, eight times the fp32 rate, once per part: three parts for
+// dW, whose fp32 result keeps fp32's accuracy (2^-24 of each term), two for
+// dx, which is rounded to bf16 (2^-17 of each term against 2^-9).
+//   1. router_split_kernel writes the parts of dz once (and sums db);
+//   2. router_dx_kernel: a wave keeps the parts of its 32 token rows in
+//      registers for all experts and walks column steps of 64, W coming
+//      through LDS;
+//   3. router_dw_kernel: 64 x 64 of dW per wave, both operands through an
+//      LDS ring filled by direct loads, split over the tokens;
+//   4. router_reduce_kernel adds the token chunks in order.
+#include "mok_gemm2.h"
 #include "mok_internal.h"
 
 namespace mok {
@@ -16,6 +32,8 @@ constexpr int kThreads = 256;
 constexpr int kTile = 64;   // output tile 64 x 64, four waves of 32 x 32
 constexpr int kKB = 32;     // contraction steps staged through LDS at a time
 constexpr int kPitch = kTile + 4;
+constexpr int kBf16Threads = 512;   // eight waves in the bf16 products
+constexpr int kBK = 16;             // token rows per LDS stage of dW
 
 struct RArgs {
   const float* dz;
@@ -29,11 +47,16 @@ struct RArgs {
   int T, T_src, d, E, own_lo, chunks;
   int64_t chunk_rows;
   int add;
+  // bf16: the parts of dz, [T][E tiles][3 parts][EW]
+  bf16_t* parts;
+  int ew, etiles;      // experts per tile (64, 128 or 256) and tiles
+  int64_t split_rows;  // token rows per workgroup of the split
+  int db_parts;        // partial sums of db per expert
+  int n_chunks;        // column chunks of dx, each a workgroup per row block
 };
 
-template <typename T>
-__device__ __forceinline__ const T* x_row(const RArgs& a, int t) {
-  return reinterpret_cast<const T*>(a.x.p[a.own_lo + t / a.T_src]) + (size_t)(t % a.T_src) * a.d;
+__device__ __forceinline__ const float* x_row(const RArgs& a, int t) {
+  return reinterpret_cast<const float*>(a.x.p[a.own_lo + t / a.T_src]) + (size_t)(t % a.T_src) * a.d;
 }
 
 // acc += A B over one staged block: sA [kKB][kPitch] (k, m), sB (k, n)
@@ -47,21 +70,20 @@ __device__ __forceinline__ void mma_block(const float* sA, const float* sB, int 
 // row of accumulator register r in a 32 x 32 block (its column is lane % 32)
 __device__ __forceinline__ int acc_row(int r, int lane) { return (r >> 2) * 8 + (lane >> 5) * 4 + (r & 3); }
 
-template <typename T>
 __global__ __launch_bounds__(kThreads) void router_dx_kernel(RArgs a) {
   __shared__ float sA[kKB * kPitch], sB[kKB * kPitch];
   const int nt = a.d / kTile;
   const int n0 = (int)(blockIdx.x % nt) * kTile, t0 = (int)(blockIdx.x / nt) * kTile;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int wm = (wave >> 1) * 32, wn = (wave & 1) * 32;
-  const T* w = reinterpret_cast<const T*>(a.w);
+  const float* w = reinterpret_cast<const float*>(a.w);
   f32x16_t acc = {};
   for (int e0 = 0; e0 < a.E; e0 += kKB) {
     for (int i = tid; i < kTile * kKB; i += kThreads) {
       const int t = i / kKB, e = i % kKB;
       sA[e * kPitch + t] = t0 + t < a.T && e0 + e < a.E ? a.dz[(size_t)(t0 + t) * a.E + e0 + e] : 0.0f;
       const int k = i / kTile, n = i % kTile;
-      sB[k * kPitch + n] = e0 + k < a.E ? to_f32<T>(w[(size_t)(e0 + k) * a.d + n0 + n]) : 0.0f;
+      sB[k * kPitch + n] = e0 + k < a.E ? w[(size_t)(e0 + k) * a.d + n0 + n] : 0.0f;
     }
     __syncthreads();
     mma_block(sA, sB, wm, wn, acc);
@@ -71,12 +93,11 @@ __global__ __launch_bounds__(kThreads) void router_dx_kernel(RArgs a) {
   for (int r = 0; r < 16; ++r) {
     const int t = t0 + wm + acc_row(r, lane);
     if (t >= a.T) continue;
-    T* o = reinterpret_cast<T*>(a.d_x.p[a.own_lo + t / a.T_src]) + (size_t)(t % a.T_src) * a.d + n0 + wn + (lane & 31);
-    *o = from_f32<T>(a.add ? to_f32<T>(*o) + acc[r] : acc[r]);
+    float* o = reinterpret_cast<float*>(a.d_x.p[a.own_lo + t / a.T_src]) + (size_t)(t % a.T_src) * a.d + n0 + wn + (lane & 31);
+    *o = a.add ? *o + acc[r] : acc[r];
   }
 }
 
-template <typename T>
 __global__ __launch_bounds__(kThreads) void router_dw_kernel(RArgs a) {
   __shared__ float sA[kKB * kPitch], sB[kKB * kPitch];
   const int n0 = blockIdx.x * kTile, e0 = blockIdx.y * kTile, chunk = blockIdx.z;
@@ -92,7 +113,7 @@ __global__ __launch_bounds__(kThreads) void router_dw_kernel(RArgs a) {
       const int k = i / kTile, c = i % kTile;
       const bool there = t0 + k < hi;
       sA[k * kPitch + c] = there && e0 + c < a.E ? a.dz[(size_t)(t0 + k) * a.E + e0 + c] : 0.0f;
-      sB[k * kPitch + c] = there && a.dw ? to_f32<T>(x_row<T>(a, t0 + k)[n0 + c]) : 0.0f;
+      sB[k * kPitch + c] = there && a.dw ? x_row(a, t0 + k)[n0 + c] : 0.0f;
     }
     __syncthreads();
     mma_block(sA, sB, wm, wn, acc);
@@ -117,50 +138,465 @@ __global__ __launch_bounds__(kThreads) void router_dw_kernel(RArgs a) {
   }
 }
 
-// dW and db from the chunks' partial sums, in chunk order
-__global__ __launch_bounds__(kThreads) void router_reduce_kernel(RArgs a) {
-  const size_t n = (size_t)a.E * a.d, i = ((size_t)blockIdx.x * kThreads + threadIdx.x) * 4;
-  if (a.dw && i < n) {
+// ------------------------------------------------------------------ bf16: split
+// Workgroup: split_rows token rows; a thread keeps one group of 8 experts
+// (so the column sums of db stay in its registers, in 64 bits) and takes
+// every (256 / groups)-th row.
+__global__ __launch_bounds__(kThreads) void router_split_kernel(RArgs a) {
+  __shared__ double s_db[8][kThreads];
+  const int Ep = a.ew * a.etiles, groups = Ep / 8;
+  const int q = threadIdx.x % groups, r = threadIdx.x / groups, step = kThreads / groups;
+  const int e0 = q * 8;
+  const bool wide = a.E % 4 == 0 && ((uintptr_t)a.dz & 15) == 0;
+  const int64_t lo = (int64_t)blockIdx.x * a.split_rows;
+  const int64_t hi = lo + a.split_rows < a.T ? lo + a.split_rows : a.T;
+  double db[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) db[j] = 0.0;
+  for (int64_t t = lo + r; t < hi; t += step) {
+    float v[8];
+    const float* row = a.dz + (size_t)t * a.E + e0;
+    if (wide) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        float4 u = make_float4(0, 0, 0, 0);
+        if (e0 + 4 * h < a.E) u = *reinterpret_cast<const float4*>(row + 4 * h);
+        v[4 * h] = u.x, v[4 * h + 1] = u.y, v[4 * h + 2] = u.z, v[4 * h + 3] = u.w;
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = e0 + j < a.E ? row[j] : 0.0f;
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) db[j] += (double)v[j];
+    if (a.parts) {
+      bf16_t* o = a.parts + ((size_t)t * a.etiles + e0 / a.ew) * 3 * a.ew + e0 % a.ew;
+#pragma unroll
+      for (int p = 0; p < 3; ++p) {
+        uint32_t w[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          w[j] = pack2_bf16(v[2 * j], v[2 * j + 1]);
+          v[2 * j] -= __uint_as_float(w[j] << 16);
+          v[2 * j + 1] -= __uint_as_float(w[j] & 0xFFFF0000u);
+        }
+        st16(o + p * a.ew, make_uint4(w[0], w[1], w[2], w[3]));
+      }
+    }
+  }
+  if (!a.db) return;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) s_db[j][threadIdx.x] = db[j];
+  __syncthreads();
+  for (int e = threadIdx.x; e < a.E; e += kThreads) {
+    double s = 0.0;
+    for (int i = 0; i < step; ++i) s += s_db[e & 7][i * groups + (e >> 3)];
+    a.dbp[(size_t)blockIdx.x * a.E + e] = s;
+  }
+}
+
+// s_barrier for every wave's own LDS work and direct loads: no LDS access
+// moves across it.
+__device__ __forceinline__ void barrier() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+// ------------------------------------------------------------------ bf16: dx
+// Fragment of 32 columns from n (k = 16 s ..) of an LDS tile of 64 columns
+// (128-byte k-rows) read with ds_read_b64_tr_b16: in a 16-lane group lane a
+// points at (k + a/4, n + 4 (a%4)) and lane i receives k..k+3 of column n + i.
+// Chunk c (16 bytes) of k-row r sits at c ^ 4 ((r / 2) & 1): four consecutive
+// k-rows of one column range then cover all banks.
+__device__ __forceinline__ bf16x8_t frag64(const char* lds, int n0, int s) {
+  const int lane = threadIdx.x & 63, g = lane >> 4, li = lane & 15;
+  const int n = n0 + 16 * (g & 1) + 4 * (li & 3), kb = 16 * s + 8 * (g >> 1) + (li >> 2);
+  g2::v4s h[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int kr = kb + 4 * i, c = (n >> 3) ^ (4 * ((kr >> 1) & 1));
+    h[i] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((g2::lds_v4s*)(lds + kr * 128 + c * 16 + (n & 7) * 2));
+  }
+  return __builtin_bit_cast(bf16x8_t, __builtin_shufflevector(h[0], h[1], 0, 1, 2, 3, 4, 5, 6, 7));
+}
+
+// NK: 16-expert steps (E <= 16 NK); WAVES of 32 token rows each.
+template <int NK, int WAVES>
+__global__ __launch_bounds__(64 * WAVES, WAVES == 8 ? 2 : 1) void router_dx_bf16_kernel(RArgs a) {
+  constexpr int STAGE = NK * 16 * 128;               // bytes of W per column step
+  constexpr int LOADS = STAGE / 1024 / WAVES;        // direct loads per wave and step
+  static_assert(LOADS >= 1, "every wave loads");
+  __shared__ __attribute__((aligned(16))) char smem[2 * STAGE + WAVES * 4096];
+  const int lane = threadIdx.x & 63;
+  const int wave = (int)g2::wave_id();
+  // workgroups of one row block on one XCD (b % 8), so its parts meet in an L2
+  const int rb_n = (a.T + 32 * WAVES - 1) / (32 * WAVES);
+  int b = blockIdx.x, rb, ch;
+  const int full = rb_n / 8 * 8 * a.n_chunks;
+  if (b < full) {
+    rb = b % 8 + 8 * (b / 8 / a.n_chunks);
+    ch = b / 8 % a.n_chunks;
+  } else {
+    b -= full;
+    rb = rb_n / 8 * 8 + b / a.n_chunks;
+    ch = b % a.n_chunks;
+  }
+  const int steps = a.d / 64;
+  const int s0 = (int)((int64_t)steps * ch / a.n_chunks), s1 = (int)((int64_t)steps * (ch + 1) / a.n_chunks);
+  const bf16_t* w = reinterpret_cast<const bf16_t*>(a.w);
+  const unsigned lds0 = g2::lds_addr_of(smem);
+  // this wave's direct loads: source of column 0, or the zero page past E
+  const char* wp[LOADS];
+  int adv[LOADS];
+#pragma unroll
+  for (int j = 0; j < LOADS; ++j) {
+    const int row = (wave * LOADS + j) * 8 + lane / 8;
+    const int c = (lane % 8) ^ (4 * ((row >> 1) & 1));
+    const bool there = row < a.E;
+    wp[j] = there ? reinterpret_cast<const char*>(w + (size_t)row * a.d + c * 8)
+                  : reinterpret_cast<const char*>(g2::g_zero);
+    adv[j] = there ? 128 : 0;
+  }
+  auto issue = [&](int s, int slot) {
+#pragma unroll
+    for (int j = 0; j < LOADS; ++j)
+      g2::load_lds16(wp[j] + (size_t)s * adv[j], lds0 + slot * STAGE + (wave * LOADS + j) * 1024);
+  };
+  if (s0 < s1) issue(s0, 0);
+  // the wave's rows: parts hi and mid of every expert, in registers
+  const int t0 = (rb * WAVES + wave) * 32;
+  bf16x8_t hi[NK], mid[NK];
+  {
+    const int t = t0 + (lane & 31);
+    const bf16_t* p = a.parts + (size_t)t * a.etiles * 3 * a.ew;
+#pragma unroll
+    for (int k = 0; k < NK; ++k) {
+      const int e = 16 * k + 8 * (lane >> 5);
+      const bf16_t* q = p + (e / a.ew) * 3 * a.ew + e % a.ew;
+      uint4 u = make_uint4(0, 0, 0, 0), v = u;
+      if (t < a.T) {
+        u = ld16(q);
+        v = ld16(q + a.ew);
+      }
+      hi[k] = __builtin_bit_cast(bf16x8_t, u);
+      mid[k] = __builtin_bit_cast(bf16x8_t, v);
+    }
+  }
+  // the rows this lane stores: 8 lanes per row, four rows
+  bf16_t* out[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int t = t0 + 8 * i + lane / 8;
+    out[i] = t < a.T ? reinterpret_cast<bf16_t*>(a.d_x.p[a.own_lo + t / a.T_src]) + (size_t)(t % a.T_src) * a.d + (lane % 8) * 8
+                     : nullptr;
+  }
+  char* stg = smem + 2 * STAGE + wave * 4096;  // 32 rows x 128 bytes; chunk c of row r at c ^ (r & 7)
+  uint4 base[4];
+  auto store = [&](int s) {  // the staged tile of column step s
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (!out[i]) continue;
+      const int r = 8 * i + lane / 8;
+      uint4 u = *reinterpret_cast<const uint4*>(stg + r * 128 + ((lane % 8) ^ (r & 7)) * 16);
+      st16(out[i] + (size_t)s * 64, u);
+    }
+  };
+  for (int s = s0; s < s1; ++s) {
+    // this wave's loads of step s (and its stores of the step before last)
+    // are done, everyone's are after the barrier; everyone has also left the
+    // buffer that step s + 1 will fill
+    g2::wait_vmcnt_lgkm0<0>();
+    barrier();
+    const int slot = (s - s0) & 1;
+    if (s + 1 < s1) issue(s + 1, slot ^ 1);
+    if (s > s0) store(s - 1);
+    if (a.add) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) base[i] = out[i] ? ld16(out[i] + (size_t)s * 64) : make_uint4(0, 0, 0, 0);
+    }
+    const char* W = smem + slot * STAGE;
+    f32x16_t acc[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[j][r] = 0.0f;
+#pragma unroll
+    for (int k = 0; k < NK; ++k)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const bf16x8_t f = frag64(W, 32 * j, k);
+        acc[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f, mid[k], acc[j], 0, 0, 0);
+        acc[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f, hi[k], acc[j], 0, 0, 0);
+      }
+    // lane holds row lane % 32, columns 32 j + 8 g + 4 (lane / 32) + 0..3
+    if (a.add) {  // the base goes through the staging rows to meet the sums
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int r = 8 * i + lane / 8;
+        st16(stg + r * 128 + ((lane % 8) ^ (r & 7)) * 16, base[i]);
+      }
+      g2::wave_lds_fence();
+    }
+    const int r = lane & 31;
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const int col = 32 * j + 8 * g + 4 * (lane >> 5);
+        uint2* p = reinterpret_cast<uint2*>(stg + r * 128 + ((col >> 3) ^ (r & 7)) * 16 + (col & 7) * 2);
+        float v[4] = {acc[j][4 * g], acc[j][4 * g + 1], acc[j][4 * g + 2], acc[j][4 * g + 3]};
+        if (a.add) {
+          const uint2 u = *p;
+          v[0] += __uint_as_float(u.x << 16), v[1] += __uint_as_float(u.x & 0xFFFF0000u);
+          v[2] += __uint_as_float(u.y << 16), v[3] += __uint_as_float(u.y & 0xFFFF0000u);
+        }
+        *p = g2::pack4_bf16(v[0], v[1], v[2], v[3]);
+      }
+    g2::wave_lds_fence();
+  }
+  if (s0 < s1) store(s1 - 1);
+}
+
+// ------------------------------------------------------------------ bf16: dW
+// Tile EW experts x EN columns, eight waves of 64 x 64; LDS ring of NS stages
+// of 16 token rows, each [parts of EW experts | EN columns of x].  k-rows are
+// multiples of 256 bytes; chunk c of k-row r sits at c ^ 4 (r & 3).
+template <int EW>
+struct DwCfg {
+  static constexpr int WE = EW / 64, WN = 8 / WE;
+  static constexpr int EN = 64 * WN;
+  static constexpr int RA = EW == 64 ? 512 : 6 * EW;   // bytes of a k-row of parts (64: padded)
+  static constexpr int RB = 2 * EN;
+  static constexpr int A_BYTES = kBK * RA, STAGE = kBK * (RA + RB);
+  static constexpr int NS = 160 * 1024 / STAGE > 6 ? 6 : (160 * 1024 - 1024) / STAGE;
+  static constexpr int UNITS = STAGE / 1024;           // 1 KiB direct loads per stage
+  static constexpr int Q = UNITS / 8, X = UNITS % 8;   // per wave; waves below X issue one more
+  static_assert(STAGE % 1024 == 0 && A_BYTES % 1024 == 0 && NS >= 3, "ring");
+};
+
+__device__ __forceinline__ bf16x8_t frag_mn(const char* lds, int rb, int n0) {
+  const int lane = threadIdx.x & 63, g = lane >> 4, li = lane & 15;
+  const int n = n0 + 16 * (g & 1) + 4 * (li & 3), kb = 8 * (g >> 1) + (li >> 2);
+  g2::v4s h[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int kr = kb + 4 * i, c = (n >> 3) ^ (4 * (kr & 3));
+    h[i] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((g2::lds_v4s*)(lds + kr * rb + c * 16 + (n & 7) * 2));
+  }
+  return __builtin_bit_cast(bf16x8_t, __builtin_shufflevector(h[0], h[1], 0, 1, 2, 3, 4, 5, 6, 7));
+}
+
+template <int EW>
+__global__ __launch_bounds__(kBf16Threads, 2) void router_dw_bf16_kernel(RArgs a) {
+  typedef DwCfg<EW> C;
+  __shared__ __attribute__((aligned(16))) char smem[C::NS * C::STAGE];
+  __shared__ const bf16_t* s_x[MOK_MAX_SOURCES];
+  const int lane = threadIdx.x & 63;
+  const int wave = (int)g2::wave_id();
+  // a token chunk's tiles on one XCD (b % 8) while the chunks fill whole
+  // rounds of eight: its parts are then read from one L2
+  const int ntn = (a.d + C::EN - 1) / C::EN, per = ntn * a.etiles;
+  int b = blockIdx.x, chunk, tile;
+  const int full = a.chunks / 8 * 8 * per;
+  if (b < full) {
+    chunk = b % 8 + 8 * (b / 8 / per);
+    tile = b / 8 % per;
+  } else {
+    b -= full;
+    const int left = a.chunks - a.chunks / 8 * 8;
+    chunk = a.chunks / 8 * 8 + b % left;
+    tile = b / left;
+  }
+  const int et = tile / ntn, n0 = tile % ntn * C::EN;
+  for (int i = threadIdx.x; i < MOK_MAX_SOURCES; i += kBf16Threads) s_x[i] = reinterpret_cast<const bf16_t*>(a.x.p[i]);
+  __syncthreads();
+  const int64_t lo64 = (int64_t)chunk * a.chunk_rows;
+  const int lo = (int)min(lo64, (int64_t)a.T), hi = (int)min(lo64 + a.chunk_rows, (int64_t)a.T);
+  const int KT = (hi - lo + kBK - 1) / kBK;
+  const unsigned lds0 = g2::lds_addr_of(smem);
+  // This wave's units w, w + 8, ... of a stage: unit u is LDS bytes
+  // [1024 u, 1024 u + 1024), chunk positions 64 u + lane.
+  constexpr int QM = C::Q + (C::X ? 1 : 0);
+  const int nq = C::Q + (wave < C::X ? 1 : 0);
+  int krow[QM], ucol[QM], xt[QM], xs[QM];   // k-row, element column, and for x units the token's place
+#pragma unroll
+  for (int j = 0; j < QM; ++j) {
+    const int u = wave + 8 * j;
+    const bool isA = u * 1024 < C::A_BYTES;
+    const int pos = isA ? u * 64 + lane : (u * 1024 - C::A_BYTES) / 16 + lane;
+    const int cpr = (isA ? C::RA : C::RB) / 16;
+    krow[j] = pos / cpr;
+    const int c = (pos % cpr) ^ (4 * (krow[j] & 3));
+    ucol[j] = c * 8;
+    if (isA) {
+      if (ucol[j] >= 3 * EW) ucol[j] = -1;             // the padding of 64-wide tiles
+    } else if (n0 + ucol[j] >= a.d) ucol[j] = -1;
+    const int t = lo + krow[j];
+    xs[j] = t / a.T_src;
+    xt[j] = t % a.T_src;
+  }
+  const size_t prow = (size_t)a.etiles * 3 * EW;
+  auto issue = [&](int kt) {
+    const int slot = kt % C::NS;
+#pragma unroll
+    for (int j = 0; j < QM; ++j) {
+      if (j >= nq) continue;                            // wave-uniform
+      const int u = wave + 8 * j;
+      const int t = lo + kt * kBK + krow[j];
+      const void* src = g2::g_zero;
+      if (u * 1024 < C::A_BYTES) {
+        if (t < hi && ucol[j] >= 0) src = a.parts + (size_t)t * prow + (size_t)et * 3 * EW + ucol[j];
+      } else {
+        if (t < hi && ucol[j] >= 0) src = s_x[a.own_lo + xs[j]] + (size_t)xt[j] * a.d + n0 + ucol[j];
+        xt[j] += kBK;
+        while (xt[j] >= a.T_src && t < hi) {
+          xt[j] -= a.T_src;
+          ++xs[j];
+        }
+      }
+      g2::load_lds16(src, lds0 + slot * C::STAGE + u * 1024);
+    }
+  };
+  f32x16_t acc[2][2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
+  const int we = wave / C::WN * 64, wn = wave % C::WN * 64;
+  for (int s = 0; s < C::NS - 1; ++s) issue(s);         // stages past KT read zeros
+  for (int kt = 0; kt < KT; ++kt) {
+    // this wave's loads of stage kt have landed (the NS - 2 later stages stay
+    // in flight); after the barrier everyone's have, and everyone is done
+    // with stage kt - 1, whose slot the next loads fill
+    if (wave < C::X) g2::wait_vmcnt_lgkm0<(C::NS - 2) * (C::Q + 1)>();
+    else g2::wait_vmcnt_lgkm0<(C::NS - 2) * C::Q>();
+    barrier();
+    issue(kt + C::NS - 1);
+    const char* A = smem + kt % C::NS * C::STAGE;
+    const char* B = A + C::A_BYTES;
+    bf16x8_t fb[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) fb[j] = frag_mn(B, C::RB, wn + 32 * j);
+#pragma unroll
+    for (int p = 2; p >= 0; --p)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const bf16x8_t fa = frag_mn(A, C::RA, p * EW + we + 32 * i);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa, fb[j], acc[i][j], 0, 0, 0);
+      }
+  }
+  g2::wait_vmcnt_lgkm0<0>();   // no load of this workgroup outlives it
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        const int e = et * EW + we + 32 * i + acc_row(r, lane), n = n0 + wn + 32 * j + (lane & 31);
+        if (e >= a.E || n >= a.d) continue;
+        const size_t k = (size_t)e * a.d + n;
+        if (a.part) a.part[(size_t)chunk * a.E * a.d + k] = acc[i][j][r];
+        else a.dw[k] = a.add ? a.dw[k] + acc[i][j][r] : acc[i][j][r];
+      }
+}
+
+// dW from the chunks' partial sums in chunk order (the first dw_blocks
+// workgroups), and db: 32 experts per workgroup, eight threads an expert,
+// each adding every eighth partial sum.
+__global__ __launch_bounds__(kThreads) void router_reduce_kernel(RArgs a, int dw_blocks) {
+  __shared__ double s_db[8][32];
+  if ((int)blockIdx.x < dw_blocks) {
+    const size_t n = (size_t)a.E * a.d, i = ((size_t)blockIdx.x * kThreads + threadIdx.x) * 4;
+    if (i >= n) return;
     float4 s = a.add ? *reinterpret_cast<const float4*>(a.dw + i) : make_float4(0, 0, 0, 0);
     for (int c = 0; c < a.chunks; ++c) {
       const float4 p = *reinterpret_cast<const float4*>(a.part + c * n + i);
       s.x += p.x, s.y += p.y, s.z += p.z, s.w += p.w;
     }
     *reinterpret_cast<float4*>(a.dw + i) = s;
+    return;
   }
-  const int e = blockIdx.x * kThreads + threadIdx.x;
-  if (a.db && e < a.E) {
-    double s = a.add ? a.db[e] : 0.0;
-    for (int c = 0; c < a.chunks; ++c) s += a.dbp[(size_t)c * a.E + e];
+  const int c = threadIdx.x % 32, q = threadIdx.x / 32, e = ((int)blockIdx.x - dw_blocks) * 32 + c;
+  double s = 0.0;
+  if (e < a.E)
+    for (int i = q; i < a.db_parts; i += 8) s += a.dbp[(size_t)i * a.E + e];
+  s_db[q][c] = s;
+  __syncthreads();
+  if (q == 0 && e < a.E) {
+    s = a.add ? a.db[e] : 0.0;
+    for (int i = 0; i < 8; ++i) s += s_db[i][c];
     a.db[e] = (float)s;
   }
 }
 
 size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
-// Token chunks of the dW product: enough workgroups for four per CU, at
-// least 256 tokens each.
-void dw_chunks(int64_t T, int d, int E, int* chunks, int64_t* rows) {
-  const int64_t tiles = (int64_t)(d / kTile) * ((E + kTile - 1) / kTile);
-  int64_t c = 1024 / tiles;
-  if (c > (T + 255) / 256) c = (T + 255) / 256;
+int expert_tile(int E) { return E <= 64 ? 64 : E <= 128 ? 128 : 256; }
+
+// Token chunks of the dW product and the workspace that follows from them.
+// fp32: workgroups for four per CU, at least 64 tokens each.  bf16: one
+// workgroup of eight waves per CU, at least 128 tokens each (every chunk
+// costs a fp32 copy of dW written and read again).
+struct Plan {
+  int chunks = 1, ew = 0, etiles = 0, db_parts = 0;
+  int64_t chunk_rows = 0, split_rows = 0;
+  size_t parts = 0, dbp = 0, part = 0, total = 0;
+};
+
+Plan make_plan(int prec, int64_t T, int d, int E) {
+  Plan p;
+  const bool f32 = prec == MOK_F32;
+  p.ew = expert_tile(E);
+  p.etiles = (E + p.ew - 1) / p.ew;
+  const int en = 64 * 8 * 64 / p.ew;
+  const int64_t tiles = f32 ? (int64_t)(d / kTile) * ((E + kTile - 1) / kTile) : (int64_t)((d + en - 1) / en) * p.etiles;
+  const int64_t least = f32 ? 64 : 128, unit = f32 ? kKB : kBK;
+  int64_t c = (f32 ? 1024 : 256) / tiles;
+  if (c > (T + least - 1) / least) c = (T + least - 1) / least;
   if (c < 1) c = 1;
-  const int64_t r = ((T + c - 1) / c + kKB - 1) / kKB * kKB;
-  *rows = r;
-  *chunks = r > 0 ? (int)((T + r - 1) / r) : 1;
+  p.chunk_rows = ((T + c - 1) / c + unit - 1) / unit * unit;
+  p.chunks = p.chunk_rows > 0 ? (int)((T + p.chunk_rows - 1) / p.chunk_rows) : 1;
+  if (f32) {
+    p.db_parts = p.chunks;
+  } else {
+    p.split_rows = (T + 511) / 512 > 16 ? (T + 511) / 512 : 16;
+    p.db_parts = (int)((T + p.split_rows - 1) / p.split_rows);
+    p.parts = align256((size_t)T * p.etiles * 3 * p.ew * 2);
+  }
+  p.dbp = align256((size_t)p.db_parts * E * 8);
+  p.part = p.chunks > 1 ? align256((size_t)p.chunks * E * d * 4) : 0;
+  p.total = p.parts + p.dbp + p.part + 256;
+  return p;
+}
+
+template <int NK, int WAVES>
+void launch_dx(RArgs& a, hipStream_t stream) {
+  // one workgroup per CU at least, as far as there are column steps
+  const int64_t rb = ((int64_t)a.T + 32 * WAVES - 1) / (32 * WAVES);
+  int64_t n = (256 + rb - 1) / rb;
+  if (n > a.d / 64) n = a.d / 64;
+  a.n_chunks = (int)n;
+  hipLaunchKernelGGL((router_dx_bf16_kernel<NK, WAVES>), dim3((unsigned)(rb * n)), dim3(64 * WAVES), 0, stream, a);
+}
+
+template <int EW>
+void launch_dw(const RArgs& a, hipStream_t stream) {
+  const unsigned grid = (unsigned)((a.d + DwCfg<EW>::EN - 1) / DwCfg<EW>::EN) * a.etiles * a.chunks;
+  hipLaunchKernelGGL(router_dw_bf16_kernel<EW>, dim3(grid), dim3(kBf16Threads), 0, stream, a);
 }
 
 }  // namespace
 
 size_t router_bwd_ws_bytes(int prec, int64_t T, int d, int E) {
-  (void)prec;
-  int chunks;
-  int64_t rows;
-  dw_chunks(T, d, E, &chunks, &rows);
-  return chunks > 1 ? align256((size_t)chunks * E * d * 4) + align256((size_t)chunks * E * 8) : 256;
+  return make_plan(prec == MOK_F32 ? MOK_F32 : MOK_BF16, T, d, E).total;
 }
 
 mok_status launch_router_bwd(const RouterBwdPlan& p, hipStream_t stream) {
+  const Plan pl = make_plan(p.prec, p.T, p.d, p.E);
   RArgs a = {};
   a.dz = p.dz;
   a.w = p.w;
@@ -170,29 +606,52 @@ mok_status launch_router_bwd(const RouterBwdPlan& p, hipStream_t stream) {
   a.db = p.db;
   a.T = p.T, a.T_src = p.T_src > 0 ? p.T_src : 1, a.d = p.d, a.E = p.E, a.own_lo = p.own_lo;
   a.add = p.add;
-  dw_chunks(p.T, p.d, p.E, &a.chunks, &a.chunk_rows);
-  if (a.chunks > 1) {
-    a.part = (float*)p.ws;
-    a.dbp = (double*)((char*)p.ws + align256((size_t)a.chunks * p.E * p.d * 4));
-  }
+  a.chunks = pl.chunks, a.chunk_rows = pl.chunk_rows;
+  a.ew = pl.ew, a.etiles = pl.etiles, a.split_rows = pl.split_rows, a.db_parts = pl.db_parts;
+  char* ws = (char*)p.ws;
+  a.part = pl.chunks > 1 ? (float*)(ws + pl.parts + pl.dbp) : nullptr;
   const dim3 blk(kThreads);
   const bool f32 = p.prec == MOK_F32;
-  if (p.want_dx && p.T > 0) {
-    const dim3 grid((unsigned)((int64_t)(p.d / kTile) * (((int64_t)p.T + kTile - 1) / kTile)));
-    if (f32) hipLaunchKernelGGL(router_dx_kernel<float>, grid, blk, 0, stream, a);
-    else hipLaunchKernelGGL(router_dx_kernel<bf16_t>, grid, blk, 0, stream, a);
-    trace_mark(p.tr, "router_dx", stream);
-  }
-  if (p.dw || p.db) {
-    const dim3 grid(p.dw ? p.d / kTile : 1, (p.E + kTile - 1) / kTile, a.chunks);
-    if (f32) hipLaunchKernelGGL(router_dw_kernel<float>, grid, blk, 0, stream, a);
-    else hipLaunchKernelGGL(router_dw_kernel<bf16_t>, grid, blk, 0, stream, a);
-    trace_mark(p.tr, "router_dw", stream);
-    if (a.chunks > 1) {
-      const size_t n = (size_t)p.E * p.d / 4;
-      hipLaunchKernelGGL(router_reduce_kernel, dim3((unsigned)((n + kThreads - 1) / kThreads)), blk, 0, stream, a);
-      trace_mark(p.tr, "router_reduce", stream);
+  if (f32) {
+    a.dbp = pl.chunks > 1 ? (double*)ws : nullptr;
+    if (p.want_dx && p.T > 0) {
+      const dim3 grid((unsigned)((int64_t)(p.d / kTile) * (((int64_t)p.T + kTile - 1) / kTile)));
+      hipLaunchKernelGGL(router_dx_kernel, grid, blk, 0, stream, a);
+      trace_mark(p.tr, "router_dx", stream);
     }
+    if (p.dw || p.db) {
+      const dim3 grid(p.dw ? p.d / kTile : 1, (p.E + kTile - 1) / kTile, a.chunks);
+      hipLaunchKernelGGL(router_dw_kernel, grid, blk, 0, stream, a);
+      trace_mark(p.tr, "router_dw", stream);
+    }
+  } else {
+    if (p.T > 0) {
+      a.parts = p.want_dx || p.dw ? (bf16_t*)ws : nullptr;
+      a.dbp = (double*)(ws + pl.parts);
+      hipLaunchKernelGGL(router_split_kernel, dim3((unsigned)pl.db_parts), blk, 0, stream, a);
+      trace_mark(p.tr, "router_split", stream);
+    }
+    if (p.want_dx && p.T > 0) {
+      if (p.E <= 64) launch_dx<4, 8>(a, stream);
+      else if (p.E <= 128) launch_dx<8, 8>(a, stream);
+      else if (p.E <= 256) launch_dx<16, 8>(a, stream);
+      else launch_dx<32, 4>(a, stream);
+      trace_mark(p.tr, "router_dx", stream);
+    }
+    if (p.dw) {
+      if (a.ew == 64) launch_dw<64>(a, stream);
+      else if (a.ew == 128) launch_dw<128>(a, stream);
+      else launch_dw<256>(a, stream);
+      trace_mark(p.tr, "router_dw", stream);
+    }
+  }
+  // what is left to add up: dW over chunks, db over its partial sums
+  const bool dw_left = p.dw && a.part, db_left = p.db && (a.dbp || !f32);
+  if (dw_left || db_left) {
+    const unsigned dwb = dw_left ? (unsigned)(((size_t)p.E * p.d / 4 + kThreads - 1) / kThreads) : 0;
+    const unsigned dbb = db_left ? (unsigned)(p.E + 31) / 32 : 0;
+    hipLaunchKernelGGL(router_reduce_kernel, dim3(dwb + dbb), blk, 0, stream, a, (int)dwb);
+    trace_mark(p.tr, "router_reduce", stream);
   }
   return hipGetLastError() == hipSuccess ? MOK_OK : MOK_EDEVICE;
 }
