@@ -887,9 +887,9 @@ bool valid_type(int t) { return t == MOK_F32 || t == MOK_BF16; }
 int type_bytes(int t) { return t == MOK_F32 ? 4 : 2; }
 
 bool valid_grads(int32_t n, const mok_param* q) {
-  if (n < 0 || (n > 0 && !q)) return false;
+  if (n < 0 || n > MOK_MAX_PARAMS || (n > 0 && !q)) return false;
   for (int i = 0; i < n; ++i) {
-    if (q[i].n < 0 || !valid_type(q[i].g_type)) return false;
+    if (q[i].n < 0 || q[i].n > (int64_t)1 << 40 || !valid_type(q[i].g_type)) return false;
     if (q[i].n > 0 && (!q[i].g || !aligned(q[i].g, type_bytes(q[i].g_type)))) return false;
   }
   return true;

@@ -12,12 +12,16 @@
 //
 // Forward: a workgroup takes a slice of one group's rows.  A row is held by
 // LPR lanes (NV logits each, 16-byte loads where E and the alignment allow),
-// so a wave takes 64 / LPR rows at a time and each lane keeps the column sums
-// of its own NV experts over all its rows; counts are integer LDS atomics
-// (their order cannot change the result).  Per slice the column sums, counts,
-// row count and sum of lse^2 go to the workspace; a second kernel adds the
-// slices in order in 64 bits, a third the groups.  Backward: the same slices
-// and row layout, one pass, the row's softmax formed again from registers.
+// so a wave takes 64 / LPR rows at a time, U times over (all loads of these
+// rows before the first use: one row at a time left the kernel waiting for
+// memory, 144 us against 37 us on 131072 x 256), and each lane keeps the
+// column sums of its own NV experts over all its rows; counts are integer
+// LDS atomics (their order cannot change the result).  Per slice the column
+// sums, counts, row count and sum of lse^2 go to the workspace; a second
+// kernel adds the slices in order in 64 bits, and its last workgroup the
+// groups.  A call whose rows fit one slice ends in the first kernel.
+// Backward: the same slices and row layout, one pass, the row's softmax
+// formed again from registers.
 #include "mok_internal.h"
 #include "mok_lanes.h"
 
@@ -43,6 +47,7 @@ struct BalArgs {
   int32_t* cnt;          // [G * splits][E]
   float* zz;             // [G * splits]
   int32_t* rows;         // [G * splits]
+  int32_t* ticket;       // workgroups of the finishing kernel that are done
   double* lossp;         // [G * ceil(E / kFinCols)]
   // outputs and the backward's inputs
   int32_t* counts;
@@ -115,101 +120,48 @@ struct RowLayout {
   }
 };
 
+// Values of a lane in U rows at once, so their loads are in flight together.
+template <int NV>
+constexpr int rows_at_once() {
+  return NV >= 8 ? 2 : 4;
+}
+// Chosen slots of a row per lane (k <= 16 and k <= E).
+template <int LPR, bool VEC>
+constexpr int slots_per_lane() {
+  return !VEC || LPR >= 16 ? 1 : LPR == 8 ? 2 : 4;
+}
+
 // Softmax of a row in place (v becomes p) and its log-sum-exp; false if the
 // row does not count (masked, absent or all -inf): v is then zero.  A NaN
-// among the logits reaches p and lse.
+// among the logits reaches p and lse.  exp and log are the hardware's base-2
+// ones (1 ulp) on z - max, reciprocal of the sum likewise.
 template <int LPR, int NV>
 __device__ __forceinline__ bool row_softmax(float (&v)[NV], bool there, int lane, float* lse) {
-  float mx = -__builtin_inff();
-  bool some = false;
+  float mx = v[0];
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    some = some || !(v[i] == -__builtin_inff());
-    mx = __builtin_fmaxf(mx, v[i]);
-  }
+  for (int i = 1; i < NV; ++i) mx = __builtin_fmaxf(mx, v[i]);
   mx = group_reduce<LPR, OpMax>(mx);
-  const uint64_t vote = __ballot(there && some);
-  const uint64_t grp = LPR == 64 ? ~0ull : ((1ull << (LPR & 63)) - 1) << (lane & ~(LPR - 1));
-  const bool live = (vote & grp) != 0;
+  bool live = there;
+  if (__any(mx == -__builtin_inff())) {  // fmax passes over NaN: look for one
+    bool some = mx != -__builtin_inff();
+#pragma unroll
+    for (int i = 0; i < NV; ++i) some = some || __builtin_isnan(v[i]);
+    const uint64_t vote = __ballot(some);
+    const uint64_t grp = LPR == 64 ? ~0ull : ((1ull << (LPR & 63)) - 1) << (lane & ~(LPR - 1));
+    live = there && (vote & grp) != 0;
+  }
   float sum = 0.0f;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    v[i] = live ? expf(v[i] - mx) : 0.0f;
+    v[i] = __builtin_amdgcn_exp2f((v[i] - mx) * 1.4426950408889634f);
     sum += v[i];
   }
   sum = group_reduce<LPR, OpAdd>(sum);
-  const float inv = live ? 1.0f / sum : 0.0f;
+  const float inv = __builtin_amdgcn_rcpf(sum);
 #pragma unroll
-  for (int i = 0; i < NV; ++i) v[i] *= inv;
-  *lse = live ? mx + logf(sum) : 0.0f;
+  for (int i = 0; i < NV; ++i) v[i] = live ? v[i] * inv : 0.0f;
+  *lse = live ? __builtin_fmaf(__builtin_amdgcn_logf(sum), 0.6931471805599453f, mx) : 0.0f;
   return live;
-}
-
-template <int LPR, int NV, bool VEC>
-__global__ __launch_bounds__(kBalThreads) void balance_fwd_kernel(BalArgs a) {
-  typedef RowLayout<LPR, NV, VEC> RL;
-  __shared__ float s_sum[kBalWaves][kMaxE];
-  __shared__ int s_cnt[kMaxE];
-  __shared__ float s_zz[kBalWaves];
-  __shared__ int s_n[kBalWaves];
-  const int wg = blockIdx.x, g = wg / a.splits, s = wg % a.splits;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int l = lane & (LPR - 1), sub = lane / LPR;
-  for (int e = tid; e < a.E; e += kBalThreads) s_cnt[e] = 0;
-  __syncthreads();
-  int lo = 0, hi = 0;
-  if (!slice_rows(a, g, s, &lo, &hi)) lo = hi = 0;
-  float acc[NV];
-#pragma unroll
-  for (int i = 0; i < NV; ++i) acc[i] = 0.0f;
-  float zz = 0.0f;
-  int n = 0;
-  for (int r0 = lo + wave * RL::kRows; r0 < hi; r0 += kBalWaves * RL::kRows) {
-    const int r = r0 + sub;
-    const bool there = r < hi && (!a.mask || a.mask[r]);
-    float v[NV], lse;
-    RL::load(a.z + (size_t)r * a.E, there, l, a.E, v);
-    const bool live = row_softmax<LPR, NV>(v, there, lane, &lse);
-#pragma unroll
-    for (int i = 0; i < NV; ++i) acc[i] += v[i];
-    if (live) {
-      if (l == 0) {
-        zz = __builtin_fmaf(lse, lse, zz);
-        ++n;
-      }
-      for (int j = l; j < a.k; j += LPR) {
-        const int id = a.topk[(size_t)r * a.k + j];
-        if (id >= 0 && id < a.E) atomicAdd(&s_cnt[id], 1);
-        else latch(a.status, MOK_EROUTE);
-      }
-    }
-  }
-  // the wave's row groups, then the four waves
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-#pragma unroll
-    for (int o = LPR; o < 64; o <<= 1) acc[i] += __shfl_xor(acc[i], o, 64);
-    const int e = RL::expert(l, i);
-    if (sub == 0 && e < a.E) s_sum[wave][e] = acc[i];
-  }
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) {
-    zz += __shfl_xor(zz, o, 64);
-    n += __shfl_xor(n, o, 64);
-  }
-  if (lane == 0) {
-    s_zz[wave] = zz;
-    s_n[wave] = n;
-  }
-  __syncthreads();
-  for (int e = tid; e < a.E; e += kBalThreads) {
-    a.part[(size_t)wg * a.E + e] = (s_sum[0][e] + s_sum[1][e]) + (s_sum[2][e] + s_sum[3][e]);
-    a.cnt[(size_t)wg * a.E + e] = s_cnt[e];
-  }
-  if (tid == 0) {
-    a.zz[wg] = (s_zz[0] + s_zz[1]) + (s_zz[2] + s_zz[3]);
-    a.rows[wg] = s_n[0] + s_n[1] + s_n[2] + s_n[3];
-  }
 }
 
 // Sums of n values v[i] (i < n) over the workgroup; every thread gets it.
@@ -226,15 +178,125 @@ __device__ __forceinline__ T block_sum(int n, F value) {
   return (s_w[0] + s_w[1]) + (s_w[2] + s_w[3]);
 }
 
+// n_tok[G], n_tok[G+1] and the losses from the groups' terms.
+__device__ __forceinline__ void write_totals(const BalArgs& a, int N, int groups, double bal, double zz) {
+  a.n_tok[a.G] = N;
+  a.n_tok[a.G + 1] = groups;
+  a.loss[0] = groups > 0 ? (float)(a.alpha * bal / groups) : 0.0f;
+  a.loss[1] = N > 0 ? (float)(a.beta * zz / N) : 0.0f;
+}
+__device__ __forceinline__ double group_term(const BalArgs& a, int n, double cp) {
+  return n > 0 ? cp * a.E / ((double)a.k * n * n) : 0.0;
+}
+
+template <int LPR, int NV, bool VEC>
+__global__ __launch_bounds__(kBalThreads) void balance_fwd_kernel(BalArgs a) {
+  typedef RowLayout<LPR, NV, VEC> RL;
+  constexpr int U = rows_at_once<NV>(), KJ = slots_per_lane<LPR, VEC>();
+  __shared__ float s_sum[kBalWaves][kMaxE];
+  __shared__ int s_cnt[kMaxE];
+  __shared__ float s_zz[kBalWaves];
+  __shared__ int s_n[kBalWaves];
+  const int wg = blockIdx.x, g = wg / a.splits, s = wg % a.splits;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int l = lane & (LPR - 1), sub = lane / LPR;
+  for (int e = tid; e < a.E; e += kBalThreads) s_cnt[e] = 0;
+  __syncthreads();
+  int lo = 0, hi = 0;
+  if (!slice_rows(a, g, s, &lo, &hi)) lo = hi = 0;
+  float acc[NV];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) acc[i] = 0.0f;
+  float zz = 0.0f;
+  int n = 0;
+  for (int64_t r0 = lo + wave * RL::kRows * U; r0 < hi; r0 += kBalWaves * RL::kRows * U) {
+    float v[U][NV];
+    int id[U][KJ];
+    bool there[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t r = r0 + u * RL::kRows + sub;
+      there[u] = r < hi;
+      RL::load(a.z + (size_t)r * a.E, there[u], l, a.E, v[u]);
+#pragma unroll
+      for (int q = 0; q < KJ; ++q) {
+        const int j = l + LPR * q;
+        id[u][q] = there[u] && j < a.k ? a.topk[(size_t)r * a.k + j] : 0;
+      }
+      if (a.mask) there[u] = there[u] && a.mask[r];
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      float lse;
+      const bool live = row_softmax<LPR, NV>(v[u], there[u], lane, &lse);
+#pragma unroll
+      for (int i = 0; i < NV; ++i) acc[i] += v[u][i];
+      zz = __builtin_fmaf(lse, lse, zz);   // every lane of the row: lane 0's is used
+      n += live;
+#pragma unroll
+      for (int q = 0; q < KJ; ++q) {
+        if (!live || l + LPR * q >= a.k) continue;
+        if (id[u][q] >= 0 && id[u][q] < a.E) atomicAdd(&s_cnt[id[u][q]], 1);
+        else latch(a.status, MOK_EROUTE);
+      }
+    }
+  }
+  // the wave's row groups, then the four waves
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+#pragma unroll
+    for (int o = LPR; o < 64; o <<= 1) acc[i] += __shfl_xor(acc[i], o, 64);
+    const int e = RL::expert(l, i);
+    if (sub == 0 && e < a.E) s_sum[wave][e] = acc[i];
+  }
+#pragma unroll
+  for (int o = LPR; o < 64; o <<= 1) {
+    zz += __shfl_xor(zz, o, 64);
+    n += __shfl_xor(n, o, 64);
+  }
+  if (lane == 0) {
+    s_zz[wave] = zz;
+    s_n[wave] = n;
+  }
+  __syncthreads();
+  const int rows = s_n[0] + s_n[1] + s_n[2] + s_n[3];
+  const float zsum = (s_zz[0] + s_zz[1]) + (s_zz[2] + s_zz[3]);
+  auto column = [&](int e) { return (s_sum[0][e] + s_sum[1][e]) + (s_sum[2][e] + s_sum[3][e]); };
+  if (gridDim.x == 1) {  // the only slice: nothing is left to add up
+    const double cp = block_sum<double>(a.E, [&](int e) {
+      const double p = column(e);
+      a.counts[e] = s_cnt[e];
+      a.prob[e] = rows > 0 ? (float)(p / rows) : 0.0f;
+      return p * s_cnt[e];
+    });
+    if (tid == 0) {
+      a.n_tok[0] = rows;
+      write_totals(a, rows, rows > 0, group_term(a, rows, cp), zsum);
+    }
+    return;
+  }
+  for (int e = tid; e < a.E; e += kBalThreads) {
+    a.part[(size_t)wg * a.E + e] = column(e);
+    a.cnt[(size_t)wg * a.E + e] = s_cnt[e];
+  }
+  if (tid == 0) {
+    a.zz[wg] = zsum;
+    a.rows[wg] = rows;
+    if (wg == 0) *a.ticket = 0;   // for the kernel that follows
+  }
+}
+
 // Slices of one group, kFinCols experts: thread (c, q) adds slices q, q + 16,
-// ... of expert c; the 16 partial sums meet in LDS in order.
-__global__ __launch_bounds__(kBalThreads) void balance_group_kernel(BalArgs a) {
+// ... of expert c; the 16 partial sums meet in LDS in order.  The workgroup
+// that finishes last (a ticket per workgroup; what the others wrote is made
+// visible by their release and its acquire fence) adds the groups.
+__global__ __launch_bounds__(kBalThreads) void balance_finish_kernel(BalArgs a) {
   constexpr int Q = kBalThreads / kFinCols;
   __shared__ double s_p[Q][kFinCols];
   __shared__ int s_c[Q][kFinCols];
+  __shared__ int s_last;
   const int g = blockIdx.x, c = threadIdx.x % kFinCols, q = threadIdx.x / kFinCols;
   const int e = blockIdx.y * kFinCols + c;
-  const int n = block_sum<int>(a.splits, [&](int i) { return a.rows[(size_t)g * a.splits + i]; });
   double p = 0.0;
   int cn = 0;
   if (e < a.E) {
@@ -246,7 +308,7 @@ __global__ __launch_bounds__(kBalThreads) void balance_group_kernel(BalArgs a) {
   }
   s_p[q][c] = p;
   s_c[q][c] = cn;
-  __syncthreads();
+  const int n = block_sum<int>(a.splits, [&](int i) { return a.rows[(size_t)g * a.splits + i]; });
   if (threadIdx.x < 64) {  // wave 0; its first kFinCols lanes hold an expert each
     double term = 0.0;
     if (q == 0) {
@@ -261,29 +323,26 @@ __global__ __launch_bounds__(kBalThreads) void balance_group_kernel(BalArgs a) {
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) term += __shfl_xor(term, o, 64);
     if (threadIdx.x == 0) {
-      a.lossp[(size_t)g * gridDim.y + blockIdx.y] = n > 0 ? term * a.E / ((double)a.k * n * n) : 0.0;
+      a.lossp[(size_t)g * gridDim.y + blockIdx.y] = group_term(a, n, term);
       if (blockIdx.y == 0) a.n_tok[g] = n;
+      __threadfence();
+      s_last = atomicAdd(a.ticket, 1) == (int)(gridDim.x * gridDim.y) - 1;
     }
   }
-}
-
-// Totals over the groups: n_tok[G], n_tok[G+1] and the two losses.
-__global__ __launch_bounds__(kBalThreads) void balance_total_kernel(BalArgs a, int col_blocks) {
-  const int N = block_sum<int>(a.G, [&](int g) { return a.n_tok[g]; });
-  const int groups = block_sum<int>(a.G, [&](int g) { return a.n_tok[g] > 0 ? 1 : 0; });
-  const double bal = block_sum<double>(a.G * col_blocks, [&](int i) { return a.lossp[i]; });
+  __syncthreads();
+  if (!s_last) return;
+  __threadfence();
+  const int N = block_sum<int>(a.G, [&](int i) { return a.n_tok[i]; });
+  const int groups = block_sum<int>(a.G, [&](int i) { return a.n_tok[i] > 0 ? 1 : 0; });
+  const double bal = block_sum<double>(a.G * (int)gridDim.y, [&](int i) { return a.lossp[i]; });
   const double zz = block_sum<double>(a.G * a.splits, [&](int i) { return (double)a.zz[i]; });
-  if (threadIdx.x == 0) {
-    a.n_tok[a.G] = N;
-    a.n_tok[a.G + 1] = groups;
-    a.loss[0] = groups > 0 ? (float)(a.alpha * bal / groups) : 0.0f;
-    a.loss[1] = N > 0 ? (float)(a.beta * zz / N) : 0.0f;
-  }
+  if (threadIdx.x == 0) write_totals(a, N, groups, bal, zz);
 }
 
 template <int LPR, int NV, bool VEC>
 __global__ __launch_bounds__(kBalThreads) void balance_bwd_kernel(BalArgs a) {
   typedef RowLayout<LPR, NV, VEC> RL;
+  constexpr int U = rows_at_once<NV>();
   const int wg = blockIdx.x, g = wg / a.splits, s = wg % a.splits;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int l = lane & (LPR - 1), sub = lane / LPR;
@@ -300,19 +359,30 @@ __global__ __launch_bounds__(kBalThreads) void balance_bwd_kernel(BalArgs a) {
     const int e = RL::expert(l, i);
     w[i] = e < a.E ? cw * (float)(a.counts[(size_t)g * a.E + e] - mean) : 0.0f;
   }
-  for (int r0 = lo + wave * RL::kRows; r0 < hi; r0 += kBalWaves * RL::kRows) {
-    const int r = r0 + sub;
-    const bool there = r < hi && (!a.mask || a.mask[r]);
-    float v[NV], lse;
-    RL::load(a.z + (size_t)r * a.E, there, l, a.E, v);
-    const bool live = row_softmax<LPR, NV>(v, there, lane, &lse);
-    float dot = 0.0f;
+  for (int64_t r0 = lo + wave * RL::kRows * U; r0 < hi; r0 += kBalWaves * RL::kRows * U) {
+    float v[U][NV];
+    bool there[U];
 #pragma unroll
-    for (int i = 0; i < NV; ++i) dot = __builtin_fmaf(v[i], w[i], dot);
-    dot = group_reduce<LPR, OpAdd>(dot);
+    for (int u = 0; u < U; ++u) {
+      const int64_t r = r0 + u * RL::kRows + sub;
+      there[u] = r < hi;
+      RL::load(a.z + (size_t)r * a.E, there[u], l, a.E, v[u]);
+      if (a.mask) there[u] = there[u] && a.mask[r];
+    }
 #pragma unroll
-    for (int i = 0; i < NV; ++i) v[i] = live ? v[i] * __builtin_fmaf(cz, lse, w[i] - dot) : 0.0f;
-    if (r < hi) RL::store(a.dz + (size_t)r * a.E, l, a.E, v);
+    for (int u = 0; u < U; ++u) {
+      float lse;
+      const bool live = row_softmax<LPR, NV>(v[u], there[u], lane, &lse);
+      float dot = 0.0f;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) dot = __builtin_fmaf(v[u][i], w[i], dot);
+      dot = group_reduce<LPR, OpAdd>(dot);
+      const float c = __builtin_fmaf(cz, lse, -dot);
+#pragma unroll
+      for (int i = 0; i < NV; ++i) v[u][i] = live ? v[u][i] * (w[i] + c) : 0.0f;
+      const int64_t r = r0 + u * RL::kRows + sub;
+      if (r < hi) RL::store(a.dz + (size_t)r * a.E, l, a.E, v[u]);
+    }
   }
 }
 
@@ -339,7 +409,7 @@ Shape row_shape(int E, uintptr_t align) {
 // one step of a workgroup on average.
 int split_count(int T, int E, int G) {
   const Shape s = row_shape(E, 0);
-  const int64_t step = (int64_t)kBalWaves * (64 / s.lpr);
+  const int64_t step = (int64_t)kBalWaves * (64 / s.lpr) * (s.nv >= 8 ? rows_at_once<8>() : rows_at_once<4>());
   int64_t n = kBalWgs / G;
   const int64_t most = (T + step * G - 1) / (step * G);
   if (n > most) n = most;
@@ -388,7 +458,7 @@ void launch_shape(const Shape& s, const BalArgs& a, hipStream_t st) {
 
 size_t balance_ws_bytes(int T, int E, int G) {
   const size_t wgs = (size_t)G * split_count(T, E, G);
-  return 2 * align256(wgs * E * 4) + 2 * align256(wgs * 4) + align256((size_t)G * fin_blocks(E) * 8);
+  return 2 * align256(wgs * E * 4) + 2 * align256(wgs * 4) + align256((size_t)G * fin_blocks(E) * 8) + 256;
 }
 
 mok_status launch_balance_fwd(int T, int E, int k, int G, const mok_balance& b, const float* logits,
@@ -414,15 +484,16 @@ mok_status launch_balance_fwd(int T, int E, int k, int G, const mok_balance& b, 
   a.rows = (int32_t*)p;
   p += align256(wgs * 4);
   a.lossp = (double*)p;
+  p += align256((size_t)G * fin_blocks(E) * 8);
+  a.ticket = (int32_t*)p;
   a.counts = counts, a.prob = prob, a.n_tok = n_tok, a.loss = loss;
   a.alpha = b.alpha, a.beta = b.beta;
   launch_shape<false>(row_shape(E, (uintptr_t)logits), a, stream);
   trace_mark(tr, "balance_fwd", stream);
-  const int cols = fin_blocks(E);
-  hipLaunchKernelGGL(balance_group_kernel, dim3(G, cols), dim3(kBalThreads), 0, stream, a);
-  trace_mark(tr, "balance_group", stream);
-  hipLaunchKernelGGL(balance_total_kernel, dim3(1), dim3(kBalThreads), 0, stream, a, cols);
-  trace_mark(tr, "balance_total", stream);
+  if (wgs > 1) {
+    hipLaunchKernelGGL(balance_finish_kernel, dim3(G, fin_blocks(E)), dim3(kBalThreads), 0, stream, a);
+    trace_mark(tr, "balance_finish", stream);
+  }
   return hipGetLastError() == hipSuccess ? MOK_OK : MOK_EDEVICE;
 }
 

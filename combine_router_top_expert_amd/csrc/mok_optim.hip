@@ -1,12 +1,12 @@
 // Optimizer step over many tensors: global gradient norm with the clip
 // factor, and AdamW with moments in 32 or 8 bits.
 //
-// Tensors come as descriptors in the kernel arguments (kBatch per launch; no
-// device table to keep), cut into pieces of kPiece elements; a workgroup
-// finds its tensor by a search over the pieces' prefix sums.  A lane takes 8
-// consecutive elements at a time (32 bytes of fp32, 16 of bf16, 8 of codes);
-// four lanes hold a 32-element block of an 8-bit moment, so its largest
-// magnitude is two quad exchanges away.
+// Tensors come as descriptors in the kernel arguments (as many as fit their
+// 4 KiB per launch; no device table to keep), cut into pieces of kPiece
+// elements; a workgroup finds its tensor by a search over the pieces' prefix
+// sums.  A lane takes 8 consecutive elements at a time (32 bytes of fp32, 16
+// of bf16, 8 of codes); four lanes hold a 32-element block of an 8-bit
+// moment, so its largest magnitude is two quad exchanges away.
 #include "mok_internal.h"
 #include "mok_lanes.h"
 
@@ -18,7 +18,9 @@ constexpr int kThreads = 256;
 constexpr int kLane = 8;                       // elements per lane at a time
 constexpr int kStep = kThreads * kLane;        // elements per workgroup step
 constexpr int kPiece = 4 * kStep;              // elements per workgroup
-constexpr int kBatch = 40;                     // tensors per launch
+constexpr int kBatch = 50;                     // tensors per launch of the step
+constexpr int kNormBatch = 192;                // and of the norm
+constexpr int kNormWgs = 2048;                 // workgroups of the norm per launch at most
 
 struct Desc {
   void* p;
@@ -30,8 +32,7 @@ struct Desc {
   uint8_t* vs;
   int64_t n;
   float wd;
-  uint32_t flags;
-  uint32_t index;   // place in the caller's array: the seed of its random words
+  uint32_t tag;   // flags below, and from bit 4 on the place in the caller's array
 };
 enum : uint32_t { kPBf16 = 1, kGBf16 = 2, kEight = 4, kWide = 8 };
 
@@ -54,7 +55,20 @@ struct AdamArgs {
   int random_params;
 };
 
-__device__ __forceinline__ int find_tensor(const Batch& b, uint32_t piece) {
+struct NormDesc {
+  const void* g;
+  int64_t n;        // elements, times 4, plus kNormBf16 and kNormWide
+};
+enum : int64_t { kNormBf16 = 1, kNormWide = 2 };
+struct NormBatch {
+  NormDesc d[kNormBatch];
+  uint32_t first[kNormBatch + 1];
+  int count;
+};
+static_assert(sizeof(Batch) + sizeof(AdamArgs) <= 4096 && sizeof(NormBatch) + 64 <= 4096, "kernel arguments");
+
+template <class B>
+__device__ __forceinline__ int find_tensor(const B& b, uint32_t piece) {
   int lo = 0, hi = b.count - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
@@ -66,7 +80,7 @@ __device__ __forceinline__ int find_tensor(const Batch& b, uint32_t piece) {
 
 // 8 elements from element i of an fp32 or bf16 tensor; elements past n are 0.
 __device__ __forceinline__ void load8_f32(const float* p, int64_t i, int64_t n, bool wide, float (&v)[8]) {
-  if (wide && i + 8 <= n) {
+  if (wide && i <= n - 8) {
     const float4 a = *reinterpret_cast<const float4*>(p + i), b = *reinterpret_cast<const float4*>(p + i + 4);
     v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
   } else {
@@ -75,7 +89,7 @@ __device__ __forceinline__ void load8_f32(const float* p, int64_t i, int64_t n, 
   }
 }
 __device__ __forceinline__ void load8_bf16(const bf16_t* p, int64_t i, int64_t n, bool wide, float (&v)[8]) {
-  if (wide && i + 8 <= n) {
+  if (wide && i <= n - 8) {
     const uint4 u = ld16(p + i);
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
@@ -89,7 +103,7 @@ __device__ __forceinline__ void load8_bf16(const bf16_t* p, int64_t i, int64_t n
   }
 }
 __device__ __forceinline__ void store8_f32(float* p, int64_t i, int64_t n, bool wide, const float (&v)[8]) {
-  if (wide && i + 8 <= n) {
+  if (wide && i <= n - 8) {
     *reinterpret_cast<float4*>(p + i) = make_float4(v[0], v[1], v[2], v[3]);
     *reinterpret_cast<float4*>(p + i + 4) = make_float4(v[4], v[5], v[6], v[7]);
   } else {
@@ -99,7 +113,7 @@ __device__ __forceinline__ void store8_f32(float* p, int64_t i, int64_t n, bool 
   }
 }
 __device__ __forceinline__ void store8_u16(bf16_t* p, int64_t i, int64_t n, bool wide, const uint32_t (&w)[4]) {
-  if (wide && i + 8 <= n) {
+  if (wide && i <= n - 8) {
     st16(p + i, make_uint4(w[0], w[1], w[2], w[3]));
   } else {
 #pragma unroll
@@ -108,7 +122,7 @@ __device__ __forceinline__ void store8_u16(bf16_t* p, int64_t i, int64_t n, bool
   }
 }
 __device__ __forceinline__ void load8_u8(const uint8_t* p, int64_t i, int64_t n, bool wide, uint32_t (&w)[2]) {
-  if (wide && i + 8 <= n) {
+  if (wide && i <= n - 8) {
     const uint2 u = *reinterpret_cast<const uint2*>(p + i);
     w[0] = u.x, w[1] = u.y;
   } else {
@@ -119,7 +133,7 @@ __device__ __forceinline__ void load8_u8(const uint8_t* p, int64_t i, int64_t n,
   }
 }
 __device__ __forceinline__ void store8_u8(uint8_t* p, int64_t i, int64_t n, bool wide, const uint32_t (&w)[2]) {
-  if (wide && i + 8 <= n) {
+  if (wide && i <= n - 8) {
     *reinterpret_cast<uint2*>(p + i) = make_uint2(w[0], w[1]);
   } else {
 #pragma unroll
@@ -130,23 +144,42 @@ __device__ __forceinline__ void store8_u8(uint8_t* p, int64_t i, int64_t n, bool
 
 // ------------------------------------------------------------------ norm
 // Squares summed in 64 bits (fp32 squares would overflow from 1.8e19 on and
-// vanish below 1e-23): per lane, wave and workgroup in a fixed order, one
-// partial sum per piece.
-__global__ __launch_bounds__(kThreads) void norm_kernel(Batch b, double* part) {
+// vanish below 1e-23; conversion and fused multiply-add run under the loads):
+// per lane over the workgroup's pieces, then wave and workgroup in a fixed
+// order, one partial sum per workgroup.
+__global__ __launch_bounds__(kThreads) void norm_kernel(NormBatch b, uint32_t pieces, double* part) {
   __shared__ double s_w[kThreads / 64];
-  const int ti = find_tensor(b, blockIdx.x);
-  const Desc& d = b.d[ti];
-  const int64_t base = (int64_t)(blockIdx.x - b.first[ti]) * kPiece;
-  const bool wide = d.flags & kWide;
+  constexpr int S = kPiece / kStep;
   double s = 0.0;
-  for (int it = 0; it < kPiece / kStep; ++it) {
-    const int64_t i = base + (int64_t)it * kStep + threadIdx.x * kLane;
-    if (i >= d.n) break;
-    float g[8];
-    if (d.flags & kGBf16) load8_bf16((const bf16_t*)d.g, i, d.n, wide, g);
-    else load8_f32((const float*)d.g, i, d.n, wide, g);
+  auto add = [&](const float (&g)[8]) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) s = __builtin_fma((double)g[j], (double)g[j], s);
+  };
+  for (uint32_t pc = blockIdx.x; pc < pieces; pc += gridDim.x) {
+    const int ti = find_tensor(b, pc);
+    const void* p = b.d[ti].g;
+    const int64_t tag = b.d[ti].n, n = tag >> 2;
+    const bool bf = tag & kNormBf16, wide = tag & kNormWide;
+    const int64_t base = (int64_t)(pc - b.first[ti]) * kPiece + threadIdx.x * kLane;
+    float g[S][8];
+    if (wide && base - threadIdx.x * kLane + kPiece <= n) {   // whole pieces: every load first
+      if (bf) {
+#pragma unroll
+        for (int i = 0; i < S; ++i) load8_bf16((const bf16_t*)p, base + i * kStep, INT64_MAX, true, g[i]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < S; ++i) load8_f32((const float*)p, base + i * kStep, INT64_MAX, true, g[i]);
+      }
+#pragma unroll
+      for (int i = 0; i < S; ++i) add(g[i]);
+      continue;
+    }
+    for (int i = 0; i < S; ++i) {
+      if (base + i * kStep >= n) break;
+      if (bf) load8_bf16((const bf16_t*)p, base + i * kStep, n, wide, g[0]);
+      else load8_f32((const float*)p, base + i * kStep, n, wide, g[0]);
+      add(g[0]);
+    }
   }
 #pragma unroll
   for (int o = 1; o < 64; o <<= 1) s += __shfl_xor(s, o, 64);
@@ -191,25 +224,76 @@ __device__ __forceinline__ int block_scale(float amax) {
   return s < -127 ? -127 : (s > 127 ? 127 : s);
 }
 
-// E4M3 code of |x| 2^-s rounded up or down by 16 random bits (bits 4..19 of
-// rnd).  |x| 2^(-s-120) has the code's exponent field (bias 127 - 120 = 7),
-// so its bits from 20 on are the code, subnormals included; adding below bit
-// 20 and cutting off rounds at random.  Not finite: the NaN code.
-__device__ __forceinline__ uint32_t e4m3_random(float x, int s, uint32_t rnd) {
-  const float y = __builtin_amdgcn_ldexpf(__builtin_fabsf(x), -s - 120);
-  const uint32_t c = (__float_as_uint(y) + rnd) >> 20;
-  return __builtin_isfinite(x) ? (c < 0x7Eu ? c : 0x7Eu) : 0x7Fu;
+// fp32 bits of |x| 2^(-s-120) with random bits added below bit 20: bits 20..26
+// are the E4M3 code of |x| 2^-s rounded up or down.  |x| 2^(-s-120) has the
+// code's exponent field (bias 127 - 120 = 7), so its bits from 20 on are the
+// code rounded down, subnormals included, and what is added below carries.
+// The scale keeps finite |x| 2^-s at 448 or less, so nothing passes 0x7E.
+__device__ __forceinline__ uint32_t random_code(float x, int s, uint32_t rnd) {
+  return __float_as_uint(__builtin_amdgcn_ldexpf(__builtin_fabsf(x), -s - 120)) + rnd;
 }
 
-__device__ __forceinline__ float quad_max(float x) { return group_reduce<4, OpMax>(x); }
+// Largest of the quad's four values (as unsigned bits).
+__device__ __forceinline__ uint32_t quad_max(uint32_t x) {
+  x = max(x, (uint32_t)__builtin_amdgcn_mov_dpp((int)x, 0xB1, 0xF, 0xF, true));
+  return max(x, (uint32_t)__builtin_amdgcn_mov_dpp((int)x, 0x4E, 0xF, 0xF, true));
+}
 
+// Codes of eight values and the block's scale.  Magnitudes compare as
+// integers (NaN above infinity above every number), so one comparison finds
+// out whether a lane of the wave holds something that is not finite; only
+// then the block's maximum is taken again over finite values.  ROOT: the
+// values are square roots: no sign, above zero stays above zero, and what is
+// not finite saturates (E4M3's NaN would be a divisor too).
+template <bool ROOT>
+__device__ __forceinline__ int encode8(const float (&x)[8], const uint32_t (&rnd)[8], uint32_t (&out)[2]) {
+  uint32_t top = 0;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) top = max(top, __float_as_uint(x[j]) & 0x7FFFFFFFu);
+  constexpr uint32_t kInf = 0x7F800000u;
+  const bool odd = __any(top >= kInf);
+  if (odd) {
+    top = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const uint32_t m = __float_as_uint(x[j]) & 0x7FFFFFFFu;
+      top = max(top, m < kInf ? m : 0u);
+    }
+  }
+  const int s = block_scale(__uint_as_float(quad_max(top)));
+  uint32_t c[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    c[j] = random_code(x[j], s, rnd[j]) << 4;     // the code in bits 24..30
+    if constexpr (ROOT) c[j] = max(c[j], min(__float_as_uint(x[j]), 1u) << 24);
+  }
+  if (odd) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (!__builtin_isfinite(x[j])) c[j] = ROOT ? 0x7E000000u : 0x7F000000u;
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    if constexpr (!ROOT) c[j] = (c[j] & 0x7FFFFFFFu) | (__float_as_uint(x[j]) & 0x80000000u);
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {  // the top bytes of four words
+    const uint32_t lo = __builtin_amdgcn_perm(c[4 * h + 1], c[4 * h], 0x0C0C0703u);
+    const uint32_t up = __builtin_amdgcn_perm(c[4 * h + 3], c[4 * h + 2], 0x07030C0Cu);
+    out[h] = lo | up;
+  }
+  return s;
+}
+
+// Square root and reciprocal of the update are the hardware's (1 ulp each):
+// an error of 2^-23 of the update itself.  (The square root of a v below
+// 2^-126 is 0; eps hides it.)
 template <bool EIGHT>
 __device__ __forceinline__ void adam_step(const Desc& d, const AdamArgs& a, int64_t i, float scale, float lr,
                                           float inv_bc1, float inv_sbc2, uint64_t key) {
-  const bool wide = d.flags & kWide, pb = d.flags & kPBf16;
+  const bool wide = d.tag & kWide, pb = d.tag & kPBf16;
   float g[8], p[8], m[8], v[8];
   const int64_t n = d.n;
-  if (d.flags & kGBf16) load8_bf16((const bf16_t*)d.g, i, n, wide, g);
+  if (d.tag & kGBf16) load8_bf16((const bf16_t*)d.g, i, n, wide, g);
   else load8_f32((const float*)d.g, i, n, wide, g);
   if (d.master) load8_f32(d.master, i, n, wide, p);
   else if (pb) load8_bf16((const bf16_t*)d.p, i, n, wide, p);
@@ -237,15 +321,16 @@ __device__ __forceinline__ void adam_step(const Desc& d, const AdamArgs& a, int6
     load8_f32((const float*)d.m, i, n, wide, m);
     load8_f32((const float*)d.v, i, n, wide, v);
   }
-  const float decay = 1.0f - lr * d.wd, rate = lr * inv_bc1;
+  const float decay = 1.0f - lr * d.wd, rate = -lr * inv_bc1;
   float r[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     const float gj = g[j] * scale;
     m[j] = __builtin_fmaf(a.b1, m[j], a.c1 * gj);
     v[j] = __builtin_fmaf(a.b2, v[j], a.c2 * (gj * gj));
-    r[j] = sqrtf(v[j]);
-    p[j] = __builtin_fmaf(-rate, m[j] / __builtin_fmaf(r[j], inv_sbc2, a.eps), p[j] * decay);
+    r[j] = __builtin_amdgcn_sqrtf(v[j]);
+    const float u = m[j] * __builtin_amdgcn_rcpf(__builtin_fmaf(r[j], inv_sbc2, a.eps));
+    p[j] = __builtin_fmaf(rate, u, p[j] * decay);
   }
   uint32_t w0 = 0, w1 = 0;
   if (EIGHT || a.random_params) {
@@ -253,25 +338,13 @@ __device__ __forceinline__ void adam_step(const Desc& d, const AdamArgs& a, int6
     w0 = (uint32_t)z, w1 = (uint32_t)(z >> 32);
   }
   if constexpr (EIGHT) {
-    // finite magnitudes only: one bad element must not take its block along
-    float am = 0.0f, ar = 0.0f;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      am = __builtin_fmaxf(am, __builtin_isfinite(m[j]) ? __builtin_fabsf(m[j]) : 0.0f);
-      ar = __builtin_fmaxf(ar, __builtin_isfinite(r[j]) ? r[j] : 0.0f);
-    }
-    const int sm = block_scale(quad_max(am)), sr = block_scale(quad_max(ar));
-    uint32_t mc[2] = {0, 0}, vc[2] = {0, 0};
-    uint32_t w = w0;
+    uint32_t rm[8], rv[8], w = w0, mc[2], vc[2];
 #pragma unroll
     for (int j = 0; j < 8; ++j, w += w1) {
-      const uint32_t cm = e4m3_random(m[j], sm, (w & 0xFFFFu) << 4) | ((__float_as_uint(m[j]) >> 24) & 0x80u);
-      uint32_t cv = e4m3_random(r[j], sr, (w >> 16) << 4);
-      if (cv == 0 && r[j] > 0.0f) cv = 1;   // a divisor of zero would throw the next step
-      if (cv == 0x7Fu) cv = 0x7Eu;
-      mc[j >> 2] |= cm << (8 * (j & 3));
-      vc[j >> 2] |= cv << (8 * (j & 3));
+      rm[j] = (w & 0xFFFFu) << 4;
+      rv[j] = (w >> 16) << 4;
     }
+    const int sm = encode8<false>(m, rm, mc), sr = encode8<true>(r, rv, vc);
     store8_u8((uint8_t*)d.m, i, n, wide, mc);
     store8_u8((uint8_t*)d.v, i, n, wide, vc);
     if ((threadIdx.x & 3) == 0 && i < n) {
@@ -288,9 +361,13 @@ __device__ __forceinline__ void adam_step(const Desc& d, const AdamArgs& a, int6
     if (a.random_params && !d.master) {
       uint32_t w = w1, b[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j, w += w0) b[j] = __float_as_uint(p[j]) + (__builtin_isfinite(p[j]) ? w >> 16 : 0u);
+      for (int j = 0; j < 8; ++j, w += w0) b[j] = __float_as_uint(p[j]) + (w >> 16);
+      // infinity and NaN take no random bits: they would turn into others
 #pragma unroll
-      for (int j = 0; j < 4; ++j) o[j] = (b[2 * j] >> 16) | (b[2 * j + 1] & 0xFFFF0000u);
+      for (int j = 0; j < 8; ++j)
+        if (!__builtin_isfinite(p[j])) b[j] = __float_as_uint(p[j]) | (__builtin_isnan(p[j]) ? 0x400000u : 0u);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) o[j] = __builtin_amdgcn_perm(b[2 * j + 1], b[2 * j], 0x07060302u);
     } else {
 #pragma unroll
       for (int j = 0; j < 4; ++j) o[j] = pack2_bf16(p[2 * j], p[2 * j + 1]);
@@ -319,69 +396,69 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(Batch b, AdamArgs a) {
   const int ti = find_tensor(b, blockIdx.x);
   const Desc& d = b.d[ti];
   const int64_t base = (int64_t)(blockIdx.x - b.first[ti]) * kPiece;
-  const uint64_t key = mix64(mix64(a.seed + d.index) + (uint64_t)step * kGold);
+  const uint64_t key = mix64(mix64(a.seed + (d.tag >> 4)) + (uint64_t)step * kGold);
   for (int it = 0; it < kPiece / kStep; ++it) {
     const int64_t at = base + (int64_t)it * kStep;
     if (at >= d.n) break;
     const int64_t i = at + threadIdx.x * kLane;
-    if (d.flags & kEight) adam_step<true>(d, a, i, scale, lr, inv_bc1, inv_sbc2, key);
+    if (d.tag & kEight) adam_step<true>(d, a, i, scale, lr, inv_bc1, inv_sbc2, key);
     else adam_step<false>(d, a, i, scale, lr, inv_bc1, inv_sbc2, key);
   }
 }
 
+uint32_t norm_grid(uint32_t pieces) { return pieces < kNormWgs ? pieces : kNormWgs; }
 int64_t pieces_of(int64_t n) { return (n + kPiece - 1) / kPiece; }
 
-// Calls f(batch, pieces) for batches of at most kBatch non-empty tensors and
-// at most 2^30 pieces each; a tensor never splits over batches.
-template <class F>
-bool each_batch(int n_params, const mok_param* params, F f) {
-  Batch b = {};
+// Fills batches of at most N non-empty tensors and at most 2^30 pieces (a
+// tensor never splits over batches) and calls run(batch, pieces) for each;
+// put(descriptor, tensor, place) writes one.
+template <class B, int N, class Put, class Run>
+bool each_batch(int n_params, const mok_param* params, Put put, Run run) {
+  B b = {};
   uint64_t pieces = 0;
   for (int t = 0; t < n_params; ++t) {
-    const mok_param& q = params[t];
-    if (q.n == 0) continue;
-    const uint64_t k = (uint64_t)pieces_of(q.n);
-    if (b.count == kBatch || (b.count && pieces + k > (1u << 30))) {
-      if (!f(b, (uint32_t)pieces)) return false;
+    if (params[t].n == 0) continue;
+    const uint64_t k = (uint64_t)pieces_of(params[t].n);
+    if (b.count == N || (b.count && pieces + k > (1u << 30))) {
+      if (!run(b, (uint32_t)pieces)) return false;
       b.count = 0;
       pieces = 0;
     }
-    Desc& d = b.d[b.count];
-    d.p = q.p, d.g = q.g, d.master = q.master, d.m = q.m, d.v = q.v, d.ms = q.m_scale, d.vs = q.v_scale;
-    d.n = q.n;
-    d.wd = q.weight_decay;
-    d.index = (uint32_t)t;
-    const uintptr_t all = (uintptr_t)q.p | (uintptr_t)q.g | (uintptr_t)q.master | (uintptr_t)q.m | (uintptr_t)q.v;
-    d.flags = (q.p_type == MOK_BF16 ? kPBf16 : 0) | (q.g_type == MOK_BF16 ? kGBf16 : 0) |
-              (q.state_bits == 8 ? kEight : 0) | (all % 16 == 0 ? kWide : 0);
+    put(b.d[b.count], params[t], t);
     b.first[b.count] = (uint32_t)pieces;
     pieces += k;
     b.first[++b.count] = (uint32_t)pieces;
   }
-  return b.count == 0 || f(b, (uint32_t)pieces);
+  return b.count == 0 || run(b, (uint32_t)pieces);
 }
 
 }  // namespace
 
 size_t grad_norm_ws_bytes(int n_params, const mok_param* params) {
-  uint64_t pieces = 0;
-  for (int t = 0; t < n_params; ++t) pieces += (uint64_t)pieces_of(params[t].n);
-  return (size_t)(pieces + 1) * sizeof(double);
+  size_t parts = 1;
+  each_batch<NormBatch, kNormBatch>(n_params, params, [](NormDesc&, const mok_param&, int) {},
+                                    [&](const NormBatch&, uint32_t pieces) {
+                                      parts += norm_grid(pieces);
+                                      return true;
+                                    });
+  return parts * sizeof(double);
 }
 
 mok_status launch_grad_norm(int n_params, const mok_param* params, float max_norm, float* out, void* ws,
                             hipStream_t stream) {
   double* part = (double*)ws;
   int64_t done = 0;
-  // only the gradients are read: their alignment alone decides the width
-  auto run = [&](Batch& b, uint32_t pieces) {
-    for (int i = 0; i < b.count; ++i)
-      b.d[i].flags = (b.d[i].flags & ~(uint32_t)kWide) | ((uintptr_t)b.d[i].g % 16 == 0 ? kWide : 0);
-    hipLaunchKernelGGL(norm_kernel, dim3(pieces), dim3(kThreads), 0, stream, b, part + done);
-    done += pieces;
+  auto put = [](NormDesc& d, const mok_param& q, int) {
+    d.g = q.g;
+    d.n = q.n * 4 + (q.g_type == MOK_BF16 ? kNormBf16 : 0) + ((uintptr_t)q.g % 16 == 0 ? kNormWide : 0);
+  };
+  auto run = [&](const NormBatch& b, uint32_t pieces) {
+    const uint32_t grid = norm_grid(pieces);
+    hipLaunchKernelGGL(norm_kernel, dim3(grid), dim3(kThreads), 0, stream, b, pieces, part + done);
+    done += grid;
     return hipGetLastError() == hipSuccess;
   };
-  if (!each_batch(n_params, params, run)) return MOK_EDEVICE;
+  if (!each_batch<NormBatch, kNormBatch>(n_params, params, put, run)) return MOK_EDEVICE;
   hipLaunchKernelGGL(norm_total_kernel, dim3(1), dim3(1024), 0, stream, part, done, max_norm, out);
   return hipGetLastError() == hipSuccess ? MOK_OK : MOK_EDEVICE;
 }
@@ -400,11 +477,19 @@ mok_status launch_adamw(int n_params, const mok_param* params, const mok_adamw_a
   a.seed = h.seed;
   a.dev_scale = h.dev_scale, a.dev_lr = h.dev_lr, a.dev_step = h.dev_step;
   a.random_params = h.random_params;
-  auto run = [&](Batch& b, uint32_t pieces) {
+  auto put = [](Desc& d, const mok_param& q, int t) {
+    d.p = q.p, d.g = q.g, d.master = q.master, d.m = q.m, d.v = q.v, d.ms = q.m_scale, d.vs = q.v_scale;
+    d.n = q.n;
+    d.wd = q.weight_decay;
+    const uintptr_t all = (uintptr_t)q.p | (uintptr_t)q.g | (uintptr_t)q.master | (uintptr_t)q.m | (uintptr_t)q.v;
+    d.tag = (uint32_t)t << 4 | (q.p_type == MOK_BF16 ? kPBf16 : 0) | (q.g_type == MOK_BF16 ? kGBf16 : 0) |
+            (q.state_bits == 8 ? kEight : 0) | (all % 16 == 0 ? kWide : 0);
+  };
+  auto run = [&](const Batch& b, uint32_t pieces) {
     hipLaunchKernelGGL(adamw_kernel, dim3(pieces), dim3(kThreads), 0, stream, b, a);
     return hipGetLastError() == hipSuccess;
   };
-  return each_batch(n_params, params, run) ? MOK_OK : MOK_EDEVICE;
+  return each_batch<Batch, kBatch>(n_params, params, put, run) ? MOK_OK : MOK_EDEVICE;
 }
 
 }  // namespace mok

@@ -68,6 +68,7 @@ extern "C" {
 
 #define MOK_MAX_SOURCES 64
 #define MOK_MX_BLOCK 32
+#define MOK_MAX_PARAMS (1 << 20)  /* tensors of one optimizer call */
 #define MOK_MAX_CALLS 8     /* layer calls (macrobatches) of one mok_layer_fwd_macro */
 
 typedef enum {
@@ -460,7 +461,7 @@ mok_status mok_router_bwd(const mok_config* cfg, int32_t own_lo, int32_t own_n,
                           void* const* d_x, float* dw_router, float* d_bias, int32_t accumulate,
                           void* ws, void* stream);
 
-/* One tensor of an optimizer step: n contiguous elements (any n >= 0, any
+/* One tensor of an optimizer step: n contiguous elements (0..2^40, any
  * element alignment; 16-byte aligned pointers are faster).  Types are
  * MOK_F32 or MOK_BF16.  master: fp32 values behind a bf16 p (p is then
  * written as master rounded to nearest), or NULL.  Moments: state_bits 32:

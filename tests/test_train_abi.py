@@ -115,7 +115,7 @@ def _adamw(L, params, **kw):
     return L.mok_adamw(len(params), arr, ctypes.byref(a), None)
 
 
-BAD_PARAMS = [dict(n=-1), dict(p=None), dict(g=None), dict(m=None), dict(v=None), dict(p=18),
+BAD_PARAMS = [dict(n=-1), dict(n=(1 << 40) + 1), dict(p=None), dict(g=None), dict(m=None), dict(v=None), dict(p=18),
               dict(g=18), dict(m=18), dict(v=18), dict(p_type=2), dict(g_type=7),
               dict(state_bits=16), dict(state_bits=8), dict(state_bits=8, m_scale=16),
               dict(state_bits=8, v_scale=16), dict(master=16),
