@@ -876,8 +876,9 @@ int balance_groups(const mok_balance* b) { return b->G > 0 ? b->G : 1; }
 bool valid_balance(const mok_config* cfg, int32_t T, const mok_balance* b) {
   if (!valid_cfg(cfg) || T < 0 || !b || b->G < 0) return false;
   if (b->G > 0 && !b->group_offsets) return false;
-  // counts are int32, group rows of the outputs are indexed by int32
-  if ((int64_t)T * cfg->k > 0x7FFFFFFF || (int64_t)b->G * cfg->E > 0x7FFFFFFF) return false;
+  // counts are int32, group rows of the outputs are indexed by int32; row
+  // numbers stay clear of int32's end by a workgroup's step
+  if (T > 1 << 30 || (int64_t)T * cfg->k > 0x7FFFFFFF || (int64_t)b->G * cfg->E > 0x7FFFFFFF) return false;
   return true;
 }
 

@@ -10,17 +10,20 @@
 // (p sums to one); with the mean count taken off, nearly balanced counts do
 // not leave a small difference of large numbers.
 //
-// Forward: a workgroup takes a slice of one group's rows.  A row is held by
-// LPR lanes (NV logits each, 16-byte loads where E and the alignment allow),
-// so a wave takes 64 / LPR rows at a time, U times over (all loads of these
-// rows before the first use: one row at a time left the kernel waiting for
-// memory, 144 us against 37 us on 131072 x 256), and each lane keeps the
-// column sums of its own NV experts over all its rows; counts are integer
-// LDS atomics (their order cannot change the result).  Per slice the column
-// sums, counts, row count and sum of lse^2 go to the workspace; a second
-// kernel adds the slices in order in 64 bits, and its last workgroup the
-// groups.  A call whose rows fit one slice ends in the first kernel.
-// Backward: the same slices and row layout, one pass, the row's softmax
+// Forward: a workgroup takes a chunk of consecutive rows, whatever groups they
+// belong to, so ragged groups load the chip evenly (a fixed number of slices
+// per group took 60 us instead of FWDUS on 131072 x 256 in 32 random groups).  A
+// row is held by LPR lanes (NV logits each, 16-byte loads where E and the
+// alignment allow), so a wave takes 64 / LPR rows at a time, U times over,
+// with the next rows' loads issued before this step's arithmetic, and each
+// lane keeps the column sums of its own NV experts over the rows of a group;
+// counts are integer LDS atomics (their order cannot change the result).
+// For every group that a chunk meets, the column sums, counts, row count and
+// sum of lse^2 go to a slot of the workspace: chunk + group, which no two
+// (chunk, group) pairs that meet share, because both only ascend.  A second
+// kernel adds each group's slots in order in 64 bits, and its last workgroup
+// the groups.  A call of one group and chunk ends in the first kernel.
+// Backward: the same chunks and row layout, one pass, the row's softmax
 // formed again from registers.
 #include "mok_internal.h"
 #include "mok_lanes.h"
@@ -31,24 +34,27 @@ namespace {
 
 constexpr int kBalThreads = 256;
 constexpr int kBalWaves = kBalThreads / 64;
-constexpr int kBalWgs = 1024;   // slices aimed at: four workgroups per CU
+constexpr int kBalWgs = 1024;   // chunks at most: four workgroups per CU
 constexpr int kMaxE = 512;
-constexpr int kFinCols = 16;    // experts per workgroup of the finishing kernel
+constexpr int kFinCols = 64;    // experts per workgroup of the finishing kernel
+constexpr int kFinThreads = 512;
 
 struct BalArgs {
   const float* z;
   const int32_t* topk;
   const uint8_t* mask;
   const int32_t* off;    // [G+1] or null: one group of T rows
-  int T, E, k, G, splits;
+  int T, E, k, G;
+  int chunks, rows;      // chunks of `rows` rows
   int32_t* status;
-  // workspace of the forward
-  float* part;           // [G * splits][E] column sums
-  int32_t* cnt;          // [G * splits][E]
-  float* zz;             // [G * splits]
-  int32_t* rows;         // [G * splits]
+  // workspace of the forward; slots = chunks + G
+  float* part;           // [slots][E] column sums
+  int32_t* cnt;          // [slots][E]
+  float* zz;             // [slots]
+  int32_t* nrow;         // [slots]
   int32_t* ticket;       // workgroups of the finishing kernel that are done
   double* lossp;         // [G * ceil(E / kFinCols)]
+  double* zzp;           // [G]
   // outputs and the backward's inputs
   int32_t* counts;
   float* prob;
@@ -59,22 +65,49 @@ struct BalArgs {
   float alpha, beta;
 };
 
-// Rows [lo, hi) of slice s of group g; false (and MOK_EGROUP latched) if the
-// group's offsets do not ascend within [0, T].
-__device__ __forceinline__ bool slice_rows(const BalArgs& a, int g, int s, int* lo, int* hi) {
-  int b = 0, e = a.T;
-  if (a.off) {
-    b = a.off[g];
-    e = a.off[g + 1];
-    if (b < 0 || e < b || e > a.T) {
-      if (threadIdx.x == 0) latch(a.status, MOK_EGROUP);
-      return false;
-    }
+// Sum of every thread's x over the workgroup, in a fixed order; every thread
+// gets it.
+template <class T, int THREADS>
+__device__ __forceinline__ T block_sum(T x) {
+  __shared__ T s_w[THREADS / 64];
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) x += __shfl_xor(x, o, 64);
+  __syncthreads();
+  if ((threadIdx.x & 63) == 0) s_w[threadIdx.x >> 6] = x;
+  __syncthreads();
+  x = 0;
+#pragma unroll
+  for (int i = 0; i < THREADS / 64; ++i) x += s_w[i];
+  return x;
+}
+// Sum of value(i) for i in [0, n).
+template <class T, int THREADS, class F>
+__device__ __forceinline__ T block_sum(int n, F value) {
+  T x = 0;
+  for (int i = threadIdx.x; i < n; i += THREADS) x += value(i);
+  return block_sum<T, THREADS>(x);
+}
+
+__device__ __forceinline__ int group_begin(const BalArgs& a, int g) { return a.off ? a.off[g] : g == 0 ? 0 : a.T; }
+
+// The first group that ends behind `row`, or -1 (MOK_EGROUP latched) if the
+// offsets do not ascend within [0, T].  Every workgroup reads them all, so
+// every one comes to the same answer.
+template <int THREADS>
+__device__ __forceinline__ int first_group(const BalArgs& a, int row) {
+  if (!a.off) return 0;
+  int before = 0;
+  bool bad = false;
+  for (int g = threadIdx.x; g < a.G; g += THREADS) {
+    const int b = a.off[g], e = a.off[g + 1];
+    bad = bad || b < 0 || e < b || e > a.T;
+    before += e <= row;
   }
-  const int64_t n = e - b;
-  *lo = b + (int)(n * s / a.splits);
-  *hi = b + (int)(n * (s + 1) / a.splits);
-  return true;
+  if (__syncthreads_or(bad)) {
+    if (threadIdx.x == 0) latch(a.status, MOK_EGROUP);
+    return -1;
+  }
+  return block_sum<int, THREADS>(before);
 }
 
 // The row layout: lane l of LPR holds experts 4 (l + LPR u) + 0..3 (VEC) or
@@ -85,21 +118,33 @@ struct RowLayout {
   __device__ __forceinline__ static int expert(int l, int i) {
     return VEC ? 4 * (l + LPR * (i >> 2)) + (i & 3) : l + LPR * i;
   }
-  // logits of a row; -inf past E (and for a row that is not there)
-  __device__ __forceinline__ static void load(const float* row, bool there, int l, int E, float (&v)[NV]) {
+  // logits of U rows; -inf past E
+  template <int U>
+  __device__ __forceinline__ static void load(const float* const (&row)[U], int l, int E, float (&v)[U][NV]) {
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int i = 0; i < NV; ++i) v[u][i] = -__builtin_inff();
     if constexpr (VEC) {
 #pragma unroll
-      for (int u = 0; u < NV / 4; ++u) {
-        const int e = 4 * (l + LPR * u);
-        float4 q = make_float4(-__builtin_inff(), -__builtin_inff(), -__builtin_inff(), -__builtin_inff());
-        if (there && e < E) q = *reinterpret_cast<const float4*>(row + e);
-        v[4 * u] = q.x, v[4 * u + 1] = q.y, v[4 * u + 2] = q.z, v[4 * u + 3] = q.w;
+      for (int i = 0; i < NV / 4; ++i) {
+        const int e = 4 * (l + LPR * i);
+        if (e < E) {
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            const float4 q = *reinterpret_cast<const float4*>(row[u] + e);
+            v[u][4 * i] = q.x, v[u][4 * i + 1] = q.y, v[u][4 * i + 2] = q.z, v[u][4 * i + 3] = q.w;
+          }
+        }
       }
     } else {
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         const int e = l + LPR * i;
-        v[i] = there && e < E ? row[e] : -__builtin_inff();
+        if (e < E) {
+#pragma unroll
+          for (int u = 0; u < U; ++u) v[u][i] = row[u][e];
+        }
       }
     }
   }
@@ -131,51 +176,88 @@ constexpr int slots_per_lane() {
   return !VEC || LPR >= 16 ? 1 : LPR == 8 ? 2 : 4;
 }
 
-// Softmax of a row in place (v becomes p) and its log-sum-exp; false if the
-// row does not count (masked, absent or all -inf): v is then zero.  A NaN
-// among the logits reaches p and lse.  exp and log are the hardware's base-2
-// ones (1 ulp) on z - max, reciprocal of the sum likewise.
-template <int LPR, int NV>
-__device__ __forceinline__ bool row_softmax(float (&v)[NV], bool there, int lane, float* lse) {
-  float mx = v[0];
+// U rows of a wave on their way: logits, mask bytes and whether each row is
+// one of the slice (a row past its end reads the last row instead).
+template <int LPR, int NV, bool VEC>
+struct Rows {
+  static constexpr int U = rows_at_once<NV>();
+  float v[U][NV];
+  uint32_t mask[U];
+  bool in[U];
+  __device__ __forceinline__ void load(const BalArgs& a, int r0, int hi, int l, int sub) {
+    const float* row[U];
 #pragma unroll
-  for (int i = 1; i < NV; ++i) mx = __builtin_fmaxf(mx, v[i]);
-  mx = group_reduce<LPR, OpMax>(mx);
-  bool live = there;
-  if (__any(mx == -__builtin_inff())) {  // fmax passes over NaN: look for one
-    bool some = mx != -__builtin_inff();
+    for (int u = 0; u < U; ++u) {
+      const int r = r0 + u * (64 / LPR) + sub;
+      in[u] = r < hi;
+      row[u] = a.z + (size_t)min(r, hi - 1) * a.E;
+      mask[u] = 1;
+    }
+    RowLayout<LPR, NV, VEC>::load(row, l, a.E, v);
+    if (a.mask) {
 #pragma unroll
-    for (int i = 0; i < NV; ++i) some = some || __builtin_isnan(v[i]);
-    const uint64_t vote = __ballot(some);
-    const uint64_t grp = LPR == 64 ? ~0ull : ((1ull << (LPR & 63)) - 1) << (lane & ~(LPR - 1));
-    live = there && (vote & grp) != 0;
+      for (int u = 0; u < U; ++u) mask[u] = a.mask[min(r0 + u * (64 / LPR) + sub, hi - 1)];
+    }
   }
-  float sum = 0.0f;
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    v[i] = __builtin_amdgcn_exp2f((v[i] - mx) * 1.4426950408889634f);
-    sum += v[i];
-  }
-  sum = group_reduce<LPR, OpAdd>(sum);
-  const float inv = __builtin_amdgcn_rcpf(sum);
-#pragma unroll
-  for (int i = 0; i < NV; ++i) v[i] = live ? v[i] * inv : 0.0f;
-  *lse = live ? __builtin_fmaf(__builtin_amdgcn_logf(sum), 0.6931471805599453f, mx) : 0.0f;
-  return live;
-}
+};
 
-// Sums of n values v[i] (i < n) over the workgroup; every thread gets it.
-template <class T, class F>
-__device__ __forceinline__ T block_sum(int n, F value) {
-  __shared__ T s_w[kBalWaves];
-  T x = 0;
-  for (int i = threadIdx.x; i < n; i += kBalThreads) x += value(i);
+// Softmax of U rows in place (v becomes p) and their log-sum-exp.  live: the
+// row counts (in the slice, not masked, not all -inf); v and lse are zero
+// where not.  A NaN among the logits of a live row reaches p and lse.
+// p = 2^(z log2 e - c) / sum with c = max log2 e: c's rounding is the same
+// factor in every term and in lse = (c + log2 sum) ln 2, so only the product
+// with z rounds (one fused operation); exponential, logarithm and reciprocal
+// are the hardware's (1 ulp).  Rows that do not count are rare enough to be
+// dealt with in a branch.  Returns whether there was one in the wave.
+template <int LPR, int NV, int U>
+__device__ __forceinline__ bool softmax_rows(float (&v)[U][NV], const uint32_t (&mask)[U], const bool (&in)[U],
+                                             int lane, bool (&live)[U], float (&lse)[U]) {
+  constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+  float c[U];
+  bool rare = false;
 #pragma unroll
-  for (int o = 1; o < 64; o <<= 1) x += __shfl_xor(x, o, 64);
-  __syncthreads();
-  if ((threadIdx.x & 63) == 0) s_w[threadIdx.x >> 6] = x;
-  __syncthreads();
-  return (s_w[0] + s_w[1]) + (s_w[2] + s_w[3]);
+  for (int u = 0; u < U; ++u) {
+    int mx = float_order(v[u][0]);
+#pragma unroll
+    for (int i = 1; i < NV; ++i) mx = max(mx, float_order(v[u][i]));
+    const float m = order_float(group_max<LPR>(mx));
+    c[u] = m * kLog2e;
+    live[u] = true;
+    rare = rare || !in[u] || mask[u] == 0 || m == -__builtin_inff();
+  }
+  rare = __any(rare);
+  if (rare) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      // all -inf, or -inf and negative NaN only: look for one
+      bool some = c[u] != -__builtin_inff();
+#pragma unroll
+      for (int i = 0; i < NV; ++i) some = some || __builtin_isnan(v[u][i]);
+      const uint64_t vote = __ballot(some);
+      const uint64_t grp = LPR == 64 ? ~0ull : ((1ull << (LPR & 63)) - 1) << (lane & ~(LPR - 1));
+      live[u] = in[u] && mask[u] != 0 && (vote & grp) != 0;
+      if (!live[u]) {
+        c[u] = 0.0f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) v[u][i] = -__builtin_inff();
+      }
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    float sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      v[u][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(v[u][i], kLog2e, -c[u]));
+      sum += v[u][i];
+    }
+    sum = group_sum<LPR>(sum);
+    const float inv = live[u] ? __builtin_amdgcn_rcpf(sum) : 0.0f;
+    lse[u] = live[u] ? (c[u] + __builtin_amdgcn_logf(sum)) * kLn2 : 0.0f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) v[u][i] *= inv;
+  }
+  return rare;
 }
 
 // n_tok[G], n_tok[G+1] and the losses from the groups' terms.
@@ -197,145 +279,196 @@ __global__ __launch_bounds__(kBalThreads) void balance_fwd_kernel(BalArgs a) {
   __shared__ int s_cnt[kMaxE];
   __shared__ float s_zz[kBalWaves];
   __shared__ int s_n[kBalWaves];
-  const int wg = blockIdx.x, g = wg / a.splits, s = wg % a.splits;
+  const int chunk = blockIdx.x;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int l = lane & (LPR - 1), sub = lane / LPR;
-  for (int e = tid; e < a.E; e += kBalThreads) s_cnt[e] = 0;
-  __syncthreads();
-  int lo = 0, hi = 0;
-  if (!slice_rows(a, g, s, &lo, &hi)) lo = hi = 0;
-  float acc[NV];
+  const int c_lo = chunk * a.rows, c_hi = min(a.T, c_lo + a.rows);
+  const int step = kBalWaves * RL::kRows * U;
+  if (chunk == 0 && tid == 0) *a.ticket = 0;   // for the kernel that follows
+  const int g0 = first_group<kBalThreads>(a, c_lo);
+  bool bad = false;
+  auto load = [&](int r0, int hi, Rows<LPR, NV, VEC>& rows, int (&ids)[U][KJ]) {
 #pragma unroll
-  for (int i = 0; i < NV; ++i) acc[i] = 0.0f;
-  float zz = 0.0f;
-  int n = 0;
-  for (int64_t r0 = lo + wave * RL::kRows * U; r0 < hi; r0 += kBalWaves * RL::kRows * U) {
-    float v[U][NV];
-    int id[U][KJ];
-    bool there[U];
+    for (int q = 0; q < KJ; ++q) {
+      const int j = l + LPR * q;
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int64_t r = r0 + u * RL::kRows + sub;
-      there[u] = r < hi;
-      RL::load(a.z + (size_t)r * a.E, there[u], l, a.E, v[u]);
+      for (int u = 0; u < U; ++u) ids[u][q] = 0;
+      if (j < a.k) {
 #pragma unroll
-      for (int q = 0; q < KJ; ++q) {
-        const int j = l + LPR * q;
-        id[u][q] = there[u] && j < a.k ? a.topk[(size_t)r * a.k + j] : 0;
-      }
-      if (a.mask) there[u] = there[u] && a.mask[r];
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      float lse;
-      const bool live = row_softmax<LPR, NV>(v[u], there[u], lane, &lse);
-#pragma unroll
-      for (int i = 0; i < NV; ++i) acc[i] += v[u][i];
-      zz = __builtin_fmaf(lse, lse, zz);   // every lane of the row: lane 0's is used
-      n += live;
-#pragma unroll
-      for (int q = 0; q < KJ; ++q) {
-        if (!live || l + LPR * q >= a.k) continue;
-        if (id[u][q] >= 0 && id[u][q] < a.E) atomicAdd(&s_cnt[id[u][q]], 1);
-        else latch(a.status, MOK_EROUTE);
+        for (int u = 0; u < U; ++u) ids[u][q] = a.topk[(size_t)min(r0 + u * RL::kRows + sub, hi - 1) * a.k + j];
       }
     }
-  }
-  // the wave's row groups, then the four waves
+    rows.load(a, r0, hi, l, sub);
+  };
+  // (a lone chunk and group also writes its zeros when nothing counts)
+  const bool lone = gridDim.x == 1 && a.G == 1;
+  for (int g = lone ? 0 : g0; g < a.G && (g0 >= 0 || lone); ++g) {
+    const int g_lo = g0 < 0 ? 0 : group_begin(a, g), g_hi = g0 < 0 ? 0 : group_begin(a, g + 1);
+    if (g_lo >= c_hi && !lone) break;
+    const int lo = max(g_lo, c_lo), hi = min(g_hi, c_hi);
+    if (lo >= hi && !lone) continue;
+    for (int e = tid; e < a.E; e += kBalThreads) s_cnt[e] = 0;
+    __syncthreads();
+    float acc[NV];
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
+    for (int i = 0; i < NV; ++i) acc[i] = 0.0f;
+    float zz = 0.0f;
+    int n = 0;
+    Rows<LPR, NV, VEC> now, next;
+    int id[U][KJ], id_next[U][KJ];
+    int r0 = lo + wave * RL::kRows * U;
+    if (r0 < hi) load(r0, hi, now, id);
+    while (r0 < hi) {
+      // the next rows' loads go out before this step's arithmetic
+      const bool more = hi - r0 > step;
+      if (more) load(r0 + step, hi, next, id_next);
+      bool live[U];
+      float lse[U];
+      softmax_rows<LPR, NV, U>(now.v, now.mask, now.in, lane, live, lse);
 #pragma unroll
-    for (int o = LPR; o < 64; o <<= 1) acc[i] += __shfl_xor(acc[i], o, 64);
-    const int e = RL::expert(l, i);
-    if (sub == 0 && e < a.E) s_sum[wave][e] = acc[i];
-  }
+      for (int u = 0; u < U; ++u) {
 #pragma unroll
-  for (int o = LPR; o < 64; o <<= 1) {
-    zz += __shfl_xor(zz, o, 64);
-    n += __shfl_xor(n, o, 64);
-  }
-  if (lane == 0) {
-    s_zz[wave] = zz;
-    s_n[wave] = n;
-  }
-  __syncthreads();
-  const int rows = s_n[0] + s_n[1] + s_n[2] + s_n[3];
-  const float zsum = (s_zz[0] + s_zz[1]) + (s_zz[2] + s_zz[3]);
-  auto column = [&](int e) { return (s_sum[0][e] + s_sum[1][e]) + (s_sum[2][e] + s_sum[3][e]); };
-  if (gridDim.x == 1) {  // the only slice: nothing is left to add up
-    const double cp = block_sum<double>(a.E, [&](int e) {
-      const double p = column(e);
-      a.counts[e] = s_cnt[e];
-      a.prob[e] = rows > 0 ? (float)(p / rows) : 0.0f;
-      return p * s_cnt[e];
-    });
+        for (int i = 0; i < NV; ++i) acc[i] += now.v[u][i];
+        zz = __builtin_fmaf(lse[u], lse[u], zz);   // every lane of the row: lane 0's is used
+        n += live[u];
+      }
+#pragma unroll
+      for (int q = 0; q < KJ; ++q)
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const bool slot = live[u] && l + LPR * q < a.k;
+          const bool known = (uint32_t)id[u][q] < (uint32_t)a.E;
+          if (slot && known) atomicAdd(&s_cnt[id[u][q]], 1);
+          bad = bad || (slot && !known);
+        }
+      if (!more) break;
+      r0 += step;
+      now = next;
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int q = 0; q < KJ; ++q) id[u][q] = id_next[u][q];
+    }
+    // the wave's row groups, then the four waves
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+#pragma unroll
+      for (int o = LPR; o < 64; o <<= 1) acc[i] += __shfl_xor(acc[i], o, 64);
+      const int e = RL::expert(l, i);
+      if (sub == 0 && e < a.E) s_sum[wave][e] = acc[i];
+    }
+#pragma unroll
+    for (int o = LPR; o < 64; o <<= 1) {
+      zz += __shfl_xor(zz, o, 64);
+      n += __shfl_xor(n, o, 64);
+    }
+    if (lane == 0) {
+      s_zz[wave] = zz;
+      s_n[wave] = n;
+    }
+    __syncthreads();
+    const int rows = s_n[0] + s_n[1] + s_n[2] + s_n[3];
+    const float zsum = (s_zz[0] + s_zz[1]) + (s_zz[2] + s_zz[3]);
+    auto column = [&](int e) { return (s_sum[0][e] + s_sum[1][e]) + (s_sum[2][e] + s_sum[3][e]); };
+    if (lone) {  // nothing is left to add up
+      const double cp = block_sum<double, kBalThreads>(a.E, [&](int e) {
+        const double p = column(e);
+        a.counts[e] = s_cnt[e];
+        a.prob[e] = rows > 0 ? (float)(p / rows) : 0.0f;
+        return p * s_cnt[e];
+      });
+      if (tid == 0) {
+        a.n_tok[0] = rows;
+        write_totals(a, rows, rows > 0, group_term(a, rows, cp), zsum);
+      }
+      break;
+    }
+    const size_t slot = (size_t)chunk + g;
+    for (int e = tid; e < a.E; e += kBalThreads) {
+      a.part[slot * a.E + e] = column(e);
+      a.cnt[slot * a.E + e] = s_cnt[e];
+    }
     if (tid == 0) {
-      a.n_tok[0] = rows;
-      write_totals(a, rows, rows > 0, group_term(a, rows, cp), zsum);
+      a.zz[slot] = zsum;
+      a.nrow[slot] = rows;
     }
-    return;
+    __syncthreads();   // the sums are read before the next group's begin
   }
-  for (int e = tid; e < a.E; e += kBalThreads) {
-    a.part[(size_t)wg * a.E + e] = column(e);
-    a.cnt[(size_t)wg * a.E + e] = s_cnt[e];
-  }
-  if (tid == 0) {
-    a.zz[wg] = zsum;
-    a.rows[wg] = rows;
-    if (wg == 0) *a.ticket = 0;   // for the kernel that follows
-  }
+  if (bad) latch(a.status, MOK_EROUTE);
 }
 
-// Slices of one group, kFinCols experts: thread (c, q) adds slices q, q + 16,
-// ... of expert c; the 16 partial sums meet in LDS in order.  The workgroup
-// that finishes last (a ticket per workgroup; what the others wrote is made
-// visible by their release and its acquire fence) adds the groups.
-__global__ __launch_bounds__(kBalThreads) void balance_finish_kernel(BalArgs a) {
-  constexpr int Q = kBalThreads / kFinCols;
-  __shared__ double s_p[Q][kFinCols];
-  __shared__ int s_c[Q][kFinCols];
+// Slots of one group, kFinCols experts: thread (c, q) adds slots q, q + Q,
+// ... of experts 4 c .. 4 c + 3; the Q partial sums meet in LDS in order.
+// The workgroup that finishes last (a ticket per workgroup) adds the groups.
+// What it reads of the others -- terms and row counts -- is written and read
+// with device-scope atomics, which pass by the XCDs' separate L2s, and every
+// write has completed (vmcnt 0) before its workgroup takes a ticket; a fence
+// would write back the whole L2 once per workgroup (17 us against 6 us for
+// 512 workgroups).
+__global__ __launch_bounds__(kFinThreads) void balance_finish_kernel(BalArgs a) {
+  constexpr int C = kFinCols / 4, Q = kFinThreads / C;
+  __shared__ double s_p[Q][kFinCols + 1];
+  __shared__ int s_c[Q][kFinCols + 1];
+  __shared__ double s_term[kFinCols];
   __shared__ int s_last;
-  const int g = blockIdx.x, c = threadIdx.x % kFinCols, q = threadIdx.x / kFinCols;
-  const int e = blockIdx.y * kFinCols + c;
-  double p = 0.0;
-  int cn = 0;
-  if (e < a.E) {
-    for (int s = q; s < a.splits; s += Q) {
-      const size_t i = ((size_t)g * a.splits + s) * a.E + e;
-      p += (double)a.part[i];
-      cn += a.cnt[i];
+  const int g = blockIdx.x, c = threadIdx.x % C, q = threadIdx.x / C;
+  const int e0 = blockIdx.y * kFinCols;
+  // the chunks that meet the group; none if it is empty or the offsets are bad
+  const bool ok = first_group<kFinThreads>(a, 0) >= 0;
+  const int g_lo = ok ? group_begin(a, g) : 0, g_hi = ok ? group_begin(a, g + 1) : 0;
+  const int first = g_lo / a.rows, slots = g_hi > g_lo ? (g_hi - 1) / a.rows - first + 1 : 0;
+  const size_t s0 = (size_t)first + g;
+  double p[4] = {0.0, 0.0, 0.0, 0.0};
+  int cn[4] = {0, 0, 0, 0};
+  for (int s = q; s < slots; s += Q) {
+    const size_t i = (s0 + s) * a.E + e0 + 4 * c;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (e0 + 4 * c + j >= a.E) break;
+      p[j] += (double)a.part[i + j];
+      cn[j] += a.cnt[i + j];
     }
   }
-  s_p[q][c] = p;
-  s_c[q][c] = cn;
-  const int n = block_sum<int>(a.splits, [&](int i) { return a.rows[(size_t)g * a.splits + i]; });
-  if (threadIdx.x < 64) {  // wave 0; its first kFinCols lanes hold an expert each
-    double term = 0.0;
-    if (q == 0) {
-      p = 0.0, cn = 0;
-      for (int i = 0; i < Q; ++i) p += s_p[i][c], cn += s_c[i][c];
-      if (e < a.E) {
-        a.counts[(size_t)g * a.E + e] = cn;
-        a.prob[(size_t)g * a.E + e] = n > 0 ? (float)(p / n) : 0.0f;
-        term = p * cn;
-      }
-    }
 #pragma unroll
-    for (int o = 1; o < 64; o <<= 1) term += __shfl_xor(term, o, 64);
-    if (threadIdx.x == 0) {
-      a.lossp[(size_t)g * gridDim.y + blockIdx.y] = group_term(a, n, term);
-      if (blockIdx.y == 0) a.n_tok[g] = n;
-      __threadfence();
-      s_last = atomicAdd(a.ticket, 1) == (int)(gridDim.x * gridDim.y) - 1;
+  for (int j = 0; j < 4; ++j) {
+    s_p[q][4 * c + j] = p[j];
+    s_c[q][4 * c + j] = cn[j];
+  }
+  const int n = block_sum<int, kFinThreads>(slots, [&](int i) { return a.nrow[s0 + i]; });
+  const double zg = blockIdx.y == 0 ? block_sum<double, kFinThreads>(slots, [&](int i) { return (double)a.zz[s0 + i]; }) : 0.0;
+  if (threadIdx.x < kFinCols) {
+    const int e = e0 + threadIdx.x;
+    double ps = 0.0;
+    int cs = 0;
+    for (int i = 0; i < Q; ++i) ps += s_p[i][threadIdx.x], cs += s_c[i][threadIdx.x];
+    if (e < a.E) {
+      a.counts[(size_t)g * a.E + e] = cs;
+      a.prob[(size_t)g * a.E + e] = n > 0 ? (float)(ps / n) : 0.0f;
     }
+    s_term[threadIdx.x] = e < a.E ? ps * cs : 0.0;
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    double term = 0.0;
+    for (int i = 0; i < kFinCols; ++i) term += s_term[i];
+    __hip_atomic_store(&a.lossp[(size_t)g * gridDim.y + blockIdx.y], group_term(a, n, term), __ATOMIC_RELAXED,
+                       __HIP_MEMORY_SCOPE_AGENT);
+    if (blockIdx.y == 0) {
+      __hip_atomic_store(&a.n_tok[g], n, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      __hip_atomic_store(&a.zzp[g], zg, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    s_last = __hip_atomic_fetch_add(a.ticket, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) ==
+             (int)(gridDim.x * gridDim.y) - 1;
   }
   __syncthreads();
   if (!s_last) return;
-  __threadfence();
-  const int N = block_sum<int>(a.G, [&](int i) { return a.n_tok[i]; });
-  const int groups = block_sum<int>(a.G, [&](int i) { return a.n_tok[i] > 0 ? 1 : 0; });
-  const double bal = block_sum<double>(a.G * (int)gridDim.y, [&](int i) { return a.lossp[i]; });
-  const double zz = block_sum<double>(a.G * a.splits, [&](int i) { return (double)a.zz[i]; });
+  auto rows_of = [&](int i) { return __hip_atomic_load(&a.n_tok[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); };
+  const int N = block_sum<int, kFinThreads>(a.G, rows_of);
+  const int groups = block_sum<int, kFinThreads>(a.G, [&](int i) { return rows_of(i) > 0 ? 1 : 0; });
+  auto term_of = [](double* p) { return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); };
+  const double bal = block_sum<double, kFinThreads>(a.G * (int)gridDim.y, [&](int i) { return term_of(&a.lossp[i]); });
+  const double zz = block_sum<double, kFinThreads>(a.G, [&](int i) { return term_of(&a.zzp[i]); });
   if (threadIdx.x == 0) write_totals(a, N, groups, bal, zz);
 }
 
@@ -343,45 +476,63 @@ template <int LPR, int NV, bool VEC>
 __global__ __launch_bounds__(kBalThreads) void balance_bwd_kernel(BalArgs a) {
   typedef RowLayout<LPR, NV, VEC> RL;
   constexpr int U = rows_at_once<NV>();
-  const int wg = blockIdx.x, g = wg / a.splits, s = wg % a.splits;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int l = lane & (LPR - 1), sub = lane / LPR;
-  int lo, hi;
-  if (!slice_rows(a, g, s, &lo, &hi)) return;
-  const int n = a.n_tok[g], N = a.n_tok[a.G], groups = a.n_tok[a.G + 1];
+  const int c_lo = blockIdx.x * a.rows, c_hi = min(a.T, c_lo + a.rows);
+  const int step = kBalWaves * RL::kRows * U;
+  const int g0 = first_group<kBalThreads>(a, c_lo);
+  if (g0 < 0) return;
+  const int N = a.n_tok[a.G], groups = a.n_tok[a.G + 1];
   const double d0 = a.d_loss ? a.d_loss[0] : 1.0, d1 = a.d_loss ? a.d_loss[1] : 1.0;
-  const float cw = n > 0 && groups > 0 ? (float)(a.alpha * d0 * a.E / ((double)a.k * n * n * groups)) : 0.0f;
   const float cz = N > 0 ? (float)(2.0 * a.beta * d1 / N) : 0.0f;
-  const double mean = (double)a.k * n / a.E;
-  float w[NV];
+  for (int g = g0; g < a.G; ++g) {
+    const int g_lo = group_begin(a, g), g_hi = group_begin(a, g + 1);
+    if (g_lo >= c_hi) break;
+    const int lo = max(g_lo, c_lo), hi = min(g_hi, c_hi);
+    if (lo >= hi) continue;
+    Rows<LPR, NV, VEC> now, next;
+    int r0 = lo + wave * RL::kRows * U;
+    if (r0 < hi) now.load(a, r0, hi, l, sub);
+    const int n = a.n_tok[g];
+    const float cw = n > 0 && groups > 0 ? (float)(a.alpha * d0 * a.E / ((double)a.k * n * n * groups)) : 0.0f;
+    const double mean = (double)a.k * n / a.E;
+    float w[NV];
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int e = RL::expert(l, i);
-    w[i] = e < a.E ? cw * (float)(a.counts[(size_t)g * a.E + e] - mean) : 0.0f;
-  }
-  for (int64_t r0 = lo + wave * RL::kRows * U; r0 < hi; r0 += kBalWaves * RL::kRows * U) {
-    float v[U][NV];
-    bool there[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int64_t r = r0 + u * RL::kRows + sub;
-      there[u] = r < hi;
-      RL::load(a.z + (size_t)r * a.E, there[u], l, a.E, v[u]);
-      if (a.mask) there[u] = there[u] && a.mask[r];
+    for (int i = 0; i < NV; ++i) {
+      const int e = RL::expert(l, i);
+      w[i] = e < a.E ? cw * (float)(a.counts[(size_t)g * a.E + e] - mean) : 0.0f;
     }
+    while (r0 < hi) {
+      const bool more = hi - r0 > step;
+      if (more) next.load(a, r0 + step, hi, l, sub);
+      bool live[U];
+      float lse[U], dot[U];
+      const bool rare = softmax_rows<LPR, NV, U>(now.v, now.mask, now.in, lane, live, lse);
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      float lse;
-      const bool live = row_softmax<LPR, NV>(v[u], there[u], lane, &lse);
-      float dot = 0.0f;
+      for (int u = 0; u < U; ++u) {
+        dot[u] = 0.0f;
 #pragma unroll
-      for (int i = 0; i < NV; ++i) dot = __builtin_fmaf(v[u][i], w[i], dot);
-      dot = group_reduce<LPR, OpAdd>(dot);
-      const float c = __builtin_fmaf(cz, lse, -dot);
+        for (int i = 0; i < NV; ++i) dot[u] = __builtin_fmaf(now.v[u][i], w[i], dot[u]);
+        dot[u] = group_sum<LPR>(dot[u]);
+      }
 #pragma unroll
-      for (int i = 0; i < NV; ++i) v[u][i] = live ? v[u][i] * (w[i] + c) : 0.0f;
-      const int64_t r = r0 + u * RL::kRows + sub;
-      if (r < hi) RL::store(a.dz + (size_t)r * a.E, l, a.E, v[u]);
+      for (int u = 0; u < U; ++u) {
+        const float c = __builtin_fmaf(cz, lse[u], -dot[u]);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) now.v[u][i] *= w[i] + c;
+      }
+      if (rare) {  // exact zeros where nothing counts, whatever d_loss holds
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+          for (int i = 0; i < NV; ++i) now.v[u][i] = live[u] ? now.v[u][i] : 0.0f;
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (now.in[u]) RL::store(a.dz + (size_t)(r0 + u * RL::kRows + sub) * a.E, l, a.E, now.v[u]);
+      if (!more) break;
+      r0 += step;
+      now = next;
     }
   }
 }
@@ -405,15 +556,16 @@ Shape row_shape(int E, uintptr_t align) {
   return s;
 }
 
-// Slices per group: about kBalWgs workgroups in all, no slice shorter than
-// one step of a workgroup on average.
-int split_count(int T, int E, int G) {
+// Rows per chunk: whole steps of a workgroup, at most kBalWgs chunks.
+int chunk_rows(int T, int E) {
   const Shape s = row_shape(E, 0);
   const int64_t step = (int64_t)kBalWaves * (64 / s.lpr) * (s.nv >= 8 ? rows_at_once<8>() : rows_at_once<4>());
-  int64_t n = kBalWgs / G;
-  const int64_t most = (T + step * G - 1) / (step * G);
-  if (n > most) n = most;
-  return n < 1 ? 1 : (int)n;
+  const int64_t n = (T + kBalWgs * step - 1) / (kBalWgs * step);
+  return (int)(step * (n < 1 ? 1 : n));
+}
+int chunk_count(int T, int E) {
+  const int rows = chunk_rows(T, E);
+  return T > rows ? (T + rows - 1) / rows : 1;
 }
 
 int fin_blocks(int E) { return (E + kFinCols - 1) / kFinCols; }
@@ -422,7 +574,7 @@ size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 template <bool BWD, int LPR, int NV, bool VEC>
 void launch_rows(const BalArgs& a, hipStream_t st) {
-  const dim3 grid((unsigned)(a.G * a.splits)), blk(kBalThreads);
+  const dim3 grid((unsigned)a.chunks), blk(kBalThreads);
   if constexpr (BWD)
     hipLaunchKernelGGL((balance_bwd_kernel<LPR, NV, VEC>), grid, blk, 0, st, a);
   else
@@ -457,8 +609,9 @@ void launch_shape(const Shape& s, const BalArgs& a, hipStream_t st) {
 }  // namespace
 
 size_t balance_ws_bytes(int T, int E, int G) {
-  const size_t wgs = (size_t)G * split_count(T, E, G);
-  return 2 * align256(wgs * E * 4) + 2 * align256(wgs * 4) + align256((size_t)G * fin_blocks(E) * 8) + 256;
+  const size_t slots = (size_t)G + chunk_count(T, E);
+  return 2 * align256(slots * E * 4) + 2 * align256(slots * 4) + align256((size_t)G * fin_blocks(E) * 8) +
+         align256((size_t)G * 8) + 256;
 }
 
 mok_status launch_balance_fwd(int T, int E, int k, int G, const mok_balance& b, const float* logits,
@@ -471,27 +624,29 @@ mok_status launch_balance_fwd(int T, int E, int k, int G, const mok_balance& b, 
   a.mask = b.token_mask;
   a.off = b.G > 0 ? b.group_offsets : nullptr;
   a.T = T, a.E = E, a.k = k, a.G = G;
-  a.splits = split_count(T, E, G);
+  a.rows = chunk_rows(T, E);
+  a.chunks = chunk_count(T, E);
   a.status = status;
-  const size_t wgs = (size_t)G * a.splits;
+  const size_t slots = (size_t)G + a.chunks;
   char* p = (char*)ws;
-  a.part = (float*)p;
-  p += align256(wgs * E * 4);
-  a.cnt = (int32_t*)p;
-  p += align256(wgs * E * 4);
-  a.zz = (float*)p;
-  p += align256(wgs * 4);
-  a.rows = (int32_t*)p;
-  p += align256(wgs * 4);
-  a.lossp = (double*)p;
-  p += align256((size_t)G * fin_blocks(E) * 8);
+  auto take = [&](size_t bytes) {
+    char* q = p;
+    p += align256(bytes);
+    return q;
+  };
+  a.part = (float*)take(slots * E * 4);
+  a.cnt = (int32_t*)take(slots * E * 4);
+  a.zz = (float*)take(slots * 4);
+  a.nrow = (int32_t*)take(slots * 4);
+  a.lossp = (double*)take((size_t)G * fin_blocks(E) * 8);
+  a.zzp = (double*)take((size_t)G * 8);
   a.ticket = (int32_t*)p;
   a.counts = counts, a.prob = prob, a.n_tok = n_tok, a.loss = loss;
   a.alpha = b.alpha, a.beta = b.beta;
   launch_shape<false>(row_shape(E, (uintptr_t)logits), a, stream);
   trace_mark(tr, "balance_fwd", stream);
-  if (wgs > 1) {
-    hipLaunchKernelGGL(balance_finish_kernel, dim3(G, fin_blocks(E)), dim3(kBalThreads), 0, stream, a);
+  if (a.chunks > 1 || G > 1) {
+    hipLaunchKernelGGL(balance_finish_kernel, dim3(G, fin_blocks(E)), dim3(kFinThreads), 0, stream, a);
     trace_mark(tr, "balance_finish", stream);
   }
   return hipGetLastError() == hipSuccess ? MOK_OK : MOK_EDEVICE;
@@ -505,7 +660,8 @@ mok_status launch_balance_bwd(int T, int E, int k, int G, const mok_balance& b, 
   a.mask = b.token_mask;
   a.off = b.G > 0 ? b.group_offsets : nullptr;
   a.T = T, a.E = E, a.k = k, a.G = G;
-  a.splits = split_count(T, E, G);
+  a.rows = chunk_rows(T, E);
+  a.chunks = chunk_count(T, E);
   a.status = status;
   a.counts = const_cast<int32_t*>(counts);
   a.n_tok = const_cast<int32_t*>(n_tok);

@@ -17,26 +17,49 @@ __device__ __forceinline__ float dpp_f(float x) {
   return __uint_as_float((unsigned)__builtin_amdgcn_mov_dpp((int)__float_as_uint(x), CTRL, 0xF, 0xF, true));
 }
 
-struct OpAdd {
-  __device__ __forceinline__ static float op(float a, float b) { return a + b; }
-};
-struct OpMax {
-  __device__ __forceinline__ static float op(float a, float b) { return __builtin_fmaxf(a, b); }
-};
-
-template <int L, class Op>
-__device__ __forceinline__ float group_reduce(float x) {
-  if constexpr (L >= 2) x = Op::op(x, dpp_f<0xB1>(x));
-  if constexpr (L >= 4) x = Op::op(x, dpp_f<0x4E>(x));
-  if constexpr (L >= 8) x = Op::op(x, dpp_f<0x141>(x));
-  if constexpr (L >= 16) x = Op::op(x, dpp_f<0x140>(x));
+template <int L>
+__device__ __forceinline__ float group_sum(float x) {
+  if constexpr (L >= 2) x = x + dpp_f<0xB1>(x);
+  if constexpr (L >= 4) x = x + dpp_f<0x4E>(x);
+  if constexpr (L >= 8) x = x + dpp_f<0x141>(x);
+  if constexpr (L >= 16) x = x + dpp_f<0x140>(x);
   if constexpr (L >= 32) {
     const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
-    x = Op::op(__uint_as_float(r[0]), __uint_as_float(r[1]));
+    x = __uint_as_float(r[0]) + __uint_as_float(r[1]);
   }
   if constexpr (L >= 64) {
     const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
-    x = Op::op(__uint_as_float(r[0]), __uint_as_float(r[1]));
+    x = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+  }
+  return x;
+}
+
+// fp32 values as signed integers of the same order (-0 below +0; a positive
+// NaN above infinity, a negative one below -inf), so that a maximum is one
+// integer instruction with the exchange folded in.
+__device__ __forceinline__ int float_order(float x) {
+  const int b = (int)__float_as_uint(x);
+  return b ^ ((b >> 31) & 0x7FFFFFFF);
+}
+__device__ __forceinline__ float order_float(int o) { return __uint_as_float((unsigned)(o ^ ((o >> 31) & 0x7FFFFFFF))); }
+
+template <int CTRL>
+__device__ __forceinline__ int dpp_i(int x) {
+  return __builtin_amdgcn_mov_dpp(x, CTRL, 0xF, 0xF, true);
+}
+template <int L>
+__device__ __forceinline__ int group_max(int x) {
+  if constexpr (L >= 2) x = max(x, dpp_i<0xB1>(x));
+  if constexpr (L >= 4) x = max(x, dpp_i<0x4E>(x));
+  if constexpr (L >= 8) x = max(x, dpp_i<0x141>(x));
+  if constexpr (L >= 16) x = max(x, dpp_i<0x140>(x));
+  if constexpr (L >= 32) {
+    const auto r = __builtin_amdgcn_permlane16_swap((unsigned)x, (unsigned)x, false, false);
+    x = max((int)r[0], (int)r[1]);
+  }
+  if constexpr (L >= 64) {
+    const auto r = __builtin_amdgcn_permlane32_swap((unsigned)x, (unsigned)x, false, false);
+    x = max((int)r[0], (int)r[1]);
   }
   return x;
 }

@@ -393,7 +393,7 @@ mok_status mok_prepare_bwd(const mok_config* cfg, const void* w_gate, const void
                            uint8_t* st_gu, void* stream);
 
 /* Balance loss of the router and its gradient, for training.  The T tokens
- * come in G groups of consecutive rows (the sequences of a batch, or one
+ * (at most 2^30, T * k and G * E at most 2^31 - 1) come in G groups of consecutive rows (the sequences of a batch, or one
  * group); rows outside [group_offsets[0], group_offsets[G]) belong to no
  * group.  A row counts if its mask byte is nonzero and not all of its logits
  * are -inf.  With p = softmax(z) of a counted row, N_g the counted rows of
@@ -420,8 +420,8 @@ size_t mok_balance_ws_bytes(const mok_config* cfg, int32_t T, const mok_balance*
  * prob [G, E] the mean of p over the group's counted rows (0 for an empty
  * group), n_tok [G+2] = N_g of every group, then N, then G+; loss [2] =
  * L_balance, L_z.  An id outside [0, E) latches MOK_EROUTE and is not
- * counted; offsets that do not ascend within [0, T] latch MOK_EGROUP and the
- * group counts nothing.  NaN logits of counted rows reach the losses; values
+ * counted; offsets that do not ascend within [0, T] latch MOK_EGROUP and
+ * nothing counts.  NaN logits of counted rows reach the losses; values
  * of rows that do not count are never used. */
 mok_status mok_balance_fwd(const mok_config* cfg, int32_t T, const mok_balance* bal,
                            const float* logits, const int32_t* topk_idx, int32_t* counts,
@@ -432,7 +432,8 @@ mok_status mok_balance_fwd(const mok_config* cfg, int32_t T, const mok_balance* 
  *   d_logits[t][e] = p_te (w_ge - sum_i p_ti w_gi) + p_te 2 beta d_loss[1] lse_t / N,
  *   w_ge = alpha d_loss[0] E c_ge / (k N_g^2 G+),
  * [T, E] fp32, overwritten: zero in rows of a group that do not count; rows
- * outside every group are left as they are.  counts and n_tok as the forward
+ * outside every group are left as they are (all rows, with MOK_EGROUP
+ * latched, if the offsets do not ascend within [0, T]).  counts and n_tok as the forward
  * wrote them; d_loss [2] fp32 on the device, or NULL = {1, 1}.  d_logits may
  * be logits itself. */
 mok_status mok_balance_bwd(const mok_config* cfg, int32_t T, const mok_balance* bal,

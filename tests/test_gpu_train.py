@@ -13,7 +13,7 @@ Tolerances (u = 2^-24, half a step of fp32):
     of the sum of exponentials (24 u absolute) and a logf and an add (4 u
     |lse|): bound 96 u p (|w| + sum p|w|) * 2 + 96 u p |c| (1 + |lse|);
   * losses and mean probabilities are sums of positive terms: 64 u from p, u
-    per row that a lane adds (at most rows / slices) and one rounding;
+    per row that a lane adds within a chunk and one rounding;
   * matrix products: n terms give at most (n + 2) u sum |a||b|, a result in
     bf16 half a step (2^-8 |ref|) more; where fp32 operands are split into
     bf16 parts, 2^-16 sum |a||b| (two parts, bf16 results) or 2^-23 (three);
@@ -153,6 +153,10 @@ BALANCE = [
     (130, 100, 4, [0, 130], 0, 0),
     (130, 33, 16, None, 0.2, 0),
     (100, 17, 2, None, 0, 0),
+    # many chunks and groups: empty groups at both ends and between, groups of one row, one long
+    (3000, 256, 8, [0, 0, 0, 1, 2, 17, 17, 2900, 2990, 2990], 0.1, 0),
+    (2500, 512, 2, [3] + list(range(3, 2400, 7)) + [2499], 0, 0),
+    (40000, 16, 4, [0, 39999, 39999, 40000], 0, 0),
 ]
 
 
@@ -173,7 +177,7 @@ def test_balance_against_definition(case, shift):
     assert torch.equal(got[1].long(), ref[1])
     assert got[3].tolist() == ref[3]
     most = max([b - a for a, b in zip(off, off[1:])] if off else [T])
-    sums = (64 + min(most, 256) + 2) * U      # a slice adds at most 256 rows per lane here
+    sums = (64 + min(most, 256) + 2) * U      # a chunk adds at most 256 rows per lane here
     _within(got[2], ref[2], sums * ref[2], "prob")
     lse2 = 2 * (28 * U) + sums                # lse^2: twice the relative error of lse >= 1, here
     _within(got[0][:1], ref[0][:1], sums * ref[0][:1], "balance loss")
@@ -237,12 +241,11 @@ def test_balance_bad_ids_and_offsets_are_latched():
     ref = _balance_ref(z, bad, E, k, 1e-2, 1e-3, None, None, [1.0, 1.0], torch.zeros(T, E))
     got = _balance_run(z, bad, E, k, 1e-2, 1e-3, None, None, [1.0, 1.0], torch.zeros(T, E))
     assert got[5] == -6 and torch.equal(got[1].long(), ref[1])
-    for off in ([0, 30, 20, 50], [0, 20, 51], [-1, 20, 50]):
-        got = _balance_run(z, topk, E, k, 1e-2, 1e-3, off, None, [1.0, 1.0], torch.zeros(T, E))
+    for off in ([0, 30, 20, 50], [0, 20, 51], [-1, 20, 50], [0, 51], [50, 0]):
+        got = _balance_run(z, topk, E, k, 1e-2, 1e-3, off, None, [1.0, 1.0], torch.full((T, E), 3.0))
         assert got[5] == -8
-        for g in range(len(off) - 1):
-            if not 0 <= off[g] <= off[g + 1] <= T:
-                assert not got[1][g].any() and got[3][g] == 0
+        assert not got[0].any() and not got[1].any() and not got[2].any() and not got[3].any()
+        assert (got[4] == 3.0).all()
 
 
 def test_balance_gradient_against_differences():

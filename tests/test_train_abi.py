@@ -50,6 +50,7 @@ def test_balance_refusals(L):
     assert _balance_fwd(L, cfg, bal=_bal(G=-1)) == EINVAL
     assert _balance_fwd(L, cfg, bal=_bal(G=3)) == EINVAL               # groups without offsets
     assert _balance_fwd(L, _cfg(T_src=1, k=8), T=1 << 29) == EINVAL    # counts beyond int32
+    assert _balance_fwd(L, _cfg(T_src=1, k=1), T=(1 << 30) + 1) == EINVAL
     assert _balance_fwd(L, cfg, bal=_bal(G=1 << 29, off=16)) == EINVAL  # G * E beyond int32
     assert L.mok_balance_fwd(ctypes.byref(cfg), 10, None, 16, 16, 16, 16, 16, 16, 256, None,
                              None) == EINVAL
