@@ -291,10 +291,21 @@ def _ptr(t) -> Optional[int]:
     return t.data_ptr()
 
 
+_raw_stream = None
+
+
 def _stream(stream) -> Optional[int]:
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        global _raw_stream
+        if _raw_stream is None:
+            # torch.cuda.current_stream() builds a Stream object, 3 us of every
+            # call; the raw handle of the current device's stream is the same
+            import torch
+            raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+            dev = torch.cuda.current_device
+            _raw_stream = ((lambda: raw(dev())) if raw is not None
+                           else (lambda: torch.cuda.current_stream().cuda_stream))
+        return _raw_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream

@@ -925,7 +925,7 @@ mok_status mok_balance_fwd(const mok_config* cfg, int32_t T, const mok_balance* 
                            int32_t* dev_status, void* stream) {
   if (!valid_balance(cfg, T, bal)) return MOK_EINVAL;
   if (T > 0 && (!logits || !topk_idx)) return MOK_EINVAL;
-  if (!counts || !prob || !n_tok || !loss || !ws || !aligned(ws, 8)) return MOK_EINVAL;
+  if (!counts || !prob || !n_tok || !loss || !ws || !aligned(ws, 16)) return MOK_EINVAL;
   trace_mark(cfg->trace, "start", (hipStream_t)stream);
   return launch_balance_fwd(T, cfg->E, cfg->k, balance_groups(bal), *bal, logits, topk_idx, counts,
                             prob, n_tok, loss, ws, dev_status, (hipStream_t)stream, cfg->trace);

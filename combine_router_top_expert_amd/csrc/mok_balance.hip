@@ -52,7 +52,7 @@ struct BalArgs {
   int32_t* cnt;          // [slots][E]
   float* zz;             // [slots]
   int32_t* nrow;         // [slots]
-  int32_t* ticket;       // workgroups of the finishing kernel that are done
+  int32_t* ticket;       // [0] workgroups of the finishing kernel that are done, [1] the offsets are good
   double* lossp;         // [G * ceil(E / kFinCols)]
   double* zzp;           // [G]
   // outputs and the backward's inputs
@@ -91,23 +91,23 @@ __device__ __forceinline__ T block_sum(int n, F value) {
 __device__ __forceinline__ int group_begin(const BalArgs& a, int g) { return a.off ? a.off[g] : g == 0 ? 0 : a.T; }
 
 // The first group that ends behind `row`, or -1 (MOK_EGROUP latched) if the
-// offsets do not ascend within [0, T].  Every workgroup reads them all, so
-// every one comes to the same answer.
-template <int THREADS>
+// offsets do not ascend within [0, T].  Every wave reads them all, so every
+// one comes to the same answer without a barrier.
 __device__ __forceinline__ int first_group(const BalArgs& a, int row) {
   if (!a.off) return 0;
+  const int lane = threadIdx.x & 63;
   int before = 0;
-  bool bad = false;
-  for (int g = threadIdx.x; g < a.G; g += THREADS) {
-    const int b = a.off[g], e = a.off[g + 1];
-    bad = bad || b < 0 || e < b || e > a.T;
-    before += e <= row;
+  for (int g0 = 0; g0 < a.G; g0 += 64) {
+    const int g = g0 + lane;
+    const bool in = g < a.G;
+    const int b = in ? a.off[g] : 0, e = in ? a.off[g + 1] : 0;
+    if (__any(in && (b < 0 || e < b || e > a.T))) {
+      if (lane == 0) latch(a.status, MOK_EGROUP);
+      return -1;
+    }
+    before += (int)__popcll(__ballot(in && e <= row));
   }
-  if (__syncthreads_or(bad)) {
-    if (threadIdx.x == 0) latch(a.status, MOK_EGROUP);
-    return -1;
-  }
-  return block_sum<int, THREADS>(before);
+  return before;
 }
 
 // The row layout: lane l of LPR holds experts 4 (l + LPR u) + 0..3 (VEC) or
@@ -168,7 +168,7 @@ struct RowLayout {
 // Values of a lane in U rows at once, so their loads are in flight together.
 template <int NV>
 constexpr int rows_at_once() {
-  return NV >= 8 ? 2 : 4;
+  return 2;
 }
 // Chosen slots of a row per lane (k <= 16 and k <= E).
 template <int LPR, bool VEC>
@@ -284,8 +284,11 @@ __global__ __launch_bounds__(kBalThreads) void balance_fwd_kernel(BalArgs a) {
   const int l = lane & (LPR - 1), sub = lane / LPR;
   const int c_lo = chunk * a.rows, c_hi = min(a.T, c_lo + a.rows);
   const int step = kBalWaves * RL::kRows * U;
-  if (chunk == 0 && tid == 0) *a.ticket = 0;   // for the kernel that follows
-  const int g0 = first_group<kBalThreads>(a, c_lo);
+  const int g0 = first_group(a, c_lo);
+  if (chunk == 0 && tid == 0) {  // for the kernel that follows
+    a.ticket[0] = 0;
+    a.ticket[1] = g0 >= 0;
+  }
   bool bad = false;
   auto load = [&](int r0, int hi, Rows<LPR, NV, VEC>& rows, int (&ids)[U][KJ]) {
 #pragma unroll
@@ -406,22 +409,37 @@ __global__ __launch_bounds__(kBalThreads) void balance_fwd_kernel(BalArgs a) {
 // would write back the whole L2 once per workgroup (17 us against 6 us for
 // 512 workgroups).
 __global__ __launch_bounds__(kFinThreads) void balance_finish_kernel(BalArgs a) {
-  constexpr int C = kFinCols / 4, Q = kFinThreads / C;
+  constexpr int C = kFinCols / 4, Q = kFinThreads / C, W = kFinThreads / 64;
+  static_assert(kFinCols == 64, "an expert per lane of wave 0");
   __shared__ double s_p[Q][kFinCols + 1];
   __shared__ int s_c[Q][kFinCols + 1];
-  __shared__ double s_term[kFinCols];
+  __shared__ double s_a[W], s_b[W];
+  __shared__ int s_n[W], s_m[W];
   __shared__ int s_last;
   const int g = blockIdx.x, c = threadIdx.x % C, q = threadIdx.x / C;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int e0 = blockIdx.y * kFinCols;
   // the chunks that meet the group; none if it is empty or the offsets are bad
-  const bool ok = first_group<kFinThreads>(a, 0) >= 0;
-  const int g_lo = ok ? group_begin(a, g) : 0, g_hi = ok ? group_begin(a, g + 1) : 0;
-  const int first = g_lo / a.rows, slots = g_hi > g_lo ? (g_hi - 1) / a.rows - first + 1 : 0;
+  const int g_lo = group_begin(a, g), g_hi = group_begin(a, g + 1);
+  const bool some = a.ticket[1] && g_hi > g_lo;
+  const int first = some ? g_lo / a.rows : 0, slots = some ? (g_hi - 1) / a.rows - first + 1 : 0;
   const size_t s0 = (size_t)first + g;
-  double p[4] = {0.0, 0.0, 0.0, 0.0};
-  int cn[4] = {0, 0, 0, 0};
+  double p[4] = {0.0, 0.0, 0.0, 0.0}, zz = 0.0;
+  int cn[4] = {0, 0, 0, 0}, n = 0;
+  for (int i = threadIdx.x; i < slots; i += kFinThreads) {
+    n += a.nrow[s0 + i];
+    zz += (double)a.zz[s0 + i];
+  }
   for (int s = q; s < slots; s += Q) {
     const size_t i = (s0 + s) * a.E + e0 + 4 * c;
+    if (a.E % 4 == 0) {
+      if (e0 + 4 * c >= a.E) break;
+      const float4 x = *reinterpret_cast<const float4*>(a.part + i);
+      const int4 y = *reinterpret_cast<const int4*>(a.cnt + i);
+      p[0] += (double)x.x, p[1] += (double)x.y, p[2] += (double)x.z, p[3] += (double)x.w;
+      cn[0] += y.x, cn[1] += y.y, cn[2] += y.z, cn[3] += y.w;
+      continue;
+    }
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       if (e0 + 4 * c + j >= a.E) break;
@@ -434,42 +452,69 @@ __global__ __launch_bounds__(kFinThreads) void balance_finish_kernel(BalArgs a) 
     s_p[q][4 * c + j] = p[j];
     s_c[q][4 * c + j] = cn[j];
   }
-  const int n = block_sum<int, kFinThreads>(slots, [&](int i) { return a.nrow[s0 + i]; });
-  const double zg = blockIdx.y == 0 ? block_sum<double, kFinThreads>(slots, [&](int i) { return (double)a.zz[s0 + i]; }) : 0.0;
-  if (threadIdx.x < kFinCols) {
-    const int e = e0 + threadIdx.x;
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    n += __shfl_xor(n, o, 64);
+    zz += __shfl_xor(zz, o, 64);
+  }
+  if (lane == 0) s_n[wave] = n, s_a[wave] = zz;
+  __syncthreads();
+  if (wave == 0) {
+    const int e = e0 + lane;
     double ps = 0.0;
     int cs = 0;
-    for (int i = 0; i < Q; ++i) ps += s_p[i][threadIdx.x], cs += s_c[i][threadIdx.x];
+#pragma unroll 8
+    for (int i = 0; i < Q; ++i) ps += s_p[i][lane], cs += s_c[i][lane];
+    n = 0, zz = 0.0;
+#pragma unroll
+    for (int i = 0; i < W; ++i) n += s_n[i], zz += s_a[i];
     if (e < a.E) {
       a.counts[(size_t)g * a.E + e] = cs;
       a.prob[(size_t)g * a.E + e] = n > 0 ? (float)(ps / n) : 0.0f;
     }
-    s_term[threadIdx.x] = e < a.E ? ps * cs : 0.0;
-  }
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    double term = 0.0;
-    for (int i = 0; i < kFinCols; ++i) term += s_term[i];
-    __hip_atomic_store(&a.lossp[(size_t)g * gridDim.y + blockIdx.y], group_term(a, n, term), __ATOMIC_RELAXED,
-                       __HIP_MEMORY_SCOPE_AGENT);
-    if (blockIdx.y == 0) {
-      __hip_atomic_store(&a.n_tok[g], n, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-      __hip_atomic_store(&a.zzp[g], zg, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    double term = e < a.E ? ps * cs : 0.0;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) term += __shfl_xor(term, o, 64);
+    if (lane == 0) {
+      __hip_atomic_store(&a.lossp[(size_t)g * gridDim.y + blockIdx.y], group_term(a, n, term), __ATOMIC_RELAXED,
+                         __HIP_MEMORY_SCOPE_AGENT);
+      if (blockIdx.y == 0) {
+        __hip_atomic_store(&a.n_tok[g], n, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        __hip_atomic_store(&a.zzp[g], zz, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      }
+      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+      s_last = __hip_atomic_fetch_add(a.ticket, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) ==
+               (int)(gridDim.x * gridDim.y) - 1;
     }
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    s_last = __hip_atomic_fetch_add(a.ticket, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) ==
-             (int)(gridDim.x * gridDim.y) - 1;
   }
   __syncthreads();
   if (!s_last) return;
-  auto rows_of = [&](int i) { return __hip_atomic_load(&a.n_tok[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); };
-  const int N = block_sum<int, kFinThreads>(a.G, rows_of);
-  const int groups = block_sum<int, kFinThreads>(a.G, [&](int i) { return rows_of(i) > 0 ? 1 : 0; });
-  auto term_of = [](double* p) { return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); };
-  const double bal = block_sum<double, kFinThreads>(a.G * (int)gridDim.y, [&](int i) { return term_of(&a.lossp[i]); });
-  const double zz = block_sum<double, kFinThreads>(a.G, [&](int i) { return term_of(&a.zzp[i]); });
-  if (threadIdx.x == 0) write_totals(a, N, groups, bal, zz);
+  int N = 0, groups = 0;
+  double bal = 0.0;
+  zz = 0.0;
+  for (int i = threadIdx.x; i < a.G; i += kFinThreads) {
+    const int r = __hip_atomic_load(&a.n_tok[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    N += r;
+    groups += r > 0;
+    zz += __hip_atomic_load(&a.zzp[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  }
+  for (int i = threadIdx.x; i < a.G * (int)gridDim.y; i += kFinThreads)
+    bal += __hip_atomic_load(&a.lossp[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    N += __shfl_xor(N, o, 64);
+    groups += __shfl_xor(groups, o, 64);
+    zz += __shfl_xor(zz, o, 64);
+    bal += __shfl_xor(bal, o, 64);
+  }
+  if (lane == 0) s_n[wave] = N, s_m[wave] = groups, s_a[wave] = zz, s_b[wave] = bal;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    N = groups = 0, zz = bal = 0.0;
+#pragma unroll
+    for (int i = 0; i < W; ++i) N += s_n[i], groups += s_m[i], zz += s_a[i], bal += s_b[i];
+    write_totals(a, N, groups, bal, zz);
+  }
 }
 
 template <int LPR, int NV, bool VEC>
@@ -480,7 +525,7 @@ __global__ __launch_bounds__(kBalThreads) void balance_bwd_kernel(BalArgs a) {
   const int l = lane & (LPR - 1), sub = lane / LPR;
   const int c_lo = blockIdx.x * a.rows, c_hi = min(a.T, c_lo + a.rows);
   const int step = kBalWaves * RL::kRows * U;
-  const int g0 = first_group<kBalThreads>(a, c_lo);
+  const int g0 = first_group(a, c_lo);
   if (g0 < 0) return;
   const int N = a.n_tok[a.G], groups = a.n_tok[a.G + 1];
   const double d0 = a.d_loss ? a.d_loss[0] : 1.0, d1 = a.d_loss ? a.d_loss[1] : 1.0;

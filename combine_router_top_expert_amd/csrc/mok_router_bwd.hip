@@ -32,7 +32,8 @@ constexpr int kThreads = 256;
 constexpr int kTile = 64;   // output tile 64 x 64, four waves of 32 x 32
 constexpr int kKB = 32;     // contraction steps staged through LDS at a time
 constexpr int kPitch = kTile + 4;
-constexpr int kBf16Threads = 512;   // eight waves in the bf16 products
+constexpr int kDxWaves = 4;
+constexpr int kBf16Threads = 512;   // eight waves in the dW product of bf16 layers
 constexpr int kBK = 16;             // token rows per LDS stage of dW
 
 struct RArgs {
@@ -221,17 +222,17 @@ __device__ __forceinline__ bf16x8_t frag64(const char* lds, int n0, int s) {
   return __builtin_bit_cast(bf16x8_t, __builtin_shufflevector(h[0], h[1], 0, 1, 2, 3, 4, 5, 6, 7));
 }
 
-// NK: 16-expert steps (E <= 16 NK); WAVES of 32 token rows each.
-template <int NK, int WAVES>
-__global__ __launch_bounds__(64 * WAVES, WAVES == 8 ? 2 : 1) void router_dx_bf16_kernel(RArgs a) {
+// NK: 16-expert steps (E <= 16 NK); four waves of 32 token rows each, two
+// workgroups per CU up to NK = 16 (one computes while the other stores).
+template <int NK>
+__global__ __launch_bounds__(kThreads, NK <= 16 ? 2 : 1) void router_dx_bf16_kernel(RArgs a) {
   constexpr int STAGE = NK * 16 * 128;               // bytes of W per column step
-  constexpr int LOADS = STAGE / 1024 / WAVES;        // direct loads per wave and step
-  static_assert(LOADS >= 1, "every wave loads");
-  __shared__ __attribute__((aligned(16))) char smem[2 * STAGE + WAVES * 4096];
+  constexpr int LOADS = STAGE / 1024 / kDxWaves;     // direct loads per wave and step
+  __shared__ __attribute__((aligned(16))) char smem[2 * STAGE + kDxWaves * 4096];
   const int lane = threadIdx.x & 63;
   const int wave = (int)g2::wave_id();
   // workgroups of one row block on one XCD (b % 8), so its parts meet in an L2
-  const int rb_n = (a.T + 32 * WAVES - 1) / (32 * WAVES);
+  const int rb_n = (a.T + 32 * kDxWaves - 1) / (32 * kDxWaves);
   int b = blockIdx.x, rb, ch;
   const int full = rb_n / 8 * 8 * a.n_chunks;
   if (b < full) {
@@ -265,7 +266,7 @@ __global__ __launch_bounds__(64 * WAVES, WAVES == 8 ? 2 : 1) void router_dx_bf16
   };
   if (s0 < s1) issue(s0, 0);
   // the wave's rows: parts hi and mid of every expert, in registers
-  const int t0 = (rb * WAVES + wave) * 32;
+  const int t0 = (rb * kDxWaves + wave) * 32;
   bf16x8_t hi[NK], mid[NK];
   {
     const int t = t0 + (lane & 31);
@@ -283,24 +284,26 @@ __global__ __launch_bounds__(64 * WAVES, WAVES == 8 ? 2 : 1) void router_dx_bf16
       mid[k] = __builtin_bit_cast(bf16x8_t, v);
     }
   }
-  // the rows this lane stores: 8 lanes per row, four rows
+  // the rows this lane stores: 8 lanes per row, four rows; chunk c of a
+  // staged row (128 bytes) sits at c ^ (row & 7), so this lane's chunk of row
+  // 8 i + lane / 8 is LDS position 64 i + lane for the column chunk below
+  const int col = ((lane % 8) ^ (lane / 8)) * 8;
   bf16_t* out[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int t = t0 + 8 * i + lane / 8;
-    out[i] = t < a.T ? reinterpret_cast<bf16_t*>(a.d_x.p[a.own_lo + t / a.T_src]) + (size_t)(t % a.T_src) * a.d + (lane % 8) * 8
+    out[i] = t < a.T ? reinterpret_cast<bf16_t*>(a.d_x.p[a.own_lo + t / a.T_src]) + (size_t)(t % a.T_src) * a.d + col
                      : nullptr;
   }
-  char* stg = smem + 2 * STAGE + wave * 4096;  // 32 rows x 128 bytes; chunk c of row r at c ^ (r & 7)
-  uint4 base[4];
+  char* stg = smem + 2 * STAGE + wave * 4096;
+  const unsigned stg_lds = lds0 + 2 * STAGE + wave * 4096;
   auto store = [&](int s) {  // the staged tile of column step s
+    uint4 u[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (!out[i]) continue;
-      const int r = 8 * i + lane / 8;
-      uint4 u = *reinterpret_cast<const uint4*>(stg + r * 128 + ((lane % 8) ^ (r & 7)) * 16);
-      st16(out[i] + (size_t)s * 64, u);
-    }
+    for (int i = 0; i < 4; ++i) u[i] = *reinterpret_cast<const uint4*>(stg + i * 1024 + lane * 16);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (out[i]) st16(out[i] + (size_t)s * 64, u[i]);
   };
   for (int s = s0; s < s1; ++s) {
     // this wave's loads of step s (and its stores of the step before last)
@@ -312,8 +315,12 @@ __global__ __launch_bounds__(64 * WAVES, WAVES == 8 ? 2 : 1) void router_dx_bf16
     if (s + 1 < s1) issue(s + 1, slot ^ 1);
     if (s > s0) store(s - 1);
     if (a.add) {
+      // what d_x holds goes straight into the staging rows, which store()
+      // has read into registers by now
+      g2::wave_lds_fence();
 #pragma unroll
-      for (int i = 0; i < 4; ++i) base[i] = out[i] ? ld16(out[i] + (size_t)s * 64) : make_uint4(0, 0, 0, 0);
+      for (int i = 0; i < 4; ++i)
+        g2::load_lds16(out[i] ? (const void*)(out[i] + (size_t)s * 64) : (const void*)g2::g_zero, stg_lds + i * 1024);
     }
     const char* W = smem + slot * STAGE;
     f32x16_t acc[2];
@@ -321,30 +328,39 @@ __global__ __launch_bounds__(64 * WAVES, WAVES == 8 ? 2 : 1) void router_dx_bf16
     for (int j = 0; j < 2; ++j)
 #pragma unroll
       for (int r = 0; r < 16; ++r) acc[j][r] = 0.0f;
+    // fragments are read kAhead k16 steps before their use
+    constexpr int kAhead = 2;
+    bf16x8_t f[kAhead + 1][2];
 #pragma unroll
-    for (int k = 0; k < NK; ++k)
+    for (int k = 0; k < kAhead; ++k)
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const bf16x8_t f = frag64(W, 32 * j, k);
-        acc[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f, mid[k], acc[j], 0, 0, 0);
-        acc[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f, hi[k], acc[j], 0, 0, 0);
+      for (int j = 0; j < 2; ++j) f[k][j] = frag64(W, 32 * j, k);
+    __builtin_amdgcn_sched_group_barrier(0x100, 4 * kAhead, 0);
+#pragma unroll
+    for (int k = 0; k < NK; ++k) {
+      if (k + kAhead < NK) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) f[(k + kAhead) % (kAhead + 1)][j] = frag64(W, 32 * j, k + kAhead);
       }
-    // lane holds row lane % 32, columns 32 j + 8 g + 4 (lane / 32) + 0..3
-    if (a.add) {  // the base goes through the staging rows to meet the sums
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int r = 8 * i + lane / 8;
-        st16(stg + r * 128 + ((lane % 8) ^ (r & 7)) * 16, base[i]);
-      }
-      g2::wave_lds_fence();
+      for (int j = 0; j < 2; ++j)
+        acc[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f[k % (kAhead + 1)][j], mid[k], acc[j], 0, 0, 0);
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        acc[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f[k % (kAhead + 1)][j], hi[k], acc[j], 0, 0, 0);
+      if (k + kAhead < NK) __builtin_amdgcn_sched_group_barrier(0x100, 4, 0);
+      __builtin_amdgcn_sched_group_barrier(0x008, 4, 0);
     }
+    // lane holds row lane % 32, columns 32 j + 8 g + 4 (lane / 32) + 0..3
+    if (a.add) g2::wait_vmcnt_lgkm0<0>();
+    asm volatile("" ::: "memory");
     const int r = lane & 31;
 #pragma unroll
     for (int j = 0; j < 2; ++j)
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
-        const int col = 32 * j + 8 * g + 4 * (lane >> 5);
-        uint2* p = reinterpret_cast<uint2*>(stg + r * 128 + ((col >> 3) ^ (r & 7)) * 16 + (col & 7) * 2);
+        const int c = 32 * j + 8 * g + 4 * (lane >> 5);
+        uint2* p = reinterpret_cast<uint2*>(stg + r * 128 + ((c >> 3) ^ (r & 7)) * 16 + (c & 7) * 2);
         float v[4] = {acc[j][4 * g], acc[j][4 * g + 1], acc[j][4 * g + 2], acc[j][4 * g + 3]};
         if (a.add) {
           const uint2 u = *p;
@@ -387,6 +403,15 @@ __device__ __forceinline__ bf16x8_t frag_mn(const char* lds, int rb, int n0) {
   return __builtin_bit_cast(bf16x8_t, __builtin_shufflevector(h[0], h[1], 0, 1, 2, 3, 4, 5, 6, 7));
 }
 
+// One direct load (lane i's 16 bytes land at LDS byte lds + 16 i) from a
+// uniform base and a lane offset; lds is wave-uniform.
+__device__ __forceinline__ void load_lds16_at(const char* base, unsigned off, unsigned lds) {
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
+               :
+               : "v"(off), "s"(base), "s"(lds)
+               : "memory", "m0");
+}
+
 template <int EW>
 __global__ __launch_bounds__(kBf16Threads, 2) void router_dw_bf16_kernel(RArgs a) {
   typedef DwCfg<EW> C;
@@ -416,10 +441,13 @@ __global__ __launch_bounds__(kBf16Threads, 2) void router_dw_bf16_kernel(RArgs a
   const int KT = (hi - lo + kBK - 1) / kBK;
   const unsigned lds0 = g2::lds_addr_of(smem);
   // This wave's units w, w + 8, ... of a stage: unit u is LDS bytes
-  // [1024 u, 1024 u + 1024), chunk positions 64 u + lane.
+  // [1024 u, 1024 u + 1024), chunk positions 64 u + lane.  voff: the lane's
+  // byte offset from the stage's first row of parts (or of x).
   constexpr int QM = C::Q + (C::X ? 1 : 0);
   const int nq = C::Q + (wave < C::X ? 1 : 0);
-  int krow[QM], ucol[QM], xt[QM], xs[QM];   // k-row, element column, and for x units the token's place
+  const int prow = a.etiles * 3 * EW;                  // elements per row of parts
+  unsigned voff[QM];
+  int krow[QM];
 #pragma unroll
   for (int j = 0; j < QM; ++j) {
     const int u = wave + 8 * j;
@@ -427,36 +455,50 @@ __global__ __launch_bounds__(kBf16Threads, 2) void router_dw_bf16_kernel(RArgs a
     const int pos = isA ? u * 64 + lane : (u * 1024 - C::A_BYTES) / 16 + lane;
     const int cpr = (isA ? C::RA : C::RB) / 16;
     krow[j] = pos / cpr;
-    const int c = (pos % cpr) ^ (4 * (krow[j] & 3));
-    ucol[j] = c * 8;
-    if (isA) {
-      if (ucol[j] >= 3 * EW) ucol[j] = -1;             // the padding of 64-wide tiles
-    } else if (n0 + ucol[j] >= a.d) ucol[j] = -1;
-    const int t = lo + krow[j];
-    xs[j] = t / a.T_src;
-    xt[j] = t % a.T_src;
+    int c = ((pos % cpr) ^ (4 * (krow[j] & 3))) * 8;
+    // the padding of 64-wide tiles and columns past d: any column will do,
+    // what comes of it is not stored
+    if (isA ? c >= 3 * EW : n0 + c >= a.d) c = 0;
+    voff[j] = (unsigned)(krow[j] * (isA ? prow : a.d) + c) * 2;
   }
-  const size_t prow = (size_t)a.etiles * 3 * EW;
-  auto issue = [&](int kt) {
-    const int slot = kt % C::NS;
+  const char* parts = reinterpret_cast<const char*>(a.parts + (size_t)et * 3 * EW);
+  // the source and its row that the next stage begins with (uniform)
+  int xs = lo / a.T_src, xt = lo % a.T_src, filled = 0;
+  auto issue = [&]() {
+    const int t0 = lo + filled * kBK;
+    const unsigned slot = lds0 + filled % C::NS * C::STAGE;
+    ++filled;
+    if (t0 + kBK <= hi && xt + kBK <= a.T_src) {
+      // sixteen rows of one source: uniform bases, no address arithmetic
+      const char* pa = parts + (size_t)t0 * prow * 2;
+      const char* px = reinterpret_cast<const char*>(reinterpret_cast<const bf16_t*>(a.x.p[a.own_lo + xs]) + (size_t)xt * a.d + n0);
+#pragma unroll
+      for (int j = 0; j < QM; ++j) {
+        if (j >= nq) continue;                          // wave-uniform
+        const unsigned u = (wave + 8 * j) * 1024;
+        load_lds16_at(u < C::A_BYTES ? pa : px, voff[j], slot + u);
+      }
+      xt += kBK;
+      if (xt == a.T_src) xt = 0, ++xs;
+      return;
+    }
+    // the last rows, or rows of several sources: row by row, zeros past hi
 #pragma unroll
     for (int j = 0; j < QM; ++j) {
-      if (j >= nq) continue;                            // wave-uniform
-      const int u = wave + 8 * j;
-      const int t = lo + kt * kBK + krow[j];
-      const void* src = g2::g_zero;
-      if (u * 1024 < C::A_BYTES) {
-        if (t < hi && ucol[j] >= 0) src = a.parts + (size_t)t * prow + (size_t)et * 3 * EW + ucol[j];
-      } else {
-        if (t < hi && ucol[j] >= 0) src = s_x[a.own_lo + xs[j]] + (size_t)xt[j] * a.d + n0 + ucol[j];
-        xt[j] += kBK;
-        while (xt[j] >= a.T_src && t < hi) {
-          xt[j] -= a.T_src;
-          ++xs[j];
-        }
+      if (j >= nq) continue;
+      const unsigned u = (wave + 8 * j) * 1024;
+      const int t = t0 + krow[j];
+      const char* src = reinterpret_cast<const char*>(g2::g_zero);
+      if (t < hi) {
+        if (u < C::A_BYTES) src = parts + (size_t)t0 * prow * 2 + voff[j];
+        else src = reinterpret_cast<const char*>(s_x[a.own_lo + t / a.T_src] + (size_t)(t % a.T_src) * a.d + n0) +
+                   (voff[j] - (unsigned)krow[j] * a.d * 2);
       }
-      g2::load_lds16(src, lds0 + slot * C::STAGE + u * 1024);
+      g2::load_lds16(src, slot + u);
     }
+    xt += kBK;
+    xs += xt / a.T_src;
+    xt %= a.T_src;
   };
   f32x16_t acc[2][2];
 #pragma unroll
@@ -466,7 +508,7 @@ __global__ __launch_bounds__(kBf16Threads, 2) void router_dw_bf16_kernel(RArgs a
 #pragma unroll
       for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
   const int we = wave / C::WN * 64, wn = wave % C::WN * 64;
-  for (int s = 0; s < C::NS - 1; ++s) issue(s);         // stages past KT read zeros
+  for (int s = 0; s < C::NS - 1; ++s) issue();          // stages past KT read zeros
   for (int kt = 0; kt < KT; ++kt) {
     // this wave's loads of stage kt have landed (the NS - 2 later stages stay
     // in flight); after the barrier everyone's have, and everyone is done
@@ -474,7 +516,7 @@ __global__ __launch_bounds__(kBf16Threads, 2) void router_dw_bf16_kernel(RArgs a
     if (wave < C::X) g2::wait_vmcnt_lgkm0<(C::NS - 2) * (C::Q + 1)>();
     else g2::wait_vmcnt_lgkm0<(C::NS - 2) * C::Q>();
     barrier();
-    issue(kt + C::NS - 1);
+    issue();   // stage kt + NS - 1
     const char* A = smem + kt % C::NS * C::STAGE;
     const char* B = A + C::A_BYTES;
     bf16x8_t fb[2];
@@ -504,17 +546,32 @@ __global__ __launch_bounds__(kBf16Threads, 2) void router_dw_bf16_kernel(RArgs a
       }
 }
 
-// dW from the chunks' partial sums in chunk order (the first dw_blocks
-// workgroups), and db: 32 experts per workgroup, eight threads an expert,
+// dW from the chunks' partial sums (the first dw_blocks workgroups: 64
+// 16-byte columns, four threads each adding every fourth chunk), and db: 32 experts per workgroup, eight threads an expert,
 // each adding every eighth partial sum.
 __global__ __launch_bounds__(kThreads) void router_reduce_kernel(RArgs a, int dw_blocks) {
   __shared__ double s_db[8][32];
   if ((int)blockIdx.x < dw_blocks) {
-    const size_t n = (size_t)a.E * a.d, i = ((size_t)blockIdx.x * kThreads + threadIdx.x) * 4;
-    if (i >= n) return;
-    float4 s = a.add ? *reinterpret_cast<const float4*>(a.dw + i) : make_float4(0, 0, 0, 0);
-    for (int c = 0; c < a.chunks; ++c) {
-      const float4 p = *reinterpret_cast<const float4*>(a.part + c * n + i);
+    __shared__ float4 s_dw[4][64];
+    const int c = threadIdx.x % 64, q = threadIdx.x / 64;
+    const size_t n = (size_t)a.E * a.d, i = ((size_t)blockIdx.x * 64 + c) * 4;
+    float4 s = make_float4(0, 0, 0, 0);
+    const float4* part = reinterpret_cast<const float4*>(a.part + i);
+#pragma unroll 4
+    for (int k = i < n ? q : a.chunks; k < a.chunks; k += 4) {
+      const float4 p = part[k * (n / 4)];
+      s.x += p.x, s.y += p.y, s.z += p.z, s.w += p.w;
+    }
+    s_dw[q][c] = s;
+    __syncthreads();
+    if (q != 0 || i >= n) return;
+    if (a.add) {
+      const float4 p = *reinterpret_cast<const float4*>(a.dw + i);
+      s.x += p.x, s.y += p.y, s.z += p.z, s.w += p.w;
+    }
+#pragma unroll
+    for (int j = 1; j < 4; ++j) {
+      const float4 p = s_dw[j][c];
       s.x += p.x, s.y += p.y, s.z += p.z, s.w += p.w;
     }
     *reinterpret_cast<float4*>(a.dw + i) = s;
@@ -573,14 +630,16 @@ Plan make_plan(int prec, int64_t T, int d, int E) {
   return p;
 }
 
-template <int NK, int WAVES>
+template <int NK>
 void launch_dx(RArgs& a, hipStream_t stream) {
-  // one workgroup per CU at least, as far as there are column steps
-  const int64_t rb = ((int64_t)a.T + 32 * WAVES - 1) / (32 * WAVES);
-  int64_t n = (256 + rb - 1) / rb;
+  // workgroups for every CU as often as they fit, as far as there are column
+  // steps
+  constexpr int kPerCu = NK <= 4 ? 4 : NK <= 16 ? 2 : 1;
+  const int64_t rb = ((int64_t)a.T + 32 * kDxWaves - 1) / (32 * kDxWaves);
+  int64_t n = (256 * kPerCu + rb - 1) / rb;
   if (n > a.d / 64) n = a.d / 64;
   a.n_chunks = (int)n;
-  hipLaunchKernelGGL((router_dx_bf16_kernel<NK, WAVES>), dim3((unsigned)(rb * n)), dim3(64 * WAVES), 0, stream, a);
+  hipLaunchKernelGGL(router_dx_bf16_kernel<NK>, dim3((unsigned)(rb * n)), dim3(kThreads), 0, stream, a);
 }
 
 template <int EW>
@@ -632,10 +691,10 @@ mok_status launch_router_bwd(const RouterBwdPlan& p, hipStream_t stream) {
       trace_mark(p.tr, "router_split", stream);
     }
     if (p.want_dx && p.T > 0) {
-      if (p.E <= 64) launch_dx<4, 8>(a, stream);
-      else if (p.E <= 128) launch_dx<8, 8>(a, stream);
-      else if (p.E <= 256) launch_dx<16, 8>(a, stream);
-      else launch_dx<32, 4>(a, stream);
+      if (p.E <= 64) launch_dx<4>(a, stream);
+      else if (p.E <= 128) launch_dx<8>(a, stream);
+      else if (p.E <= 256) launch_dx<16>(a, stream);
+      else launch_dx<32>(a, stream);
       trace_mark(p.tr, "router_dx", stream);
     }
     if (p.dw) {
@@ -648,7 +707,7 @@ mok_status launch_router_bwd(const RouterBwdPlan& p, hipStream_t stream) {
   // what is left to add up: dW over chunks, db over its partial sums
   const bool dw_left = p.dw && a.part, db_left = p.db && (a.dbp || !f32);
   if (dw_left || db_left) {
-    const unsigned dwb = dw_left ? (unsigned)(((size_t)p.E * p.d / 4 + kThreads - 1) / kThreads) : 0;
+    const unsigned dwb = dw_left ? (unsigned)(((size_t)p.E * p.d + 255) / 256) : 0;
     const unsigned dbb = db_left ? (unsigned)(p.E + 31) / 32 : 0;
     hipLaunchKernelGGL(router_reduce_kernel, dim3(dwb + dbb), blk, 0, stream, a, (int)dwb);
     trace_mark(p.tr, "router_reduce", stream);
