@@ -48,9 +48,14 @@ struct RArgs {
   int T, T_src, d, E, own_lo, chunks;
   int64_t chunk_rows;
   int add;
-  // bf16: the parts of dz, [T][E tiles][3 parts][EW]
+  // bf16: the parts of dz in 1 KiB blocks of 32 tokens x 16 experts,
+  // [T / 32][3 parts][E / 16] of [expert / 8 % 2][token % 32][expert % 8]: a
+  // block is one MFMA operand of dx as it lies, and half of its tokens are
+  // four 256-byte pieces of a dW stage; padded with zeros to whole blocks
+  // and expert tiles
   bf16_t* parts;
   int ew, etiles;      // experts per tile (64, 128 or 256) and tiles
+  int eblocks;         // etiles * ew / 16
   int64_t split_rows;  // token rows per workgroup of the split
   int db_parts;        // partial sums of db per expert
   int n_chunks;        // column chunks of dx, each a workgroup per row block
@@ -140,59 +145,62 @@ __global__ __launch_bounds__(kThreads) void router_dw_kernel(RArgs a) {
 }
 
 // ------------------------------------------------------------------ bf16: split
-// Workgroup: split_rows token rows; a thread keeps one group of 8 experts
-// (so the column sums of db stay in its registers, in 64 bits) and takes
-// every (256 / groups)-th row.
+// Workgroup: split_rows token rows (whole blocks of 32) of four expert
+// blocks, one a wave; lane l token l % 32 and 8 experts of half l / 32, so a
+// wave reads 64 bytes of 32 rows and writes whole blocks.  The column sums of
+// db stay in registers (64 bits) over the rows, then over the 32 lanes.
 __global__ __launch_bounds__(kThreads) void router_split_kernel(RArgs a) {
-  __shared__ double s_db[8][kThreads];
-  const int Ep = a.ew * a.etiles, groups = Ep / 8;
-  const int q = threadIdx.x % groups, r = threadIdx.x / groups, step = kThreads / groups;
-  const int e0 = q * 8;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int tl = lane & 31, half = lane >> 5;
   const bool wide = a.E % 4 == 0 && ((uintptr_t)a.dz & 15) == 0;
   const int64_t lo = (int64_t)blockIdx.x * a.split_rows;
   const int64_t hi = lo + a.split_rows < a.T ? lo + a.split_rows : a.T;
-  double db[8];
+  const int eb = blockIdx.y * (kThreads / 64) + wave;   // eblocks is a multiple of 4
+  {
+    const int e0 = eb * 16 + half * 8;
+    double db[8];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) db[j] = 0.0;
-  for (int64_t t = lo + r; t < hi; t += step) {
-    float v[8];
-    const float* row = a.dz + (size_t)t * a.E + e0;
-    if (wide) {
+    for (int j = 0; j < 8; ++j) db[j] = 0.0;
+#pragma unroll 2
+    for (int64_t t0 = lo; t0 < hi; t0 += 32) {
+      const int64_t t = t0 + tl;
+      float v[8];
+      const float* row = a.dz + (size_t)t * a.E + e0;
+      if (wide) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        float4 u = make_float4(0, 0, 0, 0);
-        if (e0 + 4 * h < a.E) u = *reinterpret_cast<const float4*>(row + 4 * h);
-        v[4 * h] = u.x, v[4 * h + 1] = u.y, v[4 * h + 2] = u.z, v[4 * h + 3] = u.w;
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = e0 + j < a.E ? row[j] : 0.0f;
-    }
-#pragma unroll
-    for (int j = 0; j < 8; ++j) db[j] += (double)v[j];
-    if (a.parts) {
-      bf16_t* o = a.parts + ((size_t)t * a.etiles + e0 / a.ew) * 3 * a.ew + e0 % a.ew;
-#pragma unroll
-      for (int p = 0; p < 3; ++p) {
-        uint32_t w[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          w[j] = pack2_bf16(v[2 * j], v[2 * j + 1]);
-          v[2 * j] -= __uint_as_float(w[j] << 16);
-          v[2 * j + 1] -= __uint_as_float(w[j] & 0xFFFF0000u);
+        for (int h = 0; h < 2; ++h) {
+          float4 u = make_float4(0, 0, 0, 0);
+          if (t < hi && e0 + 4 * h < a.E) u = *reinterpret_cast<const float4*>(row + 4 * h);
+          v[4 * h] = u.x, v[4 * h + 1] = u.y, v[4 * h + 2] = u.z, v[4 * h + 3] = u.w;
         }
-        st16(o + p * a.ew, make_uint4(w[0], w[1], w[2], w[3]));
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = t < hi && e0 + j < a.E ? row[j] : 0.0f;
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) db[j] += (double)v[j];
+      if (a.parts) {
+        bf16_t* o = a.parts + ((size_t)(t0 / 32) * 3 * a.eblocks + eb) * 512 + lane * 8;
+#pragma unroll
+        for (int p = 0; p < 3; ++p) {
+          uint32_t w[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            w[j] = pack2_bf16(v[2 * j], v[2 * j + 1]);
+            v[2 * j] -= __uint_as_float(w[j] << 16);
+            v[2 * j + 1] -= __uint_as_float(w[j] & 0xFFFF0000u);
+          }
+          st16(o + (size_t)p * a.eblocks * 512, make_uint4(w[0], w[1], w[2], w[3]));
+        }
       }
     }
-  }
-  if (!a.db) return;
+    if (!a.db) return;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) s_db[j][threadIdx.x] = db[j];
-  __syncthreads();
-  for (int e = threadIdx.x; e < a.E; e += kThreads) {
-    double s = 0.0;
-    for (int i = 0; i < step; ++i) s += s_db[e & 7][i * groups + (e >> 3)];
-    a.dbp[(size_t)blockIdx.x * a.E + e] = s;
+    for (int j = 0; j < 8; ++j) {
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) db[j] += __shfl_xor(db[j], o, 64);
+      if (tl == 0 && e0 + j < a.E) a.dbp[(size_t)blockIdx.x * a.E + e0 + j] = db[j];
+    }
   }
 }
 
@@ -269,16 +277,14 @@ __global__ __launch_bounds__(kThreads, NK <= 16 ? 2 : 1) void router_dx_bf16_ker
   const int t0 = (rb * kDxWaves + wave) * 32;
   bf16x8_t hi[NK], mid[NK];
   {
-    const int t = t0 + (lane & 31);
-    const bf16_t* p = a.parts + (size_t)t * a.etiles * 3 * a.ew;
+    const bool there = t0 < a.T;
+    const bf16_t* p = a.parts + (size_t)(t0 / 32) * 3 * a.eblocks * 512 + lane * 8;
 #pragma unroll
     for (int k = 0; k < NK; ++k) {
-      const int e = 16 * k + 8 * (lane >> 5);
-      const bf16_t* q = p + (e / a.ew) * 3 * a.ew + e % a.ew;
       uint4 u = make_uint4(0, 0, 0, 0), v = u;
-      if (t < a.T) {
-        u = ld16(q);
-        v = ld16(q + a.ew);
+      if (there) {
+        u = ld16(p + k * 512);
+        v = ld16(p + (size_t)(a.eblocks + k) * 512);
       }
       hi[k] = __builtin_bit_cast(bf16x8_t, u);
       mid[k] = __builtin_bit_cast(bf16x8_t, v);
@@ -376,22 +382,26 @@ __global__ __launch_bounds__(kThreads, NK <= 16 ? 2 : 1) void router_dx_bf16_ker
 
 // ------------------------------------------------------------------ bf16: dW
 // Tile EW experts x EN columns, eight waves of 64 x 64; LDS ring of NS stages
-// of 16 token rows, each [parts of EW experts | EN columns of x].  k-rows are
-// multiples of 256 bytes; chunk c of k-row r sits at c ^ 4 (r & 3).
+// of 16 token rows, each [3 parts][EW / 16 expert blocks of 512 bytes | 16
+// rows of EN columns of x].  Both operands are read with ds_read_b64_tr_b16:
+// in a 16-lane group lane a points at 8 bytes of token k + a/4, columns n + 4
+// (a%4)..+3, and lane i receives tokens k..k+3 of column n + i.  Placement so
+// that a half wave covers all banks: 16-byte chunk c of x row r at c ^ 4 (r &
+// 3); chunk (half h, token t) of expert block b at 16 h + (t + 4 h + 8 b) %
+// 16.
 template <int EW>
 struct DwCfg {
   static constexpr int WE = EW / 64, WN = 8 / WE;
   static constexpr int EN = 64 * WN;
-  static constexpr int RA = EW == 64 ? 512 : 6 * EW;   // bytes of a k-row of parts (64: padded)
-  static constexpr int RB = 2 * EN;
-  static constexpr int A_BYTES = kBK * RA, STAGE = kBK * (RA + RB);
-  static constexpr int NS = 160 * 1024 / STAGE > 6 ? 6 : (160 * 1024 - 1024) / STAGE;
+  static constexpr int RB = 2 * EN;                    // bytes of a row of x
+  static constexpr int A_BYTES = 3 * EW / 16 * 512, STAGE = A_BYTES + kBK * RB;
+  static constexpr int NS = (160 * 1024 - 1024) / STAGE > 6 ? 6 : (160 * 1024 - 1024) / STAGE;
   static constexpr int UNITS = STAGE / 1024;           // 1 KiB direct loads per stage
   static constexpr int Q = UNITS / 8, X = UNITS % 8;   // per wave; waves below X issue one more
   static_assert(STAGE % 1024 == 0 && A_BYTES % 1024 == 0 && NS >= 3, "ring");
 };
 
-__device__ __forceinline__ bf16x8_t frag_mn(const char* lds, int rb, int n0) {
+__device__ __forceinline__ bf16x8_t frag_x(const char* lds, int rb, int n0) {
   const int lane = threadIdx.x & 63, g = lane >> 4, li = lane & 15;
   const int n = n0 + 16 * (g & 1) + 4 * (li & 3), kb = 8 * (g >> 1) + (li >> 2);
   g2::v4s h[2];
@@ -400,6 +410,17 @@ __device__ __forceinline__ bf16x8_t frag_mn(const char* lds, int rb, int n0) {
     const int kr = kb + 4 * i, c = (n >> 3) ^ (4 * (kr & 3));
     h[i] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((g2::lds_v4s*)(lds + kr * rb + c * 16 + (n & 7) * 2));
   }
+  return __builtin_bit_cast(bf16x8_t, __builtin_shufflevector(h[0], h[1], 0, 1, 2, 3, 4, 5, 6, 7));
+}
+// 32 experts from block eb (even) of a part
+__device__ __forceinline__ bf16x8_t frag_parts(const char* lds, int eb) {
+  const int lane = threadIdx.x & 63, g = lane >> 4, li = lane & 15;
+  const int b = g & 1, half = (li & 3) >> 1, t = 8 * (g >> 1) + (li >> 2);
+  const char* base = lds + (eb + b) * 512 + half * 256 + (li & 1) * 8;
+  g2::v4s h[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    h[i] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((g2::lds_v4s*)(base + ((t + 4 * i + 4 * half + 8 * b) & 15) * 16));
   return __builtin_bit_cast(bf16x8_t, __builtin_shufflevector(h[0], h[1], 0, 1, 2, 3, 4, 5, 6, 7));
 }
 
@@ -441,64 +462,81 @@ __global__ __launch_bounds__(kBf16Threads, 2) void router_dw_bf16_kernel(RArgs a
   const int KT = (hi - lo + kBK - 1) / kBK;
   const unsigned lds0 = g2::lds_addr_of(smem);
   // This wave's units w, w + 8, ... of a stage: unit u is LDS bytes
-  // [1024 u, 1024 u + 1024), chunk positions 64 u + lane.  voff: the lane's
-  // byte offset from the stage's first row of parts (or of x).
+  // [1024 u, 1024 u + 1024), 16-byte positions 64 u + lane.  voff: the lane's
+  // byte offset from the stage's first block of parts (or row of x).
   constexpr int QM = C::Q + (C::X ? 1 : 0);
   const int nq = C::Q + (wave < C::X ? 1 : 0);
-  const int prow = a.etiles * 3 * EW;                  // elements per row of parts
   unsigned voff[QM];
-  int krow[QM];
+  int krow[QM];   // x units: the row of the stage
 #pragma unroll
   for (int j = 0; j < QM; ++j) {
     const int u = wave + 8 * j;
-    const bool isA = u * 1024 < C::A_BYTES;
-    const int pos = isA ? u * 64 + lane : (u * 1024 - C::A_BYTES) / 16 + lane;
-    const int cpr = (isA ? C::RA : C::RB) / 16;
-    krow[j] = pos / cpr;
-    int c = ((pos % cpr) ^ (4 * (krow[j] & 3))) * 8;
-    // the padding of 64-wide tiles and columns past d: any column will do,
-    // what comes of it is not stored
-    if (isA ? c >= 3 * EW : n0 + c >= a.d) c = 0;
-    voff[j] = (unsigned)(krow[j] * (isA ? prow : a.d) + c) * 2;
+    if (u * 1024 < C::A_BYTES) {
+      const int p = u / (EW / 32), eb = 2 * (u % (EW / 32)) + lane / 32, q = lane % 32;
+      const int h = q / 16, t = (q - 4 * h - 8 * (eb & 1)) & 15;
+      krow[j] = 0;
+      voff[j] = (unsigned)(p * a.eblocks + et * (EW / 16) + eb) * 1024 + h * 512 + t * 16;
+    } else {
+      const int pos = (u * 1024 - C::A_BYTES) / 16 + lane;
+      krow[j] = pos / (C::RB / 16);
+      int c = ((pos % (C::RB / 16)) ^ (4 * (krow[j] & 3))) * 8;
+      if (n0 + c >= a.d) c = 0;   // past d any column will do: its sums are not stored
+      voff[j] = (unsigned)(krow[j] * a.d + c) * 2;
+    }
   }
-  const char* parts = reinterpret_cast<const char*>(a.parts + (size_t)et * 3 * EW);
-  // the source and its row that the next stage begins with (uniform)
-  int xs = lo / a.T_src, xt = lo % a.T_src, filled = 0;
+  // The next stage to fill, all uniform: its first token, its block of parts,
+  // its first row of x (source xs, row xt), its slot.  Kept as running
+  // values: recomputed per stage they stood between the barrier and the
+  // matrix work, with a scalar load among them.
+  auto x_at = [&](int src, int row) {
+    return reinterpret_cast<const char*>(reinterpret_cast<const bf16_t*>(a.x.p[a.own_lo + src]) + (size_t)row * a.d + n0);
+  };
+  const size_t block = (size_t)3 * a.eblocks * 1024, x_step = (size_t)kBK * a.d * 2;
+  int t0 = lo, xs = lo / a.T_src, xt = lo % a.T_src, left = KT;
+  const char* pa = reinterpret_cast<const char*>(a.parts) + (size_t)(t0 / 32) * block + t0 / 16 % 2 * 256;
+  const char* px = KT > 0 ? x_at(xs, xt) : nullptr;
+  unsigned slot = lds0;
   auto issue = [&]() {
-    const int t0 = lo + filled * kBK;
-    const unsigned slot = lds0 + filled % C::NS * C::STAGE;
-    ++filled;
     if (t0 + kBK <= hi && xt + kBK <= a.T_src) {
       // sixteen rows of one source: uniform bases, no address arithmetic
-      const char* pa = parts + (size_t)t0 * prow * 2;
-      const char* px = reinterpret_cast<const char*>(reinterpret_cast<const bf16_t*>(a.x.p[a.own_lo + xs]) + (size_t)xt * a.d + n0);
 #pragma unroll
       for (int j = 0; j < QM; ++j) {
         if (j >= nq) continue;                          // wave-uniform
         const unsigned u = (wave + 8 * j) * 1024;
         load_lds16_at(u < C::A_BYTES ? pa : px, voff[j], slot + u);
       }
-      xt += kBK;
-      if (xt == a.T_src) xt = 0, ++xs;
-      return;
-    }
-    // the last rows, or rows of several sources: row by row, zeros past hi
+    } else {
+      // the last rows, or rows of several sources: row by row, zeros past hi
 #pragma unroll
-    for (int j = 0; j < QM; ++j) {
-      if (j >= nq) continue;
-      const unsigned u = (wave + 8 * j) * 1024;
-      const int t = t0 + krow[j];
-      const char* src = reinterpret_cast<const char*>(g2::g_zero);
-      if (t < hi) {
-        if (u < C::A_BYTES) src = parts + (size_t)t0 * prow * 2 + voff[j];
-        else src = reinterpret_cast<const char*>(s_x[a.own_lo + t / a.T_src] + (size_t)(t % a.T_src) * a.d + n0) +
-                   (voff[j] - (unsigned)krow[j] * a.d * 2);
+      for (int j = 0; j < QM; ++j) {
+        if (j >= nq) continue;
+        const unsigned u = (wave + 8 * j) * 1024;
+        if (u < C::A_BYTES) {
+          load_lds16_at(pa, voff[j], slot + u);
+          continue;
+        }
+        const int t = t0 + krow[j];
+        const char* src = reinterpret_cast<const char*>(g2::g_zero);
+        if (t < hi)
+          src = reinterpret_cast<const char*>(s_x[a.own_lo + t / a.T_src] + (size_t)(t % a.T_src) * a.d + n0) +
+                (voff[j] - (unsigned)krow[j] * a.d * 2);
+        g2::load_lds16(src, slot + u);
       }
-      g2::load_lds16(src, slot + u);
     }
-    xt += kBK;
-    xs += xt / a.T_src;
-    xt %= a.T_src;
+    slot = slot + C::STAGE == lds0 + C::NS * C::STAGE ? lds0 : slot + C::STAGE;
+    // past the last stage its tokens are loaded again into slots that nothing
+    // reads, so that every stage counts as many loads
+    if (--left > 0) {
+      t0 += kBK;
+      pa += t0 & 16 ? 256 : block - 256;
+      xt += kBK;
+      px += x_step;
+      if (xt >= a.T_src) {
+        xs += xt / a.T_src;
+        xt %= a.T_src;
+        px = x_at(xs, xt);
+      }
+    }
   };
   f32x16_t acc[2][2];
 #pragma unroll
@@ -508,28 +546,53 @@ __global__ __launch_bounds__(kBf16Threads, 2) void router_dw_bf16_kernel(RArgs a
 #pragma unroll
       for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
   const int we = wave / C::WN * 64, wn = wave % C::WN * 64;
-  for (int s = 0; s < C::NS - 1; ++s) issue();          // stages past KT read zeros
-  for (int kt = 0; kt < KT; ++kt) {
-    // this wave's loads of stage kt have landed (the NS - 2 later stages stay
-    // in flight); after the barrier everyone's have, and everyone is done
-    // with stage kt - 1, whose slot the next loads fill
-    if (wave < C::X) g2::wait_vmcnt_lgkm0<(C::NS - 2) * (C::Q + 1)>();
-    else g2::wait_vmcnt_lgkm0<(C::NS - 2) * C::Q>();
-    barrier();
-    issue();   // stage kt + NS - 1
+  struct Frags {
+    bf16x8_t a[3][2], b[2];
+  };
+  auto read = [&](int kt, Frags& f) {
     const char* A = smem + kt % C::NS * C::STAGE;
     const char* B = A + C::A_BYTES;
-    bf16x8_t fb[2];
 #pragma unroll
-    for (int j = 0; j < 2; ++j) fb[j] = frag_mn(B, C::RB, wn + 32 * j);
+    for (int j = 0; j < 2; ++j) f.b[j] = frag_x(B, C::RB, wn + 32 * j);
 #pragma unroll
     for (int p = 2; p >= 0; --p)
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const bf16x8_t fa = frag_mn(A, C::RA, p * EW + we + 32 * i);
+      for (int i = 0; i < 2; ++i) f.a[p][i] = frag_parts(A + p * (EW / 16) * 512, we / 16 + 2 * i);
+  };
+  auto stage = [&](int kt, const Frags& f, Frags& next) {
+    // this wave's loads of stage kt + 1 have landed (NS - 2 later stages stay
+    // in flight) and its fragments of stage kt are in registers; after the
+    // barrier that holds for everyone, so stage kt's slot can be filled again
+    // and the next fragments are read under this stage's matrix work
+    if (wave < C::X) g2::wait_vmcnt_lgkm0<(C::NS - 2) * (C::Q + 1)>();
+    else g2::wait_vmcnt_lgkm0<(C::NS - 2) * C::Q>();
+    barrier();
+    read(kt + 1, next);
+    auto mma = [&](int p) {
 #pragma unroll
-        for (int j = 0; j < 2; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa, fb[j], acc[i][j], 0, 0, 0);
-      }
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f.a[p][i], f.b[j], acc[i][j], 0, 0, 0);
+    };
+    mma(2);
+    g2::interleave_reads<4, 16, 0, 4>();
+    issue();
+    mma(1);
+    mma(0);
+  };
+  if (KT > 0) {
+    for (int s = 0; s < C::NS; ++s) issue();
+    if (wave < C::X) g2::wait_vmcnt_lgkm0<(C::NS - 1) * (C::Q + 1)>();
+    else g2::wait_vmcnt_lgkm0<(C::NS - 1) * C::Q>();
+    barrier();
+    Frags f0, f1;
+    read(0, f0);
+    int kt = 0;
+    for (; kt + 1 < KT; kt += 2) {
+      stage(kt, f0, f1);
+      stage(kt + 1, f1, f0);
+    }
+    if (kt < KT) stage(kt, f0, f1);
   }
   g2::wait_vmcnt_lgkm0<0>();   // no load of this workgroup outlives it
 #pragma unroll
@@ -547,10 +610,10 @@ __global__ __launch_bounds__(kBf16Threads, 2) void router_dw_bf16_kernel(RArgs a
 }
 
 // dW from the chunks' partial sums (the first dw_blocks workgroups: 64
-// 16-byte columns, four threads each adding every fourth chunk), and db: 32 experts per workgroup, eight threads an expert,
-// each adding every eighth partial sum.
+// 16-byte columns, four threads each adding every fourth chunk), and db: eight experts per workgroup, 32 threads an expert,
+// each adding every 32nd partial sum.
 __global__ __launch_bounds__(kThreads) void router_reduce_kernel(RArgs a, int dw_blocks) {
-  __shared__ double s_db[8][32];
+  __shared__ double s_db[32][8];
   if ((int)blockIdx.x < dw_blocks) {
     __shared__ float4 s_dw[4][64];
     const int c = threadIdx.x % 64, q = threadIdx.x / 64;
@@ -577,15 +640,17 @@ __global__ __launch_bounds__(kThreads) void router_reduce_kernel(RArgs a, int dw
     *reinterpret_cast<float4*>(a.dw + i) = s;
     return;
   }
-  const int c = threadIdx.x % 32, q = threadIdx.x / 32, e = ((int)blockIdx.x - dw_blocks) * 32 + c;
+  const int c = threadIdx.x % 8, q = threadIdx.x / 8, e = ((int)blockIdx.x - dw_blocks) * 8 + c;
   double s = 0.0;
-  if (e < a.E)
-    for (int i = q; i < a.db_parts; i += 8) s += a.dbp[(size_t)i * a.E + e];
+  if (e < a.E) {
+#pragma unroll 8
+    for (int i = q; i < a.db_parts; i += 32) s += a.dbp[(size_t)i * a.E + e];
+  }
   s_db[q][c] = s;
   __syncthreads();
   if (q == 0 && e < a.E) {
     s = a.add ? a.db[e] : 0.0;
-    for (int i = 0; i < 8; ++i) s += s_db[i][c];
+    for (int i = 0; i < 32; ++i) s += s_db[i][c];
     a.db[e] = (float)s;
   }
 }
@@ -620,9 +685,9 @@ Plan make_plan(int prec, int64_t T, int d, int E) {
   if (f32) {
     p.db_parts = p.chunks;
   } else {
-    p.split_rows = (T + 511) / 512 > 16 ? (T + 511) / 512 : 16;
-    p.db_parts = (int)((T + p.split_rows - 1) / p.split_rows);
-    p.parts = align256((size_t)T * p.etiles * 3 * p.ew * 2);
+    p.split_rows = (T + 512 * 32 - 1) / (512 * 32) * 32;
+    p.db_parts = T > 0 ? (int)((T + p.split_rows - 1) / p.split_rows) : 0;
+    p.parts = align256((size_t)((T + 31) / 32) * 3 * p.etiles * p.ew * 64);
   }
   p.dbp = align256((size_t)p.db_parts * E * 8);
   p.part = p.chunks > 1 ? align256((size_t)p.chunks * E * d * 4) : 0;
@@ -666,7 +731,7 @@ mok_status launch_router_bwd(const RouterBwdPlan& p, hipStream_t stream) {
   a.T = p.T, a.T_src = p.T_src > 0 ? p.T_src : 1, a.d = p.d, a.E = p.E, a.own_lo = p.own_lo;
   a.add = p.add;
   a.chunks = pl.chunks, a.chunk_rows = pl.chunk_rows;
-  a.ew = pl.ew, a.etiles = pl.etiles, a.split_rows = pl.split_rows, a.db_parts = pl.db_parts;
+  a.ew = pl.ew, a.etiles = pl.etiles, a.eblocks = pl.etiles * pl.ew / 16, a.split_rows = pl.split_rows, a.db_parts = pl.db_parts;
   char* ws = (char*)p.ws;
   a.part = pl.chunks > 1 ? (float*)(ws + pl.parts + pl.dbp) : nullptr;
   const dim3 blk(kThreads);
@@ -687,7 +752,7 @@ mok_status launch_router_bwd(const RouterBwdPlan& p, hipStream_t stream) {
     if (p.T > 0) {
       a.parts = p.want_dx || p.dw ? (bf16_t*)ws : nullptr;
       a.dbp = (double*)(ws + pl.parts);
-      hipLaunchKernelGGL(router_split_kernel, dim3((unsigned)pl.db_parts), blk, 0, stream, a);
+      hipLaunchKernelGGL(router_split_kernel, dim3((unsigned)pl.db_parts, pl.etiles * pl.ew / 64), blk, 0, stream, a);
       trace_mark(p.tr, "router_split", stream);
     }
     if (p.want_dx && p.T > 0) {
@@ -708,7 +773,7 @@ mok_status launch_router_bwd(const RouterBwdPlan& p, hipStream_t stream) {
   const bool dw_left = p.dw && a.part, db_left = p.db && (a.dbp || !f32);
   if (dw_left || db_left) {
     const unsigned dwb = dw_left ? (unsigned)(((size_t)p.E * p.d + 255) / 256) : 0;
-    const unsigned dbb = db_left ? (unsigned)(p.E + 31) / 32 : 0;
+    const unsigned dbb = db_left ? (unsigned)(p.E + 7) / 8 : 0;
     hipLaunchKernelGGL(router_reduce_kernel, dim3(dwb + dbb), blk, 0, stream, a, (int)dwb);
     trace_mark(p.tr, "router_reduce", stream);
   }
