@@ -29,7 +29,9 @@ namespace mok {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kKB = 32;     // fp32: contraction steps staged through LDS at a time
+constexpr int kTile = 64;   // fp32: tile side
+constexpr int kKB = 32;     // and contraction steps staged through LDS at a time
+constexpr int kPitch = kTile + 4;
 constexpr int kDxWaves = 4;
 constexpr int kBf16Threads = 512;   // eight waves in the dW product of bf16 layers
 constexpr int kBK = 16;             // token rows per LDS stage of dW
@@ -63,19 +65,17 @@ struct RArgs {
 __device__ __forceinline__ int acc_row(int r, int lane) { return (r >> 2) * 8 + (lane >> 5) * 4 + (r & 3); }
 
 // ------------------------------------------------------------------ fp32
-// Both products as C[m][n] = sum_k A(k, m) B(k, n) on tiles of 64 B x 64 B
-// (B = 1 or 2; four waves of 32 B x 32 B).  kKB steps of k at a time go
-// through LDS as [k][m] and [k][n]; the next block's global loads are in
+// Both products as C[m][n] = sum_k A(k, m) B(k, n) on 64 x 64 tiles, four
+// waves of 32 x 32 (128 x 128 measured no faster).  kKB steps of k at a time
+// go through LDS as [k][m] and [k][n]; the next block's global loads are in
 // registers while this one is multiplied.  dx: m = token, k = expert (dz
 // read along k); dW: m = expert, k = token.
-template <int B, bool DX>
+template <bool DX>
 __device__ __forceinline__ void f32_tile(const RArgs& a, int m0, int n0, int k_lo, int k_hi, int chunk, float* smem) {
-  constexpr int TILE = 64 * B, PITCH = TILE + 4;
-  constexpr int NU = TILE * kKB / 4 / kThreads;   // 16-byte units per thread and operand
-  float* sA = smem;
-  float* sB = smem + kKB * PITCH;
+  constexpr int NU = kTile * kKB / 4 / kThreads;   // 16-byte units per thread and operand
+  constexpr int BUF = 2 * kKB * kPitch;            // two LDS buffers, one barrier a block
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int wm = (wave >> 1) * 32 * B, wn = (wave & 1) * 32 * B;
+  const int wm = (wave >> 1) * 32, wn = (wave & 1) * 32;
   const bool wide = a.E % 4 == 0 && ((uintptr_t)a.dz & 15) == 0;
   const float* w = reinterpret_cast<const float*>(a.w);
   float4 ra[NU], rb[NU];
@@ -86,92 +86,77 @@ __device__ __forceinline__ void f32_tile(const RArgs& a, int m0, int n0, int k_l
                        e + 3 < a.E ? p[3] : 0.0f);
   };
   auto fetch = [&](int k0) {
+    // the block's tokens usually come from one source: one division for all
+    const int src = DX ? 0 : k0 / a.T_src, row = DX ? 0 : k0 % a.T_src;
+    const float* xb = nullptr;
+    if (!DX && a.dw && row + kKB <= a.T_src)
+      xb = reinterpret_cast<const float*>(a.x.p[a.own_lo + src]) + (size_t)row * a.d + n0;
 #pragma unroll
     for (int i = 0; i < NU; ++i) {
       const int u = tid + i * kThreads;
-      const int kr = u / (TILE / 4), c = u % (TILE / 4) * 4;   // k-row and column of an operand with k rows
+      const int kr = u / (kTile / 4), c = u % (kTile / 4) * 4;   // k-row and column of an operand with k rows
       const bool there = k0 + kr < k_hi;
       ra[i] = rb[i] = make_float4(0, 0, 0, 0);
       if constexpr (DX) {
         const int t = m0 + u / (kKB / 4), e = k0 + u % (kKB / 4) * 4;
         if (t < a.T) ra[i] = dz4(t, e);
-        if (there && n0 + c < a.d) rb[i] = *reinterpret_cast<const float4*>(w + (size_t)(k0 + kr) * a.d + n0 + c);
+        if (there) rb[i] = *reinterpret_cast<const float4*>(w + (size_t)(k0 + kr) * a.d + n0 + c);
       } else if (there) {
         const int t = k0 + kr;
         ra[i] = dz4(t, m0 + c);
-        if (a.dw && n0 + c < a.d)
+        if (xb) rb[i] = *reinterpret_cast<const float4*>(xb + (size_t)kr * a.d + c);
+        else if (a.dw)
           rb[i] = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(a.x.p[a.own_lo + t / a.T_src]) +
                                                    (size_t)(t % a.T_src) * a.d + n0 + c);
       }
     }
   };
-  auto deposit = [&]() {
+  auto deposit = [&](float* sA, float* sB) {
 #pragma unroll
     for (int i = 0; i < NU; ++i) {
       const int u = tid + i * kThreads;
-      const int kr = u / (TILE / 4), c = u % (TILE / 4) * 4;
+      const int kr = u / (kTile / 4), c = u % (kTile / 4) * 4;
       if constexpr (DX) {
         const int m = u / (kKB / 4), k = u % (kKB / 4) * 4;
-        sA[k * PITCH + m] = ra[i].x;
-        sA[(k + 1) * PITCH + m] = ra[i].y;
-        sA[(k + 2) * PITCH + m] = ra[i].z;
-        sA[(k + 3) * PITCH + m] = ra[i].w;
+        sA[k * kPitch + m] = ra[i].x;
+        sA[(k + 1) * kPitch + m] = ra[i].y;
+        sA[(k + 2) * kPitch + m] = ra[i].z;
+        sA[(k + 3) * kPitch + m] = ra[i].w;
       } else {
-        *reinterpret_cast<float4*>(sA + kr * PITCH + c) = ra[i];
+        *reinterpret_cast<float4*>(sA + kr * kPitch + c) = ra[i];
       }
-      *reinterpret_cast<float4*>(sB + kr * PITCH + c) = rb[i];
+      *reinterpret_cast<float4*>(sB + kr * kPitch + c) = rb[i];
     }
   };
-  const bool bias = !DX && a.db && n0 == 0 && tid < TILE;
+  const bool bias = !DX && a.db && n0 == 0 && tid < kTile;
   double bsum = 0.0;
-  f32x16_t acc[B][B];
-#pragma unroll
-  for (int i = 0; i < B; ++i)
-#pragma unroll
-    for (int j = 0; j < B; ++j)
-#pragma unroll
-      for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
+  f32x16_t acc = {};
   const int c = lane & 31, h = lane >> 5;
   if (k_lo < k_hi) fetch(k_lo);
-  for (int k0 = k_lo; k0 < k_hi; k0 += kKB) {
-    deposit();
+  for (int k0 = k_lo, buf = 0; k0 < k_hi; k0 += kKB, buf ^= 1) {
+    // a buffer's readers of two blocks ago have passed the last barrier
+    float* sA = smem + buf * BUF;
+    float* sB = sA + kKB * kPitch;
+    deposit(sA, sB);
     __syncthreads();
     if (k_hi - k0 > kKB) fetch(k0 + kKB);
 #pragma unroll
-    for (int k = 0; k < kKB; k += 2) {
-      float fa[B], fb[B];
-#pragma unroll
-      for (int i = 0; i < B; ++i) {
-        fa[i] = sA[(k + h) * PITCH + wm + 32 * i + c];
-        fb[i] = sB[(k + h) * PITCH + wn + 32 * i + c];
-      }
-#pragma unroll
-      for (int i = 0; i < B; ++i)
-#pragma unroll
-        for (int j = 0; j < B; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x2f32(fa[i], fb[j], acc[i][j], 0, 0, 0);
-    }
+    for (int k = 0; k < kKB; k += 2)
+      acc = __builtin_amdgcn_mfma_f32_32x32x2f32(sA[(k + h) * kPitch + wm + c], sB[(k + h) * kPitch + wn + c], acc, 0, 0, 0);
     if (bias)
-      for (int k = 0; k < kKB; ++k) bsum += (double)sA[k * PITCH + tid];
-    __syncthreads();
+      for (int k = 0; k < kKB; ++k) bsum += (double)sA[k * kPitch + tid];
   }
+  const int n = n0 + wn + c;   // d is a multiple of the tile
 #pragma unroll
-  for (int i = 0; i < B; ++i)
-#pragma unroll
-    for (int r = 0; r < 16; ++r) {
-      const int m = m0 + wm + 32 * i + acc_row(r, lane);
-      if (m >= (DX ? a.T : a.E)) continue;
-      float* row = nullptr;
-      if constexpr (DX) row = reinterpret_cast<float*>(a.d_x.p[a.own_lo + m / a.T_src]) + (size_t)(m % a.T_src) * a.d;
-      else if (a.part) row = a.part + ((size_t)chunk * a.E + m) * a.d;
-      else if (a.dw) row = a.dw + (size_t)m * a.d;
-      const bool add = a.add && (DX || !a.part);
-#pragma unroll
-      for (int j = 0; j < B; ++j) {
-        const int n = n0 + wn + 32 * j + c;
-        if (!row || n >= a.d) continue;
-        row[n] = add ? row[n] + acc[i][j][r] : acc[i][j][r];
-      }
-    }
+  for (int r = 0; r < 16; ++r) {
+    const int m = m0 + wm + acc_row(r, lane);
+    if (m >= (DX ? a.T : a.E)) continue;
+    float* row = nullptr;
+    if constexpr (DX) row = reinterpret_cast<float*>(a.d_x.p[a.own_lo + m / a.T_src]) + (size_t)(m % a.T_src) * a.d;
+    else if (a.part) row = a.part + ((size_t)chunk * a.E + m) * a.d;
+    else if (a.dw) row = a.dw + (size_t)m * a.d;
+    if (row) row[n] = a.add && (DX || !a.part) ? row[n] + acc[r] : acc[r];
+  }
   if (bias && m0 + tid < a.E) {
     const int e = m0 + tid;
     if (a.dbp) a.dbp[(size_t)chunk * a.E + e] = bsum;
@@ -179,23 +164,21 @@ __device__ __forceinline__ void f32_tile(const RArgs& a, int m0, int n0, int k_l
   }
 }
 
-// The tiles of both products in one launch: the first dx_tiles workgroups
-// dx, the others dW (chunk by chunk of tokens).
-template <int B>
-__global__ __launch_bounds__(kThreads) void router_f32_kernel(RArgs a, int64_t dx_tiles) {
-  constexpr int TILE = 64 * B;
-  __shared__ __attribute__((aligned(16))) float smem[2 * kKB * (TILE + 4)];
-  const int nt = (a.d + TILE - 1) / TILE;
+// The tiles of both products in one launch: the first dw_tiles workgroups dW
+// (chunk by chunk of tokens: the longer ones), the others dx.
+__global__ __launch_bounds__(kThreads) void router_f32_kernel(RArgs a, int64_t dw_tiles) {
+  __shared__ __attribute__((aligned(16))) float smem[4 * kKB * kPitch];
+  const int nt = a.d / kTile;
   int64_t b = blockIdx.x;
-  if (b < dx_tiles) {
-    f32_tile<B, true>(a, (int)(b / nt) * TILE, (int)(b % nt) * TILE, 0, a.E, 0, smem);
+  if (b >= dw_tiles) {
+    b -= dw_tiles;
+    f32_tile<true>(a, (int)(b / nt) * kTile, (int)(b % nt) * kTile, 0, a.E, 0, smem);
     return;
   }
-  b -= dx_tiles;
-  const int n = a.dw ? nt : 1, me = (a.E + TILE - 1) / TILE, tile = (int)(b % (n * me)), chunk = (int)(b / (n * me));
+  const int n = a.dw ? nt : 1, me = (a.E + kTile - 1) / kTile, tile = (int)(b % (n * me)), chunk = (int)(b / (n * me));
   const int64_t lo = (int64_t)chunk * a.chunk_rows;
-  f32_tile<B, false>(a, tile / n * TILE, tile % n * TILE, (int)min(lo, (int64_t)a.T),
-                     (int)min(lo + a.chunk_rows, (int64_t)a.T), chunk, smem);
+  f32_tile<false>(a, tile / n * kTile, tile % n * kTile, (int)min(lo, (int64_t)a.T),
+                  (int)min(lo + a.chunk_rows, (int64_t)a.T), chunk, smem);
 }
 
 // ------------------------------------------------------------------ bf16: split
@@ -721,7 +704,6 @@ struct Plan {
   int chunks = 1, ew = 0, etiles = 0, db_parts = 0;
   int64_t chunk_rows = 0, split_rows = 0;
   size_t parts = 0, dbp = 0, part = 0, total = 0;
-  int b32 = 1;                 // fp32: 32-blocks per wave and side
 };
 
 Plan make_plan(int prec, int64_t T, int d, int E) {
@@ -730,13 +712,7 @@ Plan make_plan(int prec, int64_t T, int d, int E) {
   p.ew = expert_tile(E);
   p.etiles = (E + p.ew - 1) / p.ew;
   const int en = 64 * 8 * 64 / p.ew;
-  // fp32: 128 x 128 tiles where they fill the chip four times over, else
-  // 64 x 64 (FP32TILE)
-  const int64_t big = ((T + 127) / 128 + (E + 127) / 128) * ((d + 127) / 128);
-  p.b32 = big >= 1024 && E > 64 ? 2 : 1;
-  const int side = 64 * p.b32;
-  const int64_t tiles = f32 ? (int64_t)((d + side - 1) / side) * ((E + side - 1) / side)
-                            : (int64_t)((d + en - 1) / en) * p.etiles;
+  const int64_t tiles = f32 ? (int64_t)(d / kTile) * ((E + kTile - 1) / kTile) : (int64_t)((d + en - 1) / en) * p.etiles;
   const int64_t least = f32 ? 64 : 128, unit = f32 ? kKB : kBK;
   int64_t c = (f32 ? 1024 : 256) / tiles;
   if (c > (T + least - 1) / least) c = (T + least - 1) / least;
@@ -799,12 +775,11 @@ mok_status launch_router_bwd(const RouterBwdPlan& p, hipStream_t stream) {
   const bool f32 = p.prec == MOK_F32;
   if (f32) {
     a.dbp = pl.chunks > 1 ? (double*)ws : nullptr;
-    const int64_t side = 64 * pl.b32, nt = (p.d + side - 1) / side;
-    const int64_t dx = p.want_dx ? nt * (((int64_t)p.T + side - 1) / side) : 0;
-    const int64_t dw = p.dw || p.db ? (p.dw ? nt : 1) * ((p.E + side - 1) / side) * a.chunks : 0;
+    const int64_t nt = p.d / kTile;
+    const int64_t dx = p.want_dx ? nt * (((int64_t)p.T + kTile - 1) / kTile) : 0;
+    const int64_t dw = p.dw || p.db ? (p.dw ? nt : 1) * ((p.E + kTile - 1) / kTile) * a.chunks : 0;
     if (dx + dw > 0) {
-      if (pl.b32 == 2) hipLaunchKernelGGL(router_f32_kernel<2>, dim3((unsigned)(dx + dw)), blk, 0, stream, a, dx);
-      else hipLaunchKernelGGL(router_f32_kernel<1>, dim3((unsigned)(dx + dw)), blk, 0, stream, a, dx);
+      hipLaunchKernelGGL(router_f32_kernel, dim3((unsigned)(dx + dw)), blk, 0, stream, a, dw);
       trace_mark(p.tr, "router_f32", stream);
     }
   } else {
