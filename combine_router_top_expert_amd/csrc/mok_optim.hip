@@ -17,7 +17,8 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kLane = 8;                       // elements per lane at a time
 constexpr int kStep = kThreads * kLane;        // elements per workgroup step
-constexpr int kPiece = 4 * kStep;              // elements per workgroup
+constexpr int kPiece = 4 * kStep;              // elements per workgroup: of the norm and of fp32 moments,
+constexpr int kPiece8 = 2 * kStep;             // of 8-bit ones (3 % faster over many tensors; fp32 1 % slower)
 constexpr int kBatch = 50;                     // tensors per launch of the step
 constexpr int kNormBatch = 192;                // and of the norm
 constexpr int kNormWgs = 2048;                 // workgroups of the norm per launch at most
@@ -395,30 +396,31 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(Batch b, AdamArgs a) {
   }
   const int ti = find_tensor(b, blockIdx.x);
   const Desc& d = b.d[ti];
-  const int64_t base = (int64_t)(blockIdx.x - b.first[ti]) * kPiece;
   const uint64_t key = mix64(mix64(a.seed + (d.tag >> 4)) + (uint64_t)step * kGold);
-  for (int it = 0; it < kPiece / kStep; ++it) {
-    const int64_t at = base + (int64_t)it * kStep;
-    if (at >= d.n) break;
-    const int64_t i = at + threadIdx.x * kLane;
-    if (d.tag & kEight) adam_step<true>(d, a, i, scale, lr, inv_bc1, inv_sbc2, key);
+  const bool eight = d.tag & kEight;
+  const int piece = eight ? kPiece8 : kPiece;
+  const int64_t base = (int64_t)(blockIdx.x - b.first[ti]) * piece;
+  for (int at = 0; at < piece; at += kStep) {
+    if (base + at >= d.n) break;
+    const int64_t i = base + at + threadIdx.x * kLane;
+    if (eight) adam_step<true>(d, a, i, scale, lr, inv_bc1, inv_sbc2, key);
     else adam_step<false>(d, a, i, scale, lr, inv_bc1, inv_sbc2, key);
   }
 }
 
 uint32_t norm_grid(uint32_t pieces) { return pieces < kNormWgs ? pieces : kNormWgs; }
-int64_t pieces_of(int64_t n) { return (n + kPiece - 1) / kPiece; }
-
 // Fills batches of at most N non-empty tensors and at most 2^30 pieces (a
 // tensor never splits over batches) and calls run(batch, pieces) for each;
-// put(descriptor, tensor, place) writes one.
-template <class B, int N, class Put, class Run>
-bool each_batch(int n_params, const mok_param* params, Put put, Run run) {
+// put(descriptor, tensor, place) writes one; piece(tensor) is its elements
+// per workgroup.
+template <class B, int N, class Piece, class Put, class Run>
+bool each_batch(int n_params, const mok_param* params, Piece piece, Put put, Run run) {
   B b = {};
   uint64_t pieces = 0;
   for (int t = 0; t < n_params; ++t) {
     if (params[t].n == 0) continue;
-    const uint64_t k = (uint64_t)pieces_of(params[t].n);
+    const int per = piece(params[t]);
+    const uint64_t k = (uint64_t)(params[t].n + per - 1) / per;
     if (b.count == N || (b.count && pieces + k > (1u << 30))) {
       if (!run(b, (uint32_t)pieces)) return false;
       b.count = 0;
@@ -436,7 +438,7 @@ bool each_batch(int n_params, const mok_param* params, Put put, Run run) {
 
 size_t grad_norm_ws_bytes(int n_params, const mok_param* params) {
   size_t parts = 1;
-  each_batch<NormBatch, kNormBatch>(n_params, params, [](NormDesc&, const mok_param&, int) {},
+  each_batch<NormBatch, kNormBatch>(n_params, params, [](const mok_param&) { return kPiece; }, [](NormDesc&, const mok_param&, int) {},
                                     [&](const NormBatch&, uint32_t pieces) {
                                       parts += norm_grid(pieces);
                                       return true;
@@ -458,7 +460,7 @@ mok_status launch_grad_norm(int n_params, const mok_param* params, float max_nor
     done += grid;
     return hipGetLastError() == hipSuccess;
   };
-  if (!each_batch<NormBatch, kNormBatch>(n_params, params, put, run)) return MOK_EDEVICE;
+  if (!each_batch<NormBatch, kNormBatch>(n_params, params, [](const mok_param&) { return kPiece; }, put, run)) return MOK_EDEVICE;
   hipLaunchKernelGGL(norm_total_kernel, dim3(1), dim3(1024), 0, stream, part, done, max_norm, out);
   return hipGetLastError() == hipSuccess ? MOK_OK : MOK_EDEVICE;
 }
@@ -485,11 +487,12 @@ mok_status launch_adamw(int n_params, const mok_param* params, const mok_adamw_a
     d.tag = (uint32_t)t << 4 | (q.p_type == MOK_BF16 ? kPBf16 : 0) | (q.g_type == MOK_BF16 ? kGBf16 : 0) |
             (q.state_bits == 8 ? kEight : 0) | (all % 16 == 0 ? kWide : 0);
   };
+  auto piece = [](const mok_param& q) { return q.state_bits == 8 ? kPiece8 : kPiece; };
   auto run = [&](const Batch& b, uint32_t pieces) {
     hipLaunchKernelGGL(adamw_kernel, dim3(pieces), dim3(kThreads), 0, stream, b, a);
     return hipGetLastError() == hipSuccess;
   };
-  return each_batch<Batch, kBatch>(n_params, params, put, run) ? MOK_OK : MOK_EDEVICE;
+  return each_batch<Batch, kBatch>(n_params, params, piece, put, run) ? MOK_OK : MOK_EDEVICE;
 }
 
 }  // namespace mok
