@@ -397,14 +397,19 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(Batch b, AdamArgs a) {
   const int ti = find_tensor(b, blockIdx.x);
   const Desc& d = b.d[ti];
   const uint64_t key = mix64(mix64(a.seed + (d.tag >> 4)) + (uint64_t)step * kGold);
-  const bool eight = d.tag & kEight;
-  const int piece = eight ? kPiece8 : kPiece;
-  const int64_t base = (int64_t)(blockIdx.x - b.first[ti]) * piece;
-  for (int at = 0; at < piece; at += kStep) {
-    if (base + at >= d.n) break;
-    const int64_t i = base + at + threadIdx.x * kLane;
-    if (eight) adam_step<true>(d, a, i, scale, lr, inv_bc1, inv_sbc2, key);
-    else adam_step<false>(d, a, i, scale, lr, inv_bc1, inv_sbc2, key);
+  const int64_t place = blockIdx.x - b.first[ti];
+  if (d.tag & kEight) {
+    for (int it = 0; it < kPiece8 / kStep; ++it) {
+      const int64_t at = place * kPiece8 + (int64_t)it * kStep;
+      if (at >= d.n) break;
+      adam_step<true>(d, a, at + threadIdx.x * kLane, scale, lr, inv_bc1, inv_sbc2, key);
+    }
+  } else {
+    for (int it = 0; it < kPiece / kStep; ++it) {
+      const int64_t at = place * kPiece + (int64_t)it * kStep;
+      if (at >= d.n) break;
+      adam_step<false>(d, a, at + threadIdx.x * kLane, scale, lr, inv_bc1, inv_sbc2, key);
+    }
   }
 }
 

@@ -33,7 +33,8 @@ constexpr int kTile = 64;   // fp32: tile side
 constexpr int kKB = 32;     // and contraction steps staged through LDS at a time
 constexpr int kPitch = kTile + 4;
 constexpr int kDxWaves = 4;
-constexpr int kBf16Threads = 512;   // eight waves in the dW product of bf16 layers
+constexpr int kDwWaves = 4;         // dW: two workgroups per CU (one of eight waves: 54 against 49 us)
+constexpr int kBf16Threads = 64 * kDwWaves;
 constexpr int kBK = 16;             // token rows per LDS stage of dW
 
 struct RArgs {
@@ -55,7 +56,7 @@ struct RArgs {
   // and expert tiles
   bf16_t* parts;
   int ew, etiles;      // experts per tile (64, 128 or 256) and tiles
-  int eblocks;         // etiles * ew / 16
+  int eblocks;         // blocks of 16 experts in the parts
   int64_t split_rows;  // token rows per workgroup of the split
   int db_parts;        // partial sums of db per expert
   int n_chunks;        // column chunks of dx, each a workgroup per row block
@@ -418,7 +419,7 @@ __global__ __launch_bounds__(kThreads, NK <= 16 ? 2 : 1) void router_dx_bf16_ker
 }
 
 // ------------------------------------------------------------------ bf16: dW
-// Tile EW experts x EN columns, eight waves of 64 x 64; LDS ring of NS stages
+// Tile EW experts x EN columns, four waves of 64 x 64; LDS ring of NS stages
 // of 16 token rows, each [3 parts][EW / 16 expert blocks of 512 bytes | 16
 // rows of EN columns of x].  Both operands are read with ds_read_b64_tr_b16:
 // in a 16-lane group lane a points at 8 bytes of token k + a/4, columns n + 4
@@ -428,13 +429,14 @@ __global__ __launch_bounds__(kThreads, NK <= 16 ? 2 : 1) void router_dx_bf16_ker
 // 16.
 template <int EW>
 struct DwCfg {
-  static constexpr int WE = EW / 64, WN = 8 / WE;
+  static constexpr int WE = EW / 64, WN = kDwWaves / WE;
   static constexpr int EN = 64 * WN;
   static constexpr int RB = 2 * EN;                    // bytes of a row of x
   static constexpr int A_BYTES = 3 * EW / 16 * 512, STAGE = A_BYTES + kBK * RB;
-  static constexpr int NS = (160 * 1024 - 1024) / STAGE > 6 ? 6 : (160 * 1024 - 1024) / STAGE;
+  static constexpr int LDS = 160 * 1024 * kDwWaves / 8 - 1024;     // eight waves per CU
+  static constexpr int NS = LDS / STAGE > 6 ? 6 : LDS / STAGE;
   static constexpr int UNITS = STAGE / 1024;           // 1 KiB direct loads per stage
-  static constexpr int Q = UNITS / 8, X = UNITS % 8;   // per wave; waves below X issue one more
+  static constexpr int Q = UNITS / kDwWaves, X = UNITS % kDwWaves;   // per wave; waves below X issue one more
   static_assert(STAGE % 1024 == 0 && A_BYTES % 1024 == 0 && NS >= 3, "ring");
 };
 
@@ -507,7 +509,7 @@ __global__ __launch_bounds__(kBf16Threads, 2) void router_dw_bf16_kernel(RArgs a
   int krow[QM];   // x units: the row of the stage
 #pragma unroll
   for (int j = 0; j < QM; ++j) {
-    const int u = wave + 8 * j;
+    const int u = wave + kDwWaves * j;
     if (u * 1024 < C::A_BYTES) {
       const int p = u / (EW / 32), eb = 2 * (u % (EW / 32)) + lane / 32, q = lane % 32;
       const int h = q / 16, t = (q - 4 * h - 8 * (eb & 1)) & 15;
@@ -539,7 +541,7 @@ __global__ __launch_bounds__(kBf16Threads, 2) void router_dw_bf16_kernel(RArgs a
 #pragma unroll
       for (int j = 0; j < QM; ++j) {
         if (j >= nq) continue;                          // wave-uniform
-        const unsigned u = (wave + 8 * j) * 1024;
+        const unsigned u = (wave + kDwWaves * j) * 1024;
         load_lds16_at(u < C::A_BYTES ? pa : px, voff[j], slot + u);
       }
     } else {
@@ -547,7 +549,7 @@ __global__ __launch_bounds__(kBf16Threads, 2) void router_dw_bf16_kernel(RArgs a
 #pragma unroll
       for (int j = 0; j < QM; ++j) {
         if (j >= nq) continue;
-        const unsigned u = (wave + 8 * j) * 1024;
+        const unsigned u = (wave + kDwWaves * j) * 1024;
         if (u < C::A_BYTES) {
           load_lds16_at(pa, voff[j], slot + u);
           continue;
@@ -694,7 +696,11 @@ __global__ __launch_bounds__(kThreads) void router_reduce_kernel(RArgs a, int dw
 
 size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
-int expert_tile(int E) { return E <= 64 ? 64 : E <= 128 ? 128 : 256; }
+// Experts of a dW tile (128, or 64 where fewer experts are padded: both within
+// 2 % on 256 experts; 256 was 5 % slower), and experts of the parts
+// of dz: a power of two from 64 on, so that dx has whole operands.
+int expert_tile(int E) { return (E + 63) / 64 % 2 ? 64 : 128; }
+int padded_experts(int E) { return E <= 64 ? 64 : E <= 128 ? 128 : E <= 256 ? 256 : 512; }
 
 // Token chunks of the dW product and the workspace that follows from them.
 // fp32: workgroups for four per CU, at least 64 tokens each.  bf16: one
@@ -711,10 +717,10 @@ Plan make_plan(int prec, int64_t T, int d, int E) {
   const bool f32 = prec == MOK_F32;
   p.ew = expert_tile(E);
   p.etiles = (E + p.ew - 1) / p.ew;
-  const int en = 64 * 8 * 64 / p.ew;
+  const int en = 64 * kDwWaves * 64 / p.ew;
   const int64_t tiles = f32 ? (int64_t)(d / kTile) * ((E + kTile - 1) / kTile) : (int64_t)((d + en - 1) / en) * p.etiles;
   const int64_t least = f32 ? 64 : 128, unit = f32 ? kKB : kBK;
-  int64_t c = (f32 ? 1024 : 256) / tiles;
+  int64_t c = (f32 ? 1024 : 256 * 8 / kDwWaves) / tiles;
   if (c > (T + least - 1) / least) c = (T + least - 1) / least;
   if (c < 1) c = 1;
   p.chunk_rows = ((T + c - 1) / c + unit - 1) / unit * unit;
@@ -724,7 +730,7 @@ Plan make_plan(int prec, int64_t T, int d, int E) {
   } else {
     p.split_rows = (T + 512 * 32 - 1) / (512 * 32) * 32;
     p.db_parts = T > 0 ? (int)((T + p.split_rows - 1) / p.split_rows) : 0;
-    p.parts = align256((size_t)((T + 31) / 32) * 3 * p.etiles * p.ew * 64);
+    p.parts = align256((size_t)((T + 31) / 32) * 3 * padded_experts(E) * 64);
   }
   p.dbp = align256((size_t)p.db_parts * E * 8);
   p.part = p.chunks > 1 ? align256((size_t)p.chunks * E * d * 4) : 0;
@@ -768,7 +774,7 @@ mok_status launch_router_bwd(const RouterBwdPlan& p, hipStream_t stream) {
   a.T = p.T, a.T_src = p.T_src > 0 ? p.T_src : 1, a.d = p.d, a.E = p.E, a.own_lo = p.own_lo;
   a.add = p.add;
   a.chunks = pl.chunks, a.chunk_rows = pl.chunk_rows;
-  a.ew = pl.ew, a.etiles = pl.etiles, a.eblocks = pl.etiles * pl.ew / 16, a.split_rows = pl.split_rows, a.db_parts = pl.db_parts;
+  a.ew = pl.ew, a.etiles = pl.etiles, a.eblocks = padded_experts(p.E) / 16, a.split_rows = pl.split_rows, a.db_parts = pl.db_parts;
   char* ws = (char*)p.ws;
   a.part = pl.chunks > 1 ? (float*)(ws + pl.parts + pl.dbp) : nullptr;
   const dim3 blk(kThreads);
@@ -786,7 +792,7 @@ mok_status launch_router_bwd(const RouterBwdPlan& p, hipStream_t stream) {
     if (p.T > 0) {
       a.parts = p.want_dx || p.dw ? (bf16_t*)ws : nullptr;
       a.dbp = (double*)(ws + pl.parts);
-      hipLaunchKernelGGL(router_split_kernel, dim3((unsigned)pl.db_parts, pl.etiles * pl.ew / 64), blk, 0, stream, a);
+      hipLaunchKernelGGL(router_split_kernel, dim3((unsigned)pl.db_parts, a.eblocks / 4), blk, 0, stream, a);
       trace_mark(p.tr, "router_split", stream);
     }
     if (p.want_dx && p.T > 0) {
@@ -798,8 +804,7 @@ mok_status launch_router_bwd(const RouterBwdPlan& p, hipStream_t stream) {
     }
     if (p.dw) {
       if (a.ew == 64) launch_dw<64>(a, stream);
-      else if (a.ew == 128) launch_dw<128>(a, stream);
-      else launch_dw<256>(a, stream);
+      else launch_dw<128>(a, stream);
       trace_mark(p.tr, "router_dw", stream);
     }
   }
