@@ -924,7 +924,7 @@ mok_status mok_balance_fwd(const mok_config* cfg, int32_t T, const mok_balance* 
                            float* prob, int32_t* n_tok, float* loss, void* ws,
                            int32_t* dev_status, void* stream) {
   if (!valid_balance(cfg, T, bal)) return MOK_EINVAL;
-  if (T > 0 && (!logits || !topk_idx)) return MOK_EINVAL;
+  if (T > 0 && (!logits || !topk_idx || !aligned(logits, 4) || !aligned(topk_idx, 4))) return MOK_EINVAL;
   if (!counts || !prob || !n_tok || !loss || !ws || !aligned(ws, 16)) return MOK_EINVAL;
   trace_mark(cfg->trace, "start", (hipStream_t)stream);
   return launch_balance_fwd(T, cfg->E, cfg->k, balance_groups(bal), *bal, logits, topk_idx, counts,
@@ -938,6 +938,7 @@ mok_status mok_balance_bwd(const mok_config* cfg, int32_t T, const mok_balance* 
   if (!valid_balance(cfg, T, bal)) return MOK_EINVAL;
   if (T == 0) return MOK_OK;
   if (!logits || !counts || !n_tok || !d_logits) return MOK_EINVAL;
+  if (!aligned(logits, 4) || !aligned(d_logits, 4) || !aligned(d_loss, 4)) return MOK_EINVAL;
   trace_mark(cfg->trace, "start", (hipStream_t)stream);
   return launch_balance_bwd(T, cfg->E, cfg->k, balance_groups(bal), *bal, logits, counts, n_tok,
                             d_loss, d_logits, dev_status, (hipStream_t)stream, cfg->trace);
@@ -953,6 +954,7 @@ mok_status mok_router_bwd(const mok_config* cfg, int32_t own_lo, int32_t own_n,
                           void* const* d_x, float* dw_router, float* d_bias, int32_t accumulate,
                           void* ws, void* stream) {
   if (!valid_cfg(cfg) || !own_range_ok(cfg, own_lo, own_n)) return MOK_EINVAL;
+  if (cfg->d > 1 << 26) return MOK_EINVAL;   // byte offsets within 16 token rows fit 32 bits
   const int64_t T = (int64_t)own_n * cfg->T_src;
   if (T > 0 && (!d_logits || !aligned(d_logits, 4))) return MOK_EINVAL;
   if (!ws || !aligned(ws, 16) || !aligned(dw_router, 16) || !aligned(d_bias, 4)) return MOK_EINVAL;
@@ -993,7 +995,8 @@ size_t mok_grad_norm_ws_bytes(int32_t n_params, const mok_param* params) {
 
 mok_status mok_grad_norm(int32_t n_params, const mok_param* params, float max_norm, float* out,
                          void* ws, void* stream) {
-  if (!valid_grads(n_params, params) || !out || !ws || !aligned(ws, 8)) return MOK_EINVAL;
+  if (!valid_grads(n_params, params) || !out || !aligned(out, 4) || !ws || !aligned(ws, 8))
+    return MOK_EINVAL;
   return launch_grad_norm(n_params, params, max_norm, out, ws, (hipStream_t)stream);
 }
 
@@ -1004,6 +1007,8 @@ mok_status mok_adamw(int32_t n_params, const mok_param* params, const mok_adamw_
       !(args->eps >= 0.0) || !(args->lr >= 0.0))
     return MOK_EINVAL;
   if (!args->dev_step && args->step < 1) return MOK_EINVAL;
+  if (!aligned(args->dev_scale, 4) || !aligned(args->dev_lr, 8) || !aligned(args->dev_step, 8))
+    return MOK_EINVAL;
   if (args->random_params != 0 && args->random_params != 1) return MOK_EINVAL;
   return launch_adamw(n_params, params, *args, (hipStream_t)stream);
 }

@@ -207,10 +207,10 @@ class MoELayer:
         [G+2]."""
         if self.logits is None:
             raise RuntimeError("balance_loss needs MoELayer(keep_logits=True)")
-        T, dev = self.own_n * self.T_src, self.device
+        T, dev = self.own_n * self.T_src, self.logits.device
         G = 0 if group_offsets is None else group_offsets.numel() - 1
         for t, dt, n in ((group_offsets, torch.int32, None), (token_mask, torch.uint8, T)):
-            if t is not None and (t.dtype != dt or not t.is_contiguous() or t.device.type != dev.type
+            if t is not None and (t.dtype != dt or not t.is_contiguous() or t.device != dev
                                   or (n is not None and t.numel() != n) or t.numel() < 1):
                 raise ValueError(f"contiguous {dt} tensor on {dev} expected, got {t.dtype} {tuple(t.shape)}")
         if group_offsets is not None and G < 1:
@@ -235,6 +235,8 @@ class MoELayer:
         """Adds the gradient of d_loss[0] * balance loss + d_loss[1] * z-loss
         (d_loss fp32 [2] on the device, None = ones) to d_x and dw_router,
         after backward()."""
+        if getattr(self, "_bal", None) is None or not self.with_bwd:
+            raise RuntimeError("balance_backward needs balance_loss and backward before it")
         T, lo = self.own_n * self.T_src, self.own_lo * self.T_src
         if getattr(self, "d_logits", None) is None:
             self.d_logits = torch.zeros(max(T, 1), self.E, dtype=torch.float32, device=self.device)

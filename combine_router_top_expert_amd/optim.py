@@ -67,6 +67,29 @@ class AdamW:
                                dev_lr=self.dev_lr, dev_step=self.dev_step)
         self._grads = None
 
+    def state_dict(self) -> dict:
+        """Moments, fp32 copies and step number (the tensors themselves)."""
+        return {"step": int(self.dev_step.item()) if self.dev_step is not None else self.step_count,
+                "m": self.m, "v": self.v, "m_scale": self.m_scale, "v_scale": self.v_scale,
+                "master": self.master}
+
+    def load_state_dict(self, state: dict):
+        """Copies a state_dict of an optimizer over tensors of the same sizes
+        and kinds into this one's buffers (their addresses stay)."""
+        for name in ("m", "v", "m_scale", "v_scale", "master"):
+            mine, theirs = getattr(self, name), state[name]
+            if len(mine) != len(theirs) or any(
+                    (a is None) != (b is None) or (a is not None and (a.numel() != b.numel() or a.dtype != b.dtype))
+                    for a, b in zip(mine, theirs)):
+                raise ValueError(f"state of other tensors: {name}")
+        for name in ("m", "v", "m_scale", "v_scale", "master"):
+            for a, b in zip(getattr(self, name), state[name]):
+                if a is not None:
+                    a.copy_(b.view(a.shape))
+        self.step_count = int(state["step"])
+        if self.dev_step is not None:
+            self.dev_step.fill_(self.step_count)
+
     def set_lr(self, lr: float):
         self.args.lr = lr
         if self.dev_lr is not None:
@@ -94,7 +117,8 @@ class AdamW:
 
     def step(self, grads: Optional[Sequence[torch.Tensor]] = None, grad_scale: float = 1.0,
              stream=None):
-        """One step on `stream` (None: the device's current stream).  grads:
+        """One step on `stream` (a torch stream; None: the device's current
+        one).  grads:
         gradients to bind, or None for those bound before.  Gradients are
         multiplied by grad_scale (the norm is taken before)."""
         if grads is not None:

@@ -454,9 +454,12 @@ size_t mok_router_bwd_ws_bytes(const mok_config* cfg, int32_t own_n);
  *   d_bias    = sum_t d_logits          ([E] fp32, or NULL)
  * overwritten, or with accumulate != 0 added to what the buffers hold (after
  * mok_layer_bwd; d_x is then rounded once more, from the fp32 sum).  Sums in
- * fp32 at least, in a fixed order.  src_x is needed for dw_router, w_router
- * for d_x; fp32 for MOK_F32, else bf16, 16-byte aligned like the outputs.
- * own rows of zero overwrite (or leave) dw_router and d_bias with zeros. */
+ * fp32 at least, in a fixed order; a bf16 d_x carries 2^-17 of its terms
+ * beside its rounding.  No output may overlap an input.  src_x is needed for dw_router, w_router
+ * for d_x; fp32 for MOK_F32, else bf16, 16-byte aligned like the outputs;
+ * d at most 2^26.  Without own rows dw_router and d_bias become zero (or
+ * stay, with accumulate).  A NaN or infinity in d_logits makes its row of
+ * d_x and its expert's dw_router and d_bias not finite. */
 mok_status mok_router_bwd(const mok_config* cfg, int32_t own_lo, int32_t own_n,
                           const float* d_logits, const void* const* src_x, const void* w_router,
                           void* const* d_x, float* dw_router, float* d_bias, int32_t accumulate,
@@ -506,7 +509,7 @@ typedef struct mok_adamw_args {
   const float* dev_scale;    /* device, or NULL = 1 (out + 1 of mok_grad_norm); NaN: the call
                                 leaves every tensor as it is */
   const double* dev_lr;      /* device, or NULL = lr: read when the step runs, for captured steps */
-  const int64_t* dev_step;   /* device, or NULL = step */
+  const int64_t* dev_step;   /* device, or NULL = step; at least 1 when the call runs */
 } mok_adamw_args;
 
 /* One AdamW step over n_params tensors (host array; the call reads it before

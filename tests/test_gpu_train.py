@@ -469,11 +469,11 @@ def _mix(z):
         return z ^ (z >> np.uint64(31))
 
 
-def _words(n, tensor, step, seed):
-    """(w for the moments, w for p) of every element, as the header defines them."""
+def _words(n, tensor, step, seed, start=0):
+    """(w for the moments, w for p) of elements start .. start + n, as the header defines them."""
     one = lambda v: np.array([v & M64], dtype=np.uint64)  # noqa: E731
     key = int(_mix(one(int(_mix(one(seed + tensor))[0]) + step * G64))[0])
-    i = np.arange(n, dtype=np.uint64)
+    i = np.arange(start, start + n, dtype=np.uint64)
     with np.errstate(over="ignore"):
         z = _mix(np.uint64(key) + (i // np.uint64(8) + np.uint64(1)) * np.uint64(G64))
     a, b, j = z & np.uint64(0xFFFFFFFF), z >> np.uint64(32), i % np.uint64(8)
@@ -802,6 +802,99 @@ def test_balance_and_router_captured_match_eager():
             assert torch.equal(t, want[n]), (rep, n)
     assert int(st.item()) == 0
     del cg
+
+
+# ------------------------------------------------------------------ beyond 32 bits
+def test_balance_beyond_32_bit_offsets():
+    """More than 2^31 logits: counts and the last rows against the definition."""
+    T, E, k = (1 << 22) + 1000, 512, 1
+    _log("balance large", T, E)
+    cfg = mok.make_config(1, T, 64, E, k, 64, 1, "f32", 0)
+    z = torch.zeros(T, E, device=DEV)
+    tail = torch.randn(1000, E, generator=_gen(1))
+    z[-1000:] = tail.to(DEV)
+    topk = torch.zeros(T, k, dtype=torch.int32, device=DEV)
+    topk[-1000:] = torch.argmax(tail, 1, keepdim=True).to(torch.int32).to(DEV)
+    off = torch.tensor([0, T - 1000, T], dtype=torch.int32, device=DEV)
+    bal = mok.make_balance(1.0, 1e-3, 2, off)
+    counts, n_tok = torch.zeros(2, E, dtype=torch.int32, device=DEV), torch.zeros(4, dtype=torch.int32, device=DEV)
+    prob, loss = torch.zeros(2, E, device=DEV), torch.zeros(2, device=DEV)
+    ws = torch.empty(mok.mok_balance_ws_bytes(cfg, T, bal), dtype=torch.uint8, device=DEV)
+    st = torch.zeros(1, dtype=torch.int32, device=DEV)
+    mok.mok_balance_fwd(cfg, T, bal, z, topk, counts, prob, n_tok, loss, ws, st)
+    mok.mok_balance_bwd(cfg, T, bal, z, counts, n_tok, None, z, st)      # in place
+    torch.cuda.synchronize()
+    assert int(st.item()) == 0 and n_tok.tolist() == [T - 1000, 1000, T, 2]
+    assert int(counts[0, 0]) == T - 1000 and int(counts[0].sum()) == T - 1000
+    d = tail.double()
+    lse = torch.logsumexp(d, 1)
+    p = torch.exp(d - lse[:, None])
+    c = torch.bincount(torch.argmax(tail, 1), minlength=E).double()
+    w = c * E / (1000.0 * 1000 * 2)
+    assert torch.equal(counts[1].cpu().double(), c)
+    want = p * (w - (p @ w)[:, None]) + p * (2e-3 / T * lse)[:, None]
+    wc = (w - w.mean()).abs()
+    _within(z[-1000:], want, 192 * U * p * (wc + (p @ wc)[:, None]) + 96 * U * p * 2e-3 / T * (1 + lse.abs())[:, None], "tail")
+    _within(prob[1], p.mean(0), 400 * U * p.mean(0), "prob")
+
+
+def test_router_bwd_beyond_32_bit_offsets():
+    """More than 2^31 token values: the last rows of d_x, and dw and db of
+    gradients that live in the last rows alone."""
+    T, d, E = 300_100, 7168, 2
+    _log("router large", T, d)
+    cfg = mok.make_config(1, T, d, E, 1, 64, 1, "bf16", 0)
+    x = torch.zeros(T, d, dtype=torch.bfloat16, device=DEV)
+    dz = torch.zeros(T, E, device=DEV)
+    g = _gen(4)
+    xt, zt, w = (torch.randn(100, d, generator=g).bfloat16(), torch.randn(100, E, generator=g),
+                 torch.randn(E, d, generator=g).bfloat16())
+    x[-100:], dz[-100:] = xt.to(DEV), zt.to(DEV)
+    dx = torch.full((T, d), 9.0, dtype=torch.bfloat16, device=DEV)
+    dw, db = torch.empty(E, d, device=DEV), torch.empty(E, device=DEV)
+    ws = torch.empty(mok.mok_router_bwd_ws_bytes(cfg, 1), dtype=torch.uint8, device=DEV)
+    mok.mok_router_bwd(cfg, 0, 1, dz, [x], w.to(DEV), [dx], dw, db, False, ws)
+    torch.cuda.synchronize()
+    assert not dx[:-100].any()
+    zd = zt.double()
+    ref = zd @ w.double()
+    _within(dx[-100:], ref, 2.0 ** -8 * ref.abs() + (2.0 ** -16 + 4 * U) * (zd.abs() @ w.double().abs()), "d_x")
+    refw = zd.t() @ xt.double()
+    _within(dw, refw, 104 * U * (zd.abs().t() @ xt.double().abs()) + 2 * U * refw.abs(), "dw")
+    _within(db, zd.sum(0), 2 * U * zd.abs().sum(0), "db")
+
+
+def test_optimizer_beyond_32_bit_offsets():
+    """One tensor of more than 2^31 elements, bf16 with 8-bit moments: its
+    last elements (their random words count from the tensor's start), and its
+    norm."""
+    n, m = (1 << 31) + 77, 333
+    _log("adamw large", n)
+    p, g = torch.zeros(n, dtype=torch.bfloat16, device=DEV), torch.zeros(n, dtype=torch.bfloat16, device=DEV)
+    codes = [torch.zeros(n, dtype=torch.uint8, device=DEV) for _ in range(2)]
+    scales = [torch.zeros((n + 31) // 32, dtype=torch.uint8, device=DEV) for _ in range(2)]
+    gt = torch.randn(m, generator=_gen(9)).bfloat16()
+    g[-m:] = gt.to(DEV)
+    params = mok.make_params([mok.make_param(p=p, g=g, m=codes[0], v=codes[1], m_scale=scales[0], v_scale=scales[1])])
+    out = torch.zeros(2, device=DEV)
+    ws = torch.empty(mok.mok_grad_norm_ws_bytes(params), dtype=torch.uint8, device=DEV)
+    mok.mok_grad_norm(params, 0.0, out, ws)
+    mok.mok_adamw(params, mok.make_adamw(**HYPER, step=1, seed=5))
+    torch.cuda.synchronize()
+    norm = float(gt.double().norm())
+    assert abs(float(out[0]) - norm) <= 2 * U * norm
+    gd = gt.double()
+    want = -HYPER["lr"] * gd / (gd.abs() + HYPER["eps"])   # the first step from zero
+    _within(p[-m:], want, 2.0 ** -8 * want.abs() + 48 * U * want.abs(), "p")
+    assert not p[:-m].any()
+    w = torch.from_numpy(_words(m, 0, 1, 5, start=n - m)[0])
+    for val, code, sc, u in ((0.1 * gd, codes[0], scales[0], (w & 0xFFFF).double() / 65536),
+                             (math.sqrt(1e-3) * gd.abs(), codes[1], scales[1], (w >> 16).double() / 65536)):
+        at = torch.arange(n - m, n)
+        sh = sc.cpu()[at // 32].double() - 127
+        lo, hi = _round_range(val, u, sh, torch.full((m,), 16 * U, dtype=torch.float64))
+        got = _e4m3(code[-m:]).abs()
+        assert ((got >= lo) & (got <= hi.clamp_min(2.0 ** -9))).all()
 
 
 # ------------------------------------------------------------------ together

@@ -45,6 +45,8 @@ def test_balance_refusals(L):
         out = [16] * 4
         out[i] = None
         assert _balance_fwd(L, cfg, out=out) == EINVAL
+    assert _balance_fwd(L, cfg, z=18) == EINVAL
+    assert _balance_fwd(L, cfg, topk=18) == EINVAL
     assert _balance_fwd(L, cfg, ws=None) == EINVAL
     assert _balance_fwd(L, cfg, ws=4) == EINVAL                        # 8-byte partial sums
     assert _balance_fwd(L, cfg, bal=_bal(G=-1)) == EINVAL
@@ -59,6 +61,9 @@ def test_balance_refusals(L):
     assert L.mok_balance_bwd(ctypes.byref(cfg), 10, b, 16, None, 16, None, 16, None, None) == EINVAL
     assert L.mok_balance_bwd(ctypes.byref(cfg), 10, b, 16, 16, None, None, 16, None, None) == EINVAL
     assert L.mok_balance_bwd(ctypes.byref(cfg), 10, b, 16, 16, 16, None, None, None, None) == EINVAL
+    assert L.mok_balance_bwd(ctypes.byref(cfg), 10, b, 18, 16, 16, None, 16, None, None) == EINVAL
+    assert L.mok_balance_bwd(ctypes.byref(cfg), 10, b, 16, 16, 16, 18, 16, None, None) == EINVAL
+    assert L.mok_balance_bwd(ctypes.byref(cfg), 10, b, 16, 16, 16, None, 18, None, None) == EINVAL
     assert L.mok_balance_bwd(ctypes.byref(cfg), 0, b, None, None, None, None, None, None, None) == 0
 
 
@@ -80,6 +85,7 @@ def _router(L, cfg, own=(0, 2), dz=16, x=16, w=16, dx=16, dw=16, db=16, ws=256):
 def test_router_bwd_refusals(L):
     cfg = _cfg()
     assert _router(L, _cfg(d=100)) == EINVAL
+    assert _router(L, _cfg(d=(1 << 26) + 64, T_src=1)) == EINVAL
     assert _router(L, cfg, own=(1, 2)) == EINVAL          # past the last source
     assert _router(L, cfg, own=(-1, 1)) == EINVAL
     assert _router(L, cfg, dz=None) == EINVAL
@@ -148,6 +154,9 @@ def test_adamw_and_norm_refusals(L):
                        ctypes.byref(a), None) == 0
     a.random_params = 2
     assert L.mok_adamw(1, arr, ctypes.byref(a), None) == EINVAL
+    for bad in (dict(dev_scale=18), dict(dev_lr=20), dict(dev_step=20)):
+        assert _adamw(L, [_param()], **bad) == EINVAL
+    assert L.mok_grad_norm(1, arr, 1.0, 18, 16, None) == EINVAL
     assert L.mok_grad_norm(1, arr, 1.0, None, 16, None) == EINVAL
     assert L.mok_grad_norm(1, arr, 1.0, 16, None, None) == EINVAL
     assert L.mok_grad_norm(1, arr, 1.0, 16, 4, None) == EINVAL
@@ -204,3 +213,37 @@ def test_optimizer_refusals():
         opt.bind([w, w])
     with pytest.raises(ValueError):
         opt.bind([torch.zeros(9)])
+
+
+def test_optimizer_state_moves_between_optimizers():
+    from combine_router_top_expert_amd.optim import AdamW
+    ps = [torch.randn(70).bfloat16(), torch.randn(33)]
+    a, b = (AdamW([p.clone() for p in ps], state_bits=[8, 32]) for _ in range(2))
+    for t in a.m + a.v + [a.m_scale[0], a.v_scale[0], a.master[0]]:
+        t.copy_(torch.randint(0, 100, t.shape))
+    a.step_count = 17
+    b.load_state_dict(a.state_dict())
+    assert b.step_count == 17
+    for x, y in zip(a.m + a.v + a.m_scale + a.v_scale + a.master, b.m + b.v + b.m_scale + b.v_scale + b.master):
+        assert (x is None and y is None) or (torch.equal(x, y) and x.data_ptr() != y.data_ptr())
+    with pytest.raises(ValueError):
+        AdamW([p.clone() for p in ps]).load_state_dict(a.state_dict())      # 32-bit moments
+    with pytest.raises(ValueError):
+        AdamW([ps[0].clone()], state_bits=8).load_state_dict(a.state_dict())
+
+
+def test_layer_balance_refusals():
+    from combine_router_top_expert_amd.layer import MoELayer
+
+    def layer(**kw):
+        return MoELayer(1, 4, 64, 4, 1, 64, 4, "f32", 4, 0, 1, device="cpu", **kw)
+    with pytest.raises(RuntimeError):
+        layer().balance_loss(0.1)                        # no logits kept
+    L = layer(keep_logits=True)
+    with pytest.raises(RuntimeError):
+        L.balance_backward()                             # no loss before it
+    for bad in (dict(group_offsets=torch.tensor([0, 4])), dict(group_offsets=torch.tensor([0], dtype=torch.int32)),
+                dict(token_mask=torch.ones(4)), dict(token_mask=torch.ones(3, dtype=torch.uint8)),
+                dict(group_offsets=torch.zeros(0, dtype=torch.int32))):
+        with pytest.raises(ValueError):
+            L.balance_loss(0.1, **bad)
