@@ -62,6 +62,7 @@ struct BalArgs {
   float* loss;
   const float* d_loss;
   float* dz;
+  int stream;            // gradients past the caches
   float alpha, beta;
 };
 
@@ -148,12 +149,16 @@ struct RowLayout {
       }
     }
   }
+  template <bool STREAM>
   __device__ __forceinline__ static void store(float* row, int l, int E, const float (&v)[NV]) {
     if constexpr (VEC) {
 #pragma unroll
       for (int u = 0; u < NV / 4; ++u) {
         const int e = 4 * (l + LPR * u);
-        if (e < E) *reinterpret_cast<float4*>(row + e) = make_float4(v[4 * u], v[4 * u + 1], v[4 * u + 2], v[4 * u + 3]);
+        const f32x4_t q = {v[4 * u], v[4 * u + 1], v[4 * u + 2], v[4 * u + 3]};
+        if (e >= E) continue;
+        if constexpr (STREAM) __builtin_nontemporal_store(q, reinterpret_cast<f32x4_t*>(row + e));
+        else *reinterpret_cast<f32x4_t*>(row + e) = q;
       }
     } else {
 #pragma unroll
@@ -521,7 +526,9 @@ __global__ __launch_bounds__(kFinThreads) void balance_finish_kernel(BalArgs a) 
   }
 }
 
-template <int LPR, int NV, bool VEC>
+// STREAM: nontemporal stores (a template parameter: as a branch the compiler
+// merges both stores into one plain one).
+template <int LPR, int NV, bool VEC, bool STREAM>
 __global__ __launch_bounds__(kBalThreads) void balance_bwd_kernel(BalArgs a) {
   typedef RowLayout<LPR, NV, VEC> RL;
   constexpr int U = rows_at_once<NV>();
@@ -540,7 +547,10 @@ __global__ __launch_bounds__(kBalThreads) void balance_bwd_kernel(BalArgs a) {
     const int lo = max(g_lo, c_lo), hi = min(g_hi, c_hi);
     if (lo >= hi) continue;
     Rows<LPR, NV, VEC> now, next;
-    int r0 = lo + wave * RL::kRows * U;
+    // last rows first: the forward read them last, so they are likeliest to be
+    // in a cache still
+    const int first = lo + wave * RL::kRows * U;
+    int r0 = first < hi ? first + (hi - 1 - first) / step * step : first;
     if (r0 < hi) now.load(a, r0, hi, l, sub);
     const int n = a.n_tok[g];
     const float cw = n > 0 && groups > 0 ? (float)(a.alpha * d0 * a.E / ((double)a.k * n * n * groups)) : 0.0f;
@@ -552,8 +562,8 @@ __global__ __launch_bounds__(kBalThreads) void balance_bwd_kernel(BalArgs a) {
       w[i] = e < a.E ? cw * (float)(a.counts[(size_t)g * a.E + e] - mean) : 0.0f;
     }
     while (r0 < hi) {
-      const bool more = hi - r0 > step;
-      if (more) next.load(a, r0 + step, hi, l, sub);
+      const bool more = r0 > first;
+      if (more) next.load(a, r0 - step, hi, l, sub);
       bool live[U];
       float lse[U], dot[U];
       const bool rare = softmax_rows<LPR, NV, U>(now.v, now.mask, now.in, lane, live, lse);
@@ -577,10 +587,12 @@ __global__ __launch_bounds__(kBalThreads) void balance_bwd_kernel(BalArgs a) {
           for (int i = 0; i < NV; ++i) now.v[u][i] = live[u] ? now.v[u][i] : 0.0f;
       }
 #pragma unroll
-      for (int u = 0; u < U; ++u)
-        if (now.in[u]) RL::store(a.dz + (size_t)(r0 + u * RL::kRows + sub) * a.E, l, a.E, now.v[u]);
+      for (int u = 0; u < U; ++u) {
+        if (!now.in[u]) continue;
+        RL::template store<STREAM>(a.dz + (size_t)(r0 + u * RL::kRows + sub) * a.E, l, a.E, now.v[u]);
+      }
       if (!more) break;
-      r0 += step;
+      r0 -= step;
       now = next;
     }
   }
@@ -627,9 +639,15 @@ size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 template <bool BWD, int LPR, int NV, bool VEC>
 void launch_rows(const BalArgs& a, hipStream_t st) {
   const dim3 grid((unsigned)a.chunks), blk(kBalThreads);
-  if constexpr (BWD)
-    hipLaunchKernelGGL((balance_bwd_kernel<LPR, NV, VEC>), grid, blk, 0, st, a);
-  else
+  if constexpr (BWD) {
+    if constexpr (VEC) {
+      if (a.stream) {
+        hipLaunchKernelGGL((balance_bwd_kernel<LPR, NV, true, true>), grid, blk, 0, st, a);
+        return;
+      }
+    }
+    hipLaunchKernelGGL((balance_bwd_kernel<LPR, NV, VEC, false>), grid, blk, 0, st, a);
+  } else
     hipLaunchKernelGGL((balance_fwd_kernel<LPR, NV, VEC>), grid, blk, 0, st, a);
 }
 
@@ -719,6 +737,12 @@ mok_status launch_balance_bwd(int T, int E, int k, int G, const mok_balance& b, 
   a.n_tok = const_cast<int32_t*>(n_tok);
   a.d_loss = d_loss;
   a.dz = d_logits;
+  // Logits and gradients that the 256 MiB memory-side cache cannot hold
+  // together: left in it, the gradients are written back under whatever runs
+  // next, and push out the logits (131072 x 256, forward and backward: 100
+  // us, 90 us with streaming stores; smaller ones are read again from the
+  // cache by the router's backward).
+  a.stream = (int64_t)T * E * 8 >= (int64_t)256 << 20;
   a.alpha = b.alpha, a.beta = b.beta;
   launch_shape<true>(row_shape(E, (uintptr_t)logits | (uintptr_t)d_logits), a, stream);
   trace_mark(tr, "balance_bwd", stream);

@@ -21,6 +21,8 @@
 //   3. router_dw_kernel: 64 x 64 of dW per wave, both operands through an
 //      LDS ring filled by direct loads, split over the tokens;
 //   4. router_reduce_kernel adds the token chunks in order.
+#include <math.h>
+
 #include "mok_gemm2.h"
 #include "mok_internal.h"
 
@@ -270,7 +272,8 @@ __device__ __forceinline__ bf16x8_t frag64(const char* lds, int n0, int s) {
 
 // NK: 16-expert steps (E <= 16 NK); four waves of 32 token rows each, two
 // workgroups per CU up to NK = 16 (one computes while the other stores).
-template <int NK>
+// STREAM: nontemporal stores of d_x.
+template <int NK, bool STREAM>
 __global__ __launch_bounds__(kThreads, NK <= 16 ? 2 : 1) void router_dx_bf16_kernel(RArgs a) {
   constexpr int STAGE = NK * 16 * 128;               // bytes of W per column step
   constexpr int LOADS = STAGE / 1024 / kDxWaves;     // direct loads per wave and step
@@ -347,7 +350,12 @@ __global__ __launch_bounds__(kThreads, NK <= 16 ? 2 : 1) void router_dx_bf16_ker
     for (int i = 0; i < 4; ++i) u[i] = *reinterpret_cast<const uint4*>(stg + i * 1024 + lane * 16);
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      if (out[i]) st16(out[i] + (size_t)s * 64, u[i]);
+      if (out[i]) {
+        if constexpr (STREAM)
+          __builtin_nontemporal_store(__builtin_bit_cast(i32x4_t, u[i]), reinterpret_cast<i32x4_t*>(out[i] + (size_t)s * 64));
+        else
+          st16(out[i] + (size_t)s * 64, u[i]);
+      }
   };
   for (int s = s0; s < s1; ++s) {
     // this wave's loads of step s (and its stores of the step before last)
@@ -702,10 +710,8 @@ size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 int expert_tile(int E) { return (E + 63) / 64 % 2 ? 64 : 128; }
 int padded_experts(int E) { return E <= 64 ? 64 : E <= 128 ? 128 : E <= 256 ? 256 : 512; }
 
-// Token chunks of the dW product and the workspace that follows from them.
-// fp32: workgroups for four per CU, at least 64 tokens each.  bf16: one
-// workgroup of eight waves per CU, at least 128 tokens each (every chunk
-// costs a fp32 copy of dW written and read again).
+// Token chunks of the dW product, at least 64 tokens each, and the workspace
+// that follows from them.  fp32: workgroups for four per CU.
 struct Plan {
   int chunks = 1, ew = 0, etiles = 0, db_parts = 0;
   int64_t chunk_rows = 0, split_rows = 0;
@@ -719,9 +725,21 @@ Plan make_plan(int prec, int64_t T, int d, int E) {
   p.etiles = (E + p.ew - 1) / p.ew;
   const int en = 64 * kDwWaves * 64 / p.ew;
   const int64_t tiles = f32 ? (int64_t)(d / kTile) * ((E + kTile - 1) / kTile) : (int64_t)((d + en - 1) / en) * p.etiles;
-  const int64_t least = f32 ? 64 : 128, unit = f32 ? kKB : kBK;
-  int64_t c = (f32 ? 1024 : 256 * 8 / kDwWaves) / tiles;
-  if (c > (T + least - 1) / least) c = (T + least - 1) / least;
+  const int64_t unit = f32 ? kKB : kBK;
+  int64_t c;
+  if (f32) {
+    c = 1024 / tiles;
+  } else {
+    // a chunk costs E d 8 bytes (written and read) at about 5 TB/s, 16 tokens
+    // of a workgroup 0.25 us while there are fewer workgroups than CUs hold:
+    // least in all at the root below.  From one workgroup per CU on, whole
+    // rounds of the CUs, at most two (16384 x 2048 x 64: 32 chunks 55 us, 64
+    // chunks 59)
+    c = (int64_t)(sqrt(9766.0 * (double)T / ((double)E * d)) + 0.5);
+    const int64_t rounds = (c * tiles + 128) / 256;
+    if (rounds > 0) c = 256 * (rounds < 2 ? rounds : 2) / tiles;
+  }
+  if (c > (T + 63) / 64) c = (T + 63) / 64;
   if (c < 1) c = 1;
   p.chunk_rows = ((T + c - 1) / c + unit - 1) / unit * unit;
   p.chunks = p.chunk_rows > 0 ? (int)((T + p.chunk_rows - 1) / p.chunk_rows) : 1;
@@ -747,7 +765,13 @@ void launch_dx(RArgs& a, hipStream_t stream) {
   int64_t n = (256 * kPerCu + rb - 1) / rb;
   if (n > a.d / 64) n = a.d / 64;
   a.n_chunks = (int)n;
-  hipLaunchKernelGGL(router_dx_bf16_kernel<NK>, dim3((unsigned)(rb * n)), dim3(kThreads), 0, stream, a);
+  // d_x beyond the 32 MiB of the L2s is stored past them: kept, it is written
+  // back under the dW product's loads (16384 x 2048 x 64: 62 us in all against
+  // 59)
+  if ((int64_t)a.T * a.d * 2 > (int64_t)32 << 20)
+    hipLaunchKernelGGL((router_dx_bf16_kernel<NK, true>), dim3((unsigned)(rb * n)), dim3(kThreads), 0, stream, a);
+  else
+    hipLaunchKernelGGL((router_dx_bf16_kernel<NK, false>), dim3((unsigned)(rb * n)), dim3(kThreads), 0, stream, a);
 }
 
 template <int EW>
