@@ -239,7 +239,9 @@ __global__ __launch_bounds__(kThreads) void router_split_kernel(RArgs a) {
     for (int j = 0; j < 8; ++j) {
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) db[j] += __shfl_xor(db[j], o, 64);
-      if (tl == 0 && e0 + j < a.E) a.dbp[(size_t)blockIdx.x * a.E + e0 + j] = db[j];
+      if (tl != 0 || e0 + j >= a.E) continue;
+      if (a.dbp) a.dbp[(size_t)blockIdx.x * a.E + e0 + j] = db[j];
+      else a.db[e0 + j] = (float)(a.add ? a.db[e0 + j] + db[j] : db[j]);   // the only partial sum
     }
   }
 }
@@ -746,7 +748,10 @@ Plan make_plan(int prec, int64_t T, int d, int E) {
   if (f32) {
     p.db_parts = p.chunks;
   } else {
+    // blocks of 32 tokens, at most 512 workgroups a side; few tokens in one,
+    // which then writes db itself (and with one chunk nothing is left to add)
     p.split_rows = (T + 512 * 32 - 1) / (512 * 32) * 32;
+    if (T <= 128) p.split_rows = 128;
     p.db_parts = T > 0 ? (int)((T + p.split_rows - 1) / p.split_rows) : 0;
     p.parts = align256((size_t)((T + 31) / 32) * 3 * padded_experts(E) * 64);
   }
@@ -815,7 +820,7 @@ mok_status launch_router_bwd(const RouterBwdPlan& p, hipStream_t stream) {
   } else {
     if (p.T > 0) {
       a.parts = p.want_dx || p.dw ? (bf16_t*)ws : nullptr;
-      a.dbp = (double*)(ws + pl.parts);
+      a.dbp = pl.db_parts > 1 ? (double*)(ws + pl.parts) : nullptr;
       hipLaunchKernelGGL(router_split_kernel, dim3((unsigned)pl.db_parts, a.eblocks / 4), blk, 0, stream, a);
       trace_mark(p.tr, "router_split", stream);
     }
@@ -833,7 +838,7 @@ mok_status launch_router_bwd(const RouterBwdPlan& p, hipStream_t stream) {
     }
   }
   // what is left to add up: dW over chunks, db over its partial sums
-  const bool dw_left = p.dw && a.part, db_left = p.db && (a.dbp || !f32);
+  const bool dw_left = p.dw && a.part, db_left = p.db && (a.dbp || (!f32 && p.T == 0));
   if (dw_left || db_left) {
     const unsigned dwb = dw_left ? (unsigned)(((size_t)p.E * p.d + 255) / 256) : 0;
     const unsigned dbb = db_left ? (unsigned)(p.E + 7) / 8 : 0;

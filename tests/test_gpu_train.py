@@ -306,6 +306,10 @@ ROUTER = [
     ("bf16", 1, 0, 1, 700, 320, 256),
     ("bf16", 2, 0, 2, 1000, 1024, 31),
     ("bf16", 1, 0, 1, 129, 64, 512),
+    ("bf16", 1, 0, 1, 128, 128, 130),
+    ("bf16", 2, 0, 2, 16, 64, 65),
+    ("bf16", 1, 0, 1, 64, 192, 300),
+    ("bf16", 3, 0, 3, 8192, 128, 192),
     ("bf16", 8, 0, 8, 3, 448, 200),
     ("bf16", 1, 0, 1, 5000, 128, 100),
     ("bf16", 1, 0, 1, 260, 7168, 72),
