@@ -230,6 +230,9 @@ __device__ __forceinline__ int block_scale(float amax) {
 // code's exponent field (bias 127 - 120 = 7), so its bits from 20 on are the
 // code rounded down, subnormals included, and what is added below carries.
 // The scale keeps finite |x| 2^-s at 448 or less, so nothing passes 0x7E.
+// (Below the 2^-6 of the smallest full code the product is rounded to fp32's
+// own subnormals, 2^-20 of the distance of two codes: 16 times finer than the
+// random number.)
 __device__ __forceinline__ uint32_t random_code(float x, int s, uint32_t rnd) {
   return __float_as_uint(__builtin_amdgcn_ldexpf(__builtin_fabsf(x), -s - 120)) + rnd;
 }
@@ -285,9 +288,22 @@ __device__ __forceinline__ int encode8(const float (&x)[8], const uint32_t (&rnd
   return s;
 }
 
-// Square root and reciprocal of the update are the hardware's (1 ulp each):
-// an error of 2^-23 of the update itself.  (The square root of a v below
-// 2^-126 is 0; eps hides it.)
+// The square root of v, rounded to nearest but for rare last bits: the
+// hardware's reciprocal root (1 ulp) and one step of Newton's for the root,
+// whose residual v - r r is exact.  A v below 2^-126 gives v 2^63: above zero
+// too, and hidden by any eps above 1e-19.
+__device__ __forceinline__ float root(float v) {
+  const float h = __builtin_amdgcn_rsqf(__builtin_fmaxf(v, 0x1p-126f));
+  const float r = v * h;
+  const float e = __builtin_fmaf(-r, r, v);
+  return v < __builtin_inff() ? __builtin_fmaf(e, 0.5f * h, r) : v;
+}
+
+// The moments are formed as the formula says, each product and sum rounded by
+// itself, and so is the root: a fused or 1-ulp form moves one stored code in
+// about 2^21 to its neighbour, and where two gradients' histories are alike
+// their codes should not depend on how a build contracts.  The reciprocal of
+// the update is the hardware's (1 ulp): an error of 2^-23 of the update.
 template <bool EIGHT>
 __device__ __forceinline__ void adam_step(const Desc& d, const AdamArgs& a, int64_t i, float scale, float lr,
                                           float inv_bc1, float inv_sbc2, uint64_t key) {
@@ -326,10 +342,11 @@ __device__ __forceinline__ void adam_step(const Desc& d, const AdamArgs& a, int6
   float r[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
+#pragma clang fp contract(off)
     const float gj = g[j] * scale;
-    m[j] = __builtin_fmaf(a.b1, m[j], a.c1 * gj);
-    v[j] = __builtin_fmaf(a.b2, v[j], a.c2 * (gj * gj));
-    r[j] = __builtin_amdgcn_sqrtf(v[j]);
+    m[j] = a.b1 * m[j] + a.c1 * gj;
+    v[j] = a.b2 * v[j] + a.c2 * (gj * gj);
+    r[j] = root(v[j]);
     const float u = m[j] * __builtin_amdgcn_rcpf(__builtin_fmaf(r[j], inv_sbc2, a.eps));
     p[j] = __builtin_fmaf(rate, u, p[j] * decay);
   }

@@ -630,6 +630,57 @@ def test_adamw_one_step(p_type, g_type, bits):
         c.check(t, step, seed, scale, random)
 
 
+def _codes32(x, u, root):
+    """E4M3 codes (without sign) and exponents of fp32 values in blocks of 32, each rounded down or up by its u."""
+    b = x.double().abs().view(-1, 32)
+    top = b.amax(1)
+    sh = torch.ceil(torch.log2((top / 448).clamp_min(2.0 ** -127)))
+    y = (b * torch.exp2(-sh)[:, None]).view(-1)
+    q = torch.exp2(torch.floor(torch.log2(y.clamp_min(2.0 ** -6))) - 3)
+    val = torch.floor(y / q + u) * q
+    if root:
+        val = torch.where((y > 0) & (val < 2.0 ** -9), 2.0 ** -9, val)
+    return val.to(torch.float8_e4m3fn).view(torch.uint8), (sh + 127).to(torch.uint8)
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_adamw_moments_are_the_formula_in_32_bits(bits):
+    """What a step stores of the moments, bit for bit against the formula with
+    every product, sum and root rounded to fp32 by itself, over two steps."""
+    _log("adamw bits", bits)
+    n, step, seed, scale = 32 * 8000, 4, 21, 0.375
+    c = _Case(n, "f32", "f32", bits, 5)
+    c.g[33:40] = 1e-3
+    params = mok.make_params([c.to_device()])
+    f = lambda v: torch.tensor(v, dtype=torch.float32)  # noqa: E731
+    b1, b2, c1, c2 = f(HYPER["beta1"]), f(HYPER["beta2"]), f(1 - HYPER["beta1"]), f(1 - HYPER["beta2"])
+    gs = c.g * f(scale)
+    if bits == 8:
+        m = _e4m3(c.m).float() * _scales(c.ms, n).float()
+        r = _e4m3(c.v).float() * _scales(c.vs, n).float()
+    else:
+        m, v = c.m, c.v
+    for k in (step, step + 1):
+        mok.mok_adamw(params, mok.make_adamw(**HYPER, step=k, seed=seed, grad_scale=scale))
+        torch.cuda.synchronize()
+        d = c.d
+        if bits == 32:
+            m, v = b1 * m + c1 * gs, b2 * v + c2 * (gs * gs)
+            assert torch.equal(d["m"].cpu(), m) and torch.equal(d["v"].cpu(), v)
+            continue
+        m, r = b1 * m + c1 * gs, torch.sqrt(b2 * (r * r) + c2 * (gs * gs))
+        w = torch.from_numpy(_words(n, 0, k, seed)[0])
+        for x, u, code, sc in ((m, w & 0xFFFF, d["m"], d["ms"]), (r, w >> 16, d["v"], d["vs"])):
+            want, exps = _codes32(x, u.double() / 65536, x is r)
+            assert torch.equal(sc.cpu(), exps)
+            assert torch.equal(code.cpu() & 0x7F, want)
+            if x is m:
+                live = want > 0
+                assert torch.equal((code.cpu() >> 7)[live], (m < 0).to(torch.uint8)[live])
+        m = _e4m3(d["m"]).float() * _scales(d["ms"], n).float()
+        r = _e4m3(d["v"]).float() * _scales(d["vs"], n).float()
+
+
 def test_adamw_many_tensors_of_mixed_kinds():
     """More tensors than one launch takes, kinds mixed, empty ones between."""
     _log("adamw mixed")
