@@ -23,6 +23,8 @@
 //   4. router_reduce_kernel adds the token chunks in order.
 #include <math.h>
 
+#include <algorithm>
+
 #include "mok_gemm2.h"
 #include "mok_internal.h"
 
@@ -275,16 +277,18 @@ __device__ __forceinline__ bf16x8_t frag64(const char* lds, int n0, int s) {
 // NK: 16-expert steps (E <= 16 NK); four waves of 32 token rows each, two
 // workgroups per CU up to NK = 16 (one computes while the other stores).
 // STREAM: nontemporal stores of d_x.
+template <int NK>
+constexpr int dx_lds() { return 2 * NK * 16 * 128 + kDxWaves * 4096; }
+
 template <int NK, bool STREAM>
-__global__ __launch_bounds__(kThreads, NK <= 16 ? 2 : 1) void router_dx_bf16_kernel(RArgs a) {
+__device__ __forceinline__ void dx_bf16(const RArgs& a, int b, char* smem) {
   constexpr int STAGE = NK * 16 * 128;               // bytes of W per column step
   constexpr int LOADS = STAGE / 1024 / kDxWaves;     // direct loads per wave and step
-  __shared__ __attribute__((aligned(16))) char smem[2 * STAGE + kDxWaves * 4096];
   const int lane = threadIdx.x & 63;
   const int wave = (int)g2::wave_id();
   // workgroups of one row block on one XCD (b % 8), so its parts meet in an L2
   const int rb_n = (a.T + 32 * kDxWaves - 1) / (32 * kDxWaves);
-  int b = blockIdx.x, rb, ch;
+  int rb, ch;
   const int full = rb_n / 8 * 8 * a.n_chunks;
   if (b < full) {
     rb = b % 8 + 8 * (b / 8 / a.n_chunks);
@@ -483,16 +487,18 @@ __device__ __forceinline__ void load_lds16_at(const char* base, unsigned off, un
 }
 
 template <int EW>
-__global__ __launch_bounds__(kBf16Threads, 2) void router_dw_bf16_kernel(RArgs a) {
+constexpr int dw_lds() { return DwCfg<EW>::NS * DwCfg<EW>::STAGE + MOK_MAX_SOURCES * 8; }
+
+template <int EW>
+__device__ __forceinline__ void dw_bf16(const RArgs& a, int b, char* smem) {
   typedef DwCfg<EW> C;
-  __shared__ __attribute__((aligned(16))) char smem[C::NS * C::STAGE];
-  __shared__ const bf16_t* s_x[MOK_MAX_SOURCES];
+  const bf16_t** s_x = reinterpret_cast<const bf16_t**>(smem + C::NS * C::STAGE);
   const int lane = threadIdx.x & 63;
   const int wave = (int)g2::wave_id();
   // a token chunk's tiles on one XCD (b % 8) while the chunks fill whole
   // rounds of eight: its parts are then read from one L2
   const int ntn = (a.d + C::EN - 1) / C::EN, per = ntn * a.etiles;
-  int b = blockIdx.x, chunk, tile;
+  int chunk, tile;
   const int full = a.chunks / 8 * 8 * per;
   if (b < full) {
     chunk = b % 8 + 8 * (b / 8 / per);
@@ -658,9 +664,33 @@ __global__ __launch_bounds__(kBf16Threads, 2) void router_dw_bf16_kernel(RArgs a
       }
 }
 
+template <int NK, bool STREAM>
+__global__ __launch_bounds__(kThreads, NK <= 16 ? 2 : 1) void router_dx_bf16_kernel(RArgs a) {
+  __shared__ __attribute__((aligned(16))) char smem[dx_lds<NK>()];
+  dx_bf16<NK, STREAM>(a, (int)blockIdx.x, smem);
+}
+template <int EW>
+__global__ __launch_bounds__(kBf16Threads, 2) void router_dw_bf16_kernel(RArgs a) {
+  __shared__ __attribute__((aligned(16))) char smem[dw_lds<EW>()];
+  dw_bf16<EW>(a, (int)blockIdx.x, smem);
+}
+// Both products in one launch, dW's workgroups first: they are the longer
+// ones, and the dx workgroups that fill the CUs beside and after them store
+// under their loads (16384 x 2048 x 64: 49 us in all against 55 one after the
+// other; taking turns 60; 14336 x 7168 x 256, which the matrix cores bound:
+// no difference).
+template <int NK, int EW, bool STREAM>
+__global__ __launch_bounds__(kThreads, 2) void router_both_bf16_kernel(RArgs a, int dw_wgs) {
+  __shared__ __attribute__((aligned(16))) char smem[std::max(dx_lds<NK>(), dw_lds<EW>())];
+  const int b = (int)blockIdx.x;
+  if (b < dw_wgs) dw_bf16<EW>(a, b, smem);
+  else dx_bf16<NK, STREAM>(a, b - dw_wgs, smem);
+}
+
 // dW from the chunks' partial sums (the first dw_blocks workgroups: 64
-// 16-byte columns, four threads each adding every fourth chunk), and db: eight experts per workgroup, 32 threads an expert,
-// each adding every 32nd partial sum.
+// 16-byte columns, four threads each adding every fourth chunk), and db:
+// eight experts per workgroup, 32 threads an expert, each adding every 32nd
+// partial sum.
 __global__ __launch_bounds__(kThreads) void router_reduce_kernel(RArgs a, int dw_blocks) {
   __shared__ double s_db[32][8];
   if ((int)blockIdx.x < dw_blocks) {
@@ -761,28 +791,42 @@ Plan make_plan(int prec, int64_t T, int d, int E) {
   return p;
 }
 
-template <int NK>
-void launch_dx(RArgs& a, hipStream_t stream) {
-  // workgroups for every CU as often as they fit, as far as there are column
-  // steps
-  constexpr int kPerCu = NK <= 4 ? 4 : NK <= 16 ? 2 : 1;
+// Workgroups of dx: for every CU as often as they fit, as far as there are
+// column steps.
+int64_t plan_dx(RArgs& a, int per_cu) {
   const int64_t rb = ((int64_t)a.T + 32 * kDxWaves - 1) / (32 * kDxWaves);
-  int64_t n = (256 * kPerCu + rb - 1) / rb;
+  int64_t n = (256 * per_cu + rb - 1) / rb;
   if (n > a.d / 64) n = a.d / 64;
   a.n_chunks = (int)n;
-  // d_x beyond the 32 MiB of the L2s is stored past them: kept, it is written
-  // back under the dW product's loads (16384 x 2048 x 64: 62 us in all against
-  // 59)
-  if ((int64_t)a.T * a.d * 2 > (int64_t)32 << 20)
-    hipLaunchKernelGGL((router_dx_bf16_kernel<NK, true>), dim3((unsigned)(rb * n)), dim3(kThreads), 0, stream, a);
-  else
-    hipLaunchKernelGGL((router_dx_bf16_kernel<NK, false>), dim3((unsigned)(rb * n)), dim3(kThreads), 0, stream, a);
+  return rb * n;
+}
+template <int EW>
+unsigned dw_workgroups(const RArgs& a) {
+  return (unsigned)((a.d + DwCfg<EW>::EN - 1) / DwCfg<EW>::EN) * a.etiles * a.chunks;
+}
+// d_x beyond the 32 MiB of the L2s is stored past them: kept, it is written
+// back under the dW product's loads (16384 x 2048 x 64: 62 us in all against
+// 59).
+bool stream_dx(const RArgs& a) { return (int64_t)a.T * a.d * 2 > (int64_t)32 << 20; }
+
+template <int NK>
+void launch_dx(RArgs& a, hipStream_t stream) {
+  const dim3 grid((unsigned)plan_dx(a, NK <= 4 ? 4 : NK <= 16 ? 2 : 1));
+  if (stream_dx(a)) hipLaunchKernelGGL((router_dx_bf16_kernel<NK, true>), grid, dim3(kThreads), 0, stream, a);
+  else hipLaunchKernelGGL((router_dx_bf16_kernel<NK, false>), grid, dim3(kThreads), 0, stream, a);
 }
 
 template <int EW>
 void launch_dw(const RArgs& a, hipStream_t stream) {
-  const unsigned grid = (unsigned)((a.d + DwCfg<EW>::EN - 1) / DwCfg<EW>::EN) * a.etiles * a.chunks;
-  hipLaunchKernelGGL(router_dw_bf16_kernel<EW>, dim3(grid), dim3(kBf16Threads), 0, stream, a);
+  hipLaunchKernelGGL(router_dw_bf16_kernel<EW>, dim3(dw_workgroups<EW>(a)), dim3(kBf16Threads), 0, stream, a);
+}
+
+template <int NK, int EW>
+void launch_both(RArgs& a, hipStream_t stream) {
+  const unsigned dw = dw_workgroups<EW>(a);
+  const dim3 grid(dw + (unsigned)plan_dx(a, 2));
+  if (stream_dx(a)) hipLaunchKernelGGL((router_both_bf16_kernel<NK, EW, true>), grid, dim3(kThreads), 0, stream, a, (int)dw);
+  else hipLaunchKernelGGL((router_both_bf16_kernel<NK, EW, false>), grid, dim3(kThreads), 0, stream, a, (int)dw);
 }
 
 }  // namespace
@@ -824,17 +868,27 @@ mok_status launch_router_bwd(const RouterBwdPlan& p, hipStream_t stream) {
       hipLaunchKernelGGL(router_split_kernel, dim3((unsigned)pl.db_parts, a.eblocks / 4), blk, 0, stream, a);
       trace_mark(p.tr, "router_split", stream);
     }
-    if (p.want_dx && p.T > 0) {
-      if (p.E <= 64) launch_dx<4>(a, stream);
-      else if (p.E <= 128) launch_dx<8>(a, stream);
-      else if (p.E <= 256) launch_dx<16>(a, stream);
-      else launch_dx<32>(a, stream);
-      trace_mark(p.tr, "router_dx", stream);
-    }
-    if (p.dw) {
-      if (a.ew == 64) launch_dw<64>(a, stream);
-      else launch_dw<128>(a, stream);
-      trace_mark(p.tr, "router_dw", stream);
+    const bool dx = p.want_dx && p.T > 0;
+    if (dx && p.dw && p.E <= 256) {
+      if (p.E <= 64) launch_both<4, 64>(a, stream);
+      else if (p.E <= 128) launch_both<8, 128>(a, stream);
+      else if (a.ew == 64) launch_both<16, 64>(a, stream);
+      else launch_both<16, 128>(a, stream);
+      trace_mark(p.tr, "router_dx_dw", stream);
+    } else {
+      // one product alone; above 256 experts a dx workgroup fills a CU
+      if (dx) {
+        if (p.E <= 64) launch_dx<4>(a, stream);
+        else if (p.E <= 128) launch_dx<8>(a, stream);
+        else if (p.E <= 256) launch_dx<16>(a, stream);
+        else launch_dx<32>(a, stream);
+        trace_mark(p.tr, "router_dx", stream);
+      }
+      if (p.dw) {
+        if (a.ew == 64) launch_dw<64>(a, stream);
+        else launch_dw<128>(a, stream);
+        trace_mark(p.tr, "router_dw", stream);
+      }
     }
   }
   // what is left to add up: dW over chunks, db over its partial sums
