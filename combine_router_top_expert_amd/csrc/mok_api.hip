@@ -871,18 +871,18 @@ mok_status mok_mx_quantize_f32(int64_t rows, int64_t K, const float* src, uint8_
 // ------------------------------------------------------------------ training
 namespace {
 
+bool aligned(const void* p, int n) { return (uintptr_t)p % n == 0; }
+
 int balance_groups(const mok_balance* b) { return b->G > 0 ? b->G : 1; }
 
 bool valid_balance(const mok_config* cfg, int32_t T, const mok_balance* b) {
   if (!valid_cfg(cfg) || T < 0 || !b || b->G < 0) return false;
-  if (b->G > 0 && !b->group_offsets) return false;
+  if (b->G > 0 && (!b->group_offsets || !aligned(b->group_offsets, 4))) return false;
   // counts are int32, group rows of the outputs are indexed by int32; row
   // numbers stay clear of int32's end by a workgroup's step
   if (T > 1 << 30 || (int64_t)T * cfg->k > 0x7FFFFFFF || (int64_t)b->G * cfg->E > 0x7FFFFFFF) return false;
   return true;
 }
-
-bool aligned(const void* p, int n) { return (uintptr_t)p % n == 0; }
 
 bool valid_type(int t) { return t == MOK_F32 || t == MOK_BF16; }
 int type_bytes(int t) { return t == MOK_F32 ? 4 : 2; }
@@ -926,6 +926,7 @@ mok_status mok_balance_fwd(const mok_config* cfg, int32_t T, const mok_balance* 
   if (!valid_balance(cfg, T, bal)) return MOK_EINVAL;
   if (T > 0 && (!logits || !topk_idx || !aligned(logits, 4) || !aligned(topk_idx, 4))) return MOK_EINVAL;
   if (!counts || !prob || !n_tok || !loss || !ws || !aligned(ws, 16)) return MOK_EINVAL;
+  if (!aligned(counts, 4) || !aligned(prob, 4) || !aligned(n_tok, 4) || !aligned(loss, 4)) return MOK_EINVAL;
   trace_mark(cfg->trace, "start", (hipStream_t)stream);
   return launch_balance_fwd(T, cfg->E, cfg->k, balance_groups(bal), *bal, logits, topk_idx, counts,
                             prob, n_tok, loss, ws, dev_status, (hipStream_t)stream, cfg->trace);
@@ -939,6 +940,7 @@ mok_status mok_balance_bwd(const mok_config* cfg, int32_t T, const mok_balance* 
   if (T == 0) return MOK_OK;
   if (!logits || !counts || !n_tok || !d_logits) return MOK_EINVAL;
   if (!aligned(logits, 4) || !aligned(d_logits, 4) || !aligned(d_loss, 4)) return MOK_EINVAL;
+  if (!aligned(counts, 4) || !aligned(n_tok, 4)) return MOK_EINVAL;
   trace_mark(cfg->trace, "start", (hipStream_t)stream);
   return launch_balance_bwd(T, cfg->E, cfg->k, balance_groups(bal), *bal, logits, counts, n_tok,
                             d_loss, d_logits, dev_status, (hipStream_t)stream, cfg->trace);

@@ -12,7 +12,7 @@
 //
 // Forward: a workgroup takes a chunk of consecutive rows, whatever groups they
 // belong to, so ragged groups load the chip evenly (a fixed number of slices
-// per group took 60 us instead of FWDUS on 131072 x 256 in 32 random groups).  A
+// per group took 60 us instead of 35 on 131072 x 256 in 32 random groups).  A
 // row is held by LPR lanes (NV logits each, 16-byte loads where E and the
 // alignment allow), so a wave takes 64 / LPR rows at a time, U times over,
 // with the next rows' loads issued before this step's arithmetic, and each
@@ -25,6 +25,13 @@
 // the groups.  A call of one group and chunk ends in the first kernel.
 // Backward: the same chunks and row layout, one pass, the row's softmax
 // formed again from registers.
+//
+// Bound by HBM when large: 131072 x 256, k = 8 in 32 groups, forward 35 us
+// (138 MB of logits and ids, 3.9 TB/s: the counts' LDS atomics and the row
+// reductions are not hidden entirely), finishing kernel 7, backward 46 (134 MB
+// read and as much written, 5.8 TB/s; part of the logits comes from the
+// memory-side cache).  Bound by latency when small: 16384 x 64 takes 7 + 7 + 7
+// us, 512 x 8 6 + 4.
 #include "mok_internal.h"
 #include "mok_lanes.h"
 
@@ -213,29 +220,33 @@ struct Rows {
 // factor in every term and in lse = (c + log2 sum) ln 2, so only the product
 // with z rounds (one fused operation); exponential, logarithm and reciprocal
 // are the hardware's (1 ulp).  Rows that do not count are rare enough to be
-// dealt with in a branch.  Returns whether there was one in the wave.
+// dealt with in a branch, and so are rows whose c is so large (all logits at a
+// mask's -1e9, or at the type's lowest value) that its rounding, or c itself,
+// would leave the exponent's range: those subtract the maximum first.
+// Returns whether there was one in the wave.
 template <int LPR, int NV, int U>
 __device__ __forceinline__ bool softmax_rows(float (&v)[U][NV], const uint32_t (&mask)[U], const bool (&in)[U],
                                              int lane, bool (&live)[U], float (&lse)[U]) {
-  constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-  float c[U];
+  constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f, kLarge = 0x1p24f;
+  float m[U], c[U], off[U];
   bool rare = false;
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     int mx = float_order(v[u][0]);
 #pragma unroll
     for (int i = 1; i < NV; ++i) mx = max(mx, float_order(v[u][i]));
-    const float m = order_float(group_max<LPR>(mx));
-    c[u] = m * kLog2e;
+    m[u] = order_float(group_max<LPR>(mx));
+    c[u] = m[u] * kLog2e;
+    off[u] = 0.0f;
     live[u] = true;
-    rare = rare || !in[u] || mask[u] == 0 || m == -__builtin_inff();
+    rare = rare || !in[u] || mask[u] == 0 || !(__builtin_fabsf(c[u]) < kLarge);
   }
   rare = __any(rare);
   if (rare) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       // all -inf, or -inf and negative NaN only: look for one
-      bool some = c[u] != -__builtin_inff();
+      bool some = m[u] != -__builtin_inff();
 #pragma unroll
       for (int i = 0; i < NV; ++i) some = some || __builtin_isnan(v[u][i]);
       const uint64_t vote = __ballot(some);
@@ -245,6 +256,11 @@ __device__ __forceinline__ bool softmax_rows(float (&v)[U][NV], const uint32_t (
         c[u] = 0.0f;
 #pragma unroll
         for (int i = 0; i < NV; ++i) v[u][i] = -__builtin_inff();
+      } else if (__builtin_fabsf(c[u]) >= kLarge && __builtin_fabsf(m[u]) < __builtin_inff()) {
+        c[u] = 0.0f;
+        off[u] = m[u];
+#pragma unroll
+        for (int i = 0; i < NV; ++i) v[u][i] -= m[u];
       }
     }
   }
@@ -258,7 +274,7 @@ __device__ __forceinline__ bool softmax_rows(float (&v)[U][NV], const uint32_t (
     }
     sum = group_sum<LPR>(sum);
     const float inv = live[u] ? __builtin_amdgcn_rcpf(sum) : 0.0f;
-    lse[u] = live[u] ? (c[u] + __builtin_amdgcn_logf(sum)) * kLn2 : 0.0f;
+    lse[u] = live[u] ? __builtin_fmaf(c[u] + __builtin_amdgcn_logf(sum), kLn2, off[u]) : 0.0f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) v[u][i] *= inv;
   }
@@ -270,7 +286,7 @@ __device__ __forceinline__ void write_totals(const BalArgs& a, int N, int groups
   a.n_tok[a.G] = N;
   a.n_tok[a.G + 1] = groups;
   a.loss[0] = groups > 0 ? (float)(a.alpha * bal / groups) : 0.0f;
-  a.loss[1] = N > 0 ? (float)(a.beta * zz / N) : 0.0f;
+  a.loss[1] = N > 0 && a.beta != 0.0f ? (float)(a.beta * zz / N) : 0.0f;   // lse^2 may be infinite
 }
 __device__ __forceinline__ double group_term(const BalArgs& a, int n, double cp) {
   return n > 0 ? cp * a.E / ((double)a.k * n * n) : 0.0;

@@ -15,12 +15,17 @@
 // dW, whose fp32 result keeps fp32's accuracy (2^-24 of each term), two for
 // dx, which is rounded to bf16 (2^-17 of each term against 2^-9).
 //   1. router_split_kernel writes the parts of dz once (and sums db);
-//   2. router_dx_kernel: a wave keeps the parts of its 32 token rows in
-//      registers for all experts and walks column steps of 64, W coming
-//      through LDS;
-//   3. router_dw_kernel: 64 x 64 of dW per wave, both operands through an
-//      LDS ring filled by direct loads, split over the tokens;
+//   2. dx: a wave keeps the parts of its 32 token rows in registers for all
+//      experts and walks column steps of 64, W coming through LDS;
+//   3. dW: 64 x 64 of dW per wave, both operands through an LDS ring filled by
+//      direct loads, split over the tokens; beside dx in one launch;
 //   4. router_reduce_kernel adds the token chunks in order.
+//
+// What bounds it.  16384 x 2048 x 64: HBM (x read, d_x written, 67 MB each):
+// split 6 us, both products 30, reduction 5.  4096 x 7168 x 256: the matrix
+// cores, 75 GFLOP in five parts: split 6 us, both products 81 (0.93 PFLOP/s; a
+// large library product reaches 1.23), reduction 9.  fp32, 512 x 256 x 8:
+// launch latency, 7 + 3 us.
 #include <math.h>
 
 #include <algorithm>
@@ -677,7 +682,7 @@ __global__ __launch_bounds__(kBf16Threads, 2) void router_dw_bf16_kernel(RArgs a
 // Both products in one launch, dW's workgroups first: they are the longer
 // ones, and the dx workgroups that fill the CUs beside and after them store
 // under their loads (16384 x 2048 x 64: 49 us in all against 55 one after the
-// other; taking turns 60; 14336 x 7168 x 256, which the matrix cores bound:
+// other; taking turns 60; 4096 x 7168 x 256, which the matrix cores bound:
 // no difference).
 template <int NK, int EW, bool STREAM>
 __global__ __launch_bounds__(kThreads, 2) void router_both_bf16_kernel(RArgs a, int dw_wgs) {

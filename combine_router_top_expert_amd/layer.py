@@ -78,6 +78,7 @@ class MoELayer:
                                 self.row_src, self.dest_row, self.h, self.ab, self.h_scale,
                                 self.logits)
         self.with_bwd = with_bwd
+        self._bal_bufs = {}
         # bf16 backward: the weights also transposed (mok_prepare_bwd), so dh
         # and dx read them k-contiguous (bit-identical either way)
         self.transposed_weights = transposed_weights
@@ -199,12 +200,24 @@ class MoELayer:
                       self.dw_gate, self.dw_up, self.dw_down,
                       self.dw_router if router_grad else None, self.ws, self.status, stream)
 
+    def _after_current(self, stream):
+        """Work on `stream` waits for the current one: a new buffer may be
+        memory that the current stream still works on."""
+        if stream is None:
+            return
+        s = torch.cuda.ExternalStream(stream, device=self.device) if isinstance(stream, int) else stream
+        with torch.cuda.device(self.device):
+            if s != torch.cuda.current_stream():
+                s.wait_stream(torch.cuda.current_stream())
+
     def balance_loss(self, alpha, beta=0.0, group_offsets=None, token_mask=None, stream=None):
         """Balance loss and z-loss of the last forward's own tokens (fp32 [2]
         on the device; needs keep_logits).  group_offsets: int32 [G+1] over
         the own rows (sequences), None = one group; token_mask: uint8 [own
         rows] or None.  Leaves counts_all [G, E], prob [G, E] and n_tok
-        [G+2]."""
+        [G+2]; they and the losses are overwritten by the next call with as
+        many groups (buffers are kept per number of groups, so that a captured
+        call's stay)."""
         if self.logits is None:
             raise RuntimeError("balance_loss needs MoELayer(keep_logits=True)")
         T, dev = self.own_n * self.T_src, self.logits.device
@@ -218,13 +231,13 @@ class MoELayer:
         self._bal = make_balance(alpha, beta, G, group_offsets, token_mask)
         self._bal_keep = (group_offsets, token_mask)
         rows = max(G, 1)
-        if getattr(self, "n_tok", None) is None or self.n_tok.numel() != rows + 2:
-            self.counts_all = torch.zeros(rows, self.E, dtype=torch.int32, device=dev)
-            self.prob = torch.zeros(rows, self.E, dtype=torch.float32, device=dev)
-            self.n_tok = torch.zeros(rows + 2, dtype=torch.int32, device=dev)
-            self.loss = torch.zeros(2, dtype=torch.float32, device=dev)
-            self.ws_bal = torch.zeros(mok_balance_ws_bytes(self.cfg, T, self._bal),
-                                      dtype=torch.uint8, device=dev)
+        if rows not in self._bal_bufs:
+            e = lambda t, *n: torch.empty(*n, dtype=t, device=dev)  # noqa: E731
+            self._bal_bufs[rows] = (e(torch.int32, rows, self.E), e(torch.float32, rows, self.E),
+                                    e(torch.int32, rows + 2), e(torch.float32, 2),
+                                    e(torch.uint8, mok_balance_ws_bytes(self.cfg, T, self._bal)))
+            self._after_current(stream)
+        self.counts_all, self.prob, self.n_tok, self.loss, self.ws_bal = self._bal_bufs[rows]
         lo = self.own_lo * self.T_src
         mok_balance_fwd(self.cfg, T, self._bal, self.logits[lo:], self.topk_idx[lo * self.k:],
                         self.counts_all, self.prob, self.n_tok, self.loss, self.ws_bal,
@@ -239,9 +252,11 @@ class MoELayer:
             raise RuntimeError("balance_backward needs balance_loss and backward before it")
         T, lo = self.own_n * self.T_src, self.own_lo * self.T_src
         if getattr(self, "d_logits", None) is None:
+            # (zeros: rows outside every group keep theirs)
             self.d_logits = torch.zeros(max(T, 1), self.E, dtype=torch.float32, device=self.device)
-            self.ws_router = torch.zeros(mok_router_bwd_ws_bytes(self.cfg, self.own_n),
+            self.ws_router = torch.empty(mok_router_bwd_ws_bytes(self.cfg, self.own_n),
                                          dtype=torch.uint8, device=self.device)
+            self._after_current(stream)
         mok_balance_bwd(self.cfg, T, self._bal, self.logits[lo:], self.counts_all, self.n_tok,
                         d_loss, self.d_logits, self.status, stream)
         mok_router_bwd(self.cfg, self.own_lo, self.own_n, self.d_logits, self.xs, self.w_router,

@@ -65,7 +65,8 @@ class AdamW:
         self.args = make_adamw(lr, betas[0], betas[1], eps, seed=seed, random_params=random_params,
                                dev_scale=self.norm[1:] if max_norm is not None else None,
                                dev_lr=self.dev_lr, dev_step=self.dev_step)
-        self._grads = None
+        self._grads = self._ws = None
+        self._behind = True      # the current stream holds work that a step has to see
 
     def state_dict(self) -> dict:
         """Moments, fp32 copies and step number (the tensors themselves)."""
@@ -89,11 +90,13 @@ class AdamW:
         self.step_count = int(state["step"])
         if self.dev_step is not None:
             self.dev_step.fill_(self.step_count)
+        self._behind = True
 
     def set_lr(self, lr: float):
         self.args.lr = lr
         if self.dev_lr is not None:
             self.dev_lr.fill_(lr)
+            self._behind = True
 
     def bind(self, grads: Sequence[torch.Tensor]):
         """Descriptors for these gradient tensors (kept: step() without
@@ -111,22 +114,33 @@ class AdamW:
             for p, g, m, v, w, ms, vs, wd in zip(self.params, grads, self.m, self.v, self.master,
                                                  self.m_scale, self.v_scale, self.weight_decay)])
         self._grads = grads
-        if self.max_norm is not None:
-            self._ws = torch.zeros(mok_grad_norm_ws_bytes(self._desc), dtype=torch.uint8,
+        if self.max_norm is not None and self._ws is None:   # (its size follows from the parameters')
+            self._ws = torch.empty(mok_grad_norm_ws_bytes(self._desc), dtype=torch.uint8,
                                    device=self.device)
+            self._behind = True
 
     def step(self, grads: Optional[Sequence[torch.Tensor]] = None, grad_scale: float = 1.0,
              stream=None):
         """One step on `stream` (a torch stream; None: the device's current
-        one).  grads:
-        gradients to bind, or None for those bound before.  Gradients are
-        multiplied by grad_scale (the norm is taken before)."""
+        one).  grads: gradients to bind, or None for those bound before.
+        Gradients are multiplied by grad_scale > 0 (the norm is taken
+        before)."""
+        if not grad_scale > 0.0:
+            raise ValueError(f"grad_scale above zero expected, got {grad_scale}")
         if grads is not None:
             self.bind(grads)
         if self._grads is None:
             raise RuntimeError("step() before any gradients were bound")
+        if self.device.type != "cuda":
+            raise ValueError(f"a step needs parameters on a GPU, not on {self.device}")
+        if self.dev_step is None and torch.cuda.is_current_stream_capturing():
+            raise RuntimeError("a captured step needs AdamW(capturable=True): its number would stand still")
         with torch.cuda.device(self.device):
-            s = torch.cuda.current_stream() if stream is None else stream
+            cur = torch.cuda.current_stream()
+            s = cur if stream is None else stream
+            if self._behind and s != cur:
+                s.wait_stream(cur)
+            self._behind = False
             if self.max_norm is not None:
                 mok_grad_norm(self._desc, self.max_norm / grad_scale, self.norm, self._ws, s)
             self.step_count += 1

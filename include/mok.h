@@ -458,8 +458,9 @@ size_t mok_router_bwd_ws_bytes(const mok_config* cfg, int32_t own_n);
  * beside its rounding.  No output may overlap an input.  src_x is needed for dw_router, w_router
  * for d_x; fp32 for MOK_F32, else bf16, 16-byte aligned like the outputs;
  * d at most 2^26.  Without own rows dw_router and d_bias become zero (or
- * stay, with accumulate).  A NaN or infinity in d_logits makes its row of
- * d_x and its expert's dw_router and d_bias not finite. */
+ * stay, with accumulate).  A NaN or infinity in d_logits (for bf16 layers
+ * also a value that bf16 rounds to infinity, from 3.39e38 on) makes its row
+ * of d_x and its expert's dw_router and d_bias not finite. */
 mok_status mok_router_bwd(const mok_config* cfg, int32_t own_lo, int32_t own_n,
                           const float* d_logits, const void* const* src_x, const void* w_router,
                           void* const* d_x, float* dw_router, float* d_bias, int32_t accumulate,

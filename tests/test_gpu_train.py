@@ -83,7 +83,7 @@ def _balance_ref(z, topk, E, k, alpha, beta, off, mask, d_loss, dz0):
         if not n[g]:
             continue
         lse = torch.logsumexp(z[r], 1)
-        p = torch.exp(z[r] - lse[:, None])
+        p = torch.softmax(z[r], 1)
         ids = topk[r].reshape(-1).long()
         counts[g] = torch.bincount(ids[(ids >= 0) & (ids < E)], minlength=E)
         f = counts[g].double() * E / (k * n[g])
@@ -230,6 +230,33 @@ def test_balance_rows_of_minus_infinity_and_nan():
     zb[5] = float("nan")
     got = _balance_run(zb, topk, E, k, 1e-2, 1e-3, None, None, [1.0, 1.0], torch.zeros(T, E))
     assert got[3][0] == T - 1 and torch.isnan(got[0]).all()
+
+
+@pytest.mark.parametrize("E", [8, 60, 256])
+def test_balance_rows_at_the_ends_of_the_range(E):
+    """Rows whose logits are all, or but for some, a type's lowest value (a
+    finite mask), and rows near the largest: maximum times log2 e passes
+    fp32's range there.  The z-loss weight is zero (lse^2 is not finite)."""
+    _log("balance ends", E)
+    T, k = 90, 2
+    z, topk = _logits(T, E, k, seed=6)
+    low = [torch.finfo(t).min for t in (torch.float32, torch.bfloat16, torch.float16)]
+    for i, v in enumerate(low + [3.0e38, torch.finfo(torch.float32).max]):
+        z[10 * i] = v
+        z[10 * i + 1, : E // 2] = v
+        z[10 * i + 2, 1:] = v
+    z[70], z[70, 3] = low[0], low[0] / 2
+    z[71], z[71, ::2] = 3.0e38, torch.nextafter(torch.tensor(3.0e38), torch.tensor(0.0))
+    for i, v in enumerate((-1e9, 1e9, -1e7, 3e7, -1e12, 1e20)):
+        z[72 + i] += v
+    ref = _balance_ref(z, topk, E, k, 1e-2, 0.0, [0, 40, T], None, [1.0, 1.0], torch.zeros(T, E))
+    got = _balance_run(z, topk, E, k, 1e-2, 0.0, [0, 40, T], None, [1.0, 1.0], torch.full((T, E), 9.0))
+    assert got[5] == 0 and got[3].tolist() == ref[3] and torch.equal(got[1].long(), ref[1])
+    # p: 2^-22 of itself (exponential, reciprocal, the exponent's rounding up to
+    # 2^-24 of 25 beyond which p is below 2^-36 of the row), sums of E terms
+    _within(got[2], ref[2], 64 * U * ref[2] + 2.0 ** -36, "prob")
+    _within(got[0], ref[0], 64 * U * ref[0].abs() + 1e-9, "loss")
+    _within(got[4], ref[4], ref[5] + 2.0 ** -36, "d_logits")
 
 
 def test_balance_bad_ids_and_offsets_are_latched():
@@ -767,6 +794,28 @@ def test_adamw_8bit_moments_follow_a_slow_average():
     assert abs(float(m.mean()) - 1) < 0.01
 
 
+@pytest.mark.parametrize("eps", [0.0, 1e-30])
+def test_adamw_tiny_second_moments_with_tiny_eps(eps):
+    """v down to fp32's subnormals where no eps hides it: the update from the
+    moments that the step stored, in 64 bits."""
+    _log("adamw tiny v", eps)
+    n, step = 4096, 3
+    gen = _gen(3)
+    g = torch.randn(n, generator=gen) * 10.0 ** torch.linspace(-21, -16, n)
+    g[g == 0] = 1e-19
+    p, m, v = torch.zeros(n), 0.1 * g, 0.5 * g * g
+    d = [t.to(DEV) for t in (p, g, m, v)]
+    params = mok.make_params([mok.make_param(p=d[0], g=d[1], m=d[2], v=d[3])])
+    mok.mok_adamw(params, mok.make_adamw(1.0, 0.9, 0.99, eps, step=step))
+    torch.cuda.synchronize()
+    m, v = d[2].cpu().double(), d[3].cpu().double()
+    keep = v > 0
+    assert int(keep.sum()) > n // 2 and float(v[keep].min()) < 2.0 ** -126
+    want = -m / (1 - 0.9 ** step) / (v.sqrt() / math.sqrt(1 - 0.99 ** step) + eps)
+    # root, product with the correction, sum, reciprocal, two products
+    _within(d[0].cpu()[keep], want[keep], 16 * U * want[keep].abs(), "p")
+
+
 def test_adamw_captured_steps_match_eager():
     """A captured step (norm, clip, update, step number and learning rate on
     the device) replayed with eager work in between equals eager steps, bit
@@ -1062,3 +1111,72 @@ def test_bf16_layer_keeps_its_copies_in_step():
         L.update_weights()
         for a, b in zip(step(L), step(layer())):
             assert torch.equal(a.view(torch.uint8), b.view(torch.uint8)), prec
+
+
+def test_optimizer_refuses_a_captured_step_with_a_host_number(monkeypatch):
+    opt = AdamW([torch.zeros(8, device=DEV)])
+    opt.bind([torch.zeros(8, device=DEV)])
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: True)
+    with pytest.raises(RuntimeError, match="capturable"):
+        opt.step()
+
+
+def _balance_layer():
+    S, T, d, E, k, I = 1, 300, 64, 8, 2, 64
+    gen = _gen(13)
+    rnd = lambda *s: torch.randn(*s, generator=gen).to(DEV)  # noqa: E731
+    L = MoELayer(S, T, d, E, k, I, E, "f32", T * k, 0, 1, device=DEV, keep_logits=True)
+    L.set_inputs([rnd(T, d)], rnd(E, d), None, torch.arange(E, dtype=torch.int32, device=DEV), rnd(E, I, d),
+                 rnd(E, I, d), rnd(E, d, I))
+    dout = [rnd(T, d)]
+    off = [torch.tensor(o, dtype=torch.int32, device=DEV) for o in ([0, 100, 300], [0, 50, 90, 300])]
+    return L, dout, off
+
+
+def test_training_calls_on_a_side_stream():
+    """Balance loss, its gradient and a clipped step on a stream other than
+    the current one, whose buffers are made by these calls, while the current
+    stream is busy: the bytes of the same calls on the current stream."""
+    _log("side stream")
+
+    def run(side):
+        L, dout, off = _balance_layer()
+        w = [t.clone() for t in (L.w_router, L.w_gate)]
+        opt = AdamW(w, max_norm=0.1, state_bits=[32, 8])
+        L.forward()
+        L.backward(dout)
+        torch.cuda.synchronize()
+        busy = torch.ones(1 << 26, device=DEV)
+        if side is not None:
+            for _ in range(20):
+                busy.mul_(1.0)
+        loss = [L.balance_loss(0.5, 0.01, o, stream=side).clone() if side is None else
+                L.balance_loss(0.5, 0.01, o, stream=side) for o in off]
+        L.balance_backward(stream=side)
+        opt.step([L.dw_router, L.dw_gate], stream=side)
+        torch.cuda.synchronize()
+        L.check_status()
+        return [t.clone() for t in (*loss, L.d_x[0], L.dw_router, *w)]
+    for a, b in zip(run(None), run(torch.cuda.Stream())):
+        assert torch.equal(a, b)
+
+
+def test_captured_balance_keeps_its_buffers():
+    """A captured call replayed after calls with other numbers of groups."""
+    _log("balance buffers")
+    L, dout, off = _balance_layer()
+    L.forward()
+    L.balance_loss(0.5, 0.01, off[0])
+    torch.cuda.synchronize()
+    cg = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(cg):
+        loss = L.balance_loss(0.5, 0.01, off[0])
+    for i in range(3):
+        other = L.balance_loss(0.5, 0.01, off[1]).clone()
+        junk = [torch.full((n,), float("nan"), device=DEV) for n in (2, 4, 16, 24, 1000)]
+        cg.replay()
+        torch.cuda.synchronize()
+        assert all(bool(torch.isnan(j).all()) for j in junk)
+        replayed = loss.clone()
+        assert torch.equal(replayed, L.balance_loss(0.5, 0.01, off[0])), i
+        assert torch.equal(other, L.balance_loss(0.5, 0.01, off[1])), i

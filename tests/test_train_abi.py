@@ -247,3 +247,31 @@ def test_layer_balance_refusals():
                 dict(group_offsets=torch.zeros(0, dtype=torch.int32))):
         with pytest.raises(ValueError):
             L.balance_loss(0.1, **bad)
+
+
+def test_optimizer_steps_on_a_gpu_only():
+    from combine_router_top_expert_amd.optim import AdamW
+    opt = AdamW([torch.zeros(8)])
+    for scale in (0.0, -1.0, float("nan")):
+        with pytest.raises(ValueError, match="grad_scale"):
+            opt.step([torch.zeros(8)], grad_scale=scale)
+    with pytest.raises(ValueError, match="GPU"):
+        opt.step([torch.zeros(8)])
+
+
+def test_balance_misaligned_outputs_are_refused():
+    """Pointers that no kernel of the call may dereference: refused before any launch."""
+    cfg = mok.make_config(1, 8, 64, 8, 2, 64, 1, "f32", 0)
+    bal, at = mok.make_balance(1e-2, 1e-3), 1 << 20
+    ok = dict(logits=at, topk=at, counts=at, prob=at, n_tok=at, loss=at)
+    for bad in ok:
+        a = {**ok, bad: at + 2}
+        with pytest.raises(RuntimeError):
+            mok.mok_balance_fwd(cfg, 8, bal, a["logits"], a["topk"], a["counts"], a["prob"], a["n_tok"], a["loss"],
+                                at, None, 0)
+    for bad in (dict(counts=at + 2), dict(n_tok=at + 1)):
+        a = {**ok, **bad}
+        with pytest.raises(RuntimeError):
+            mok.mok_balance_bwd(cfg, 8, bal, at, a["counts"], a["n_tok"], None, at, None, 0)
+    with pytest.raises(RuntimeError):
+        mok.mok_balance_fwd(cfg, 8, mok.make_balance(1e-2, 1e-3, 2, at + 2, None), at, at, at, at, at, at, at, None, 0)
