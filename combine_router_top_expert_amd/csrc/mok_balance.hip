@@ -12,7 +12,7 @@
 //
 // Forward: a workgroup takes a chunk of consecutive rows, whatever groups they
 // belong to, so ragged groups load the chip evenly (a fixed number of slices
-// per group took 60 us instead of 35 on 131072 x 256 in 32 random groups).  A
+// per group took 60 us where chunks took 35 on 131072 x 256 in 32 random groups).  A
 // row is held by LPR lanes (NV logits each, 16-byte loads where E and the
 // alignment allow), so a wave takes 64 / LPR rows at a time, U times over,
 // with the next rows' loads issued before this step's arithmetic, and each
@@ -26,8 +26,8 @@
 // Backward: the same chunks and row layout, one pass, the row's softmax
 // formed again from registers.
 //
-// Bound by HBM when large: 131072 x 256, k = 8 in 32 groups, forward 35 us
-// (138 MB of logits and ids, 3.9 TB/s: the counts' LDS atomics and the row
+// Bound by HBM when large: 131072 x 256, k = 8 in 32 groups, forward 30 us
+// (138 MB of logits and ids, 4.6 TB/s: the counts' LDS atomics and the row
 // reductions are not hidden entirely), finishing kernel 7, backward 46 (134 MB
 // read and as much written, 5.8 TB/s; part of the logits comes from the
 // memory-side cache).  Bound by latency when small: 16384 x 64 takes 7 + 7 + 7
@@ -621,12 +621,18 @@ struct Shape {
 
 // Lanes per row and values per lane: 16-byte units where rows start aligned,
 // at most 64 lanes, the fewest that hold the row with one unit (value) each.
-Shape row_shape(int E, uintptr_t align) {
+// Rows of 33 to 64 units take 32 lanes when there are many: two rows of a
+// wave then share the steps of the row reductions (131072 x 256: 87 us against
+// 90, forward 30 against 35; 16 lanes: 29, but the backward 48 against 46),
+// while fewer rows are over sooner with twice the waves (16384 x 256: 27
+// against 29, equal at 50000).
+Shape row_shape(int T, int E, uintptr_t align) {
   Shape s;
   s.vec = E % 4 == 0 && align % 16 == 0;
   const int units = s.vec ? E / 4 : E;
+  const int most = s.vec && units <= 64 && T >= 1 << 16 ? 32 : 64;
   s.lpr = 1;
-  while (s.lpr < 64 && s.lpr < units) s.lpr <<= 1;
+  while (s.lpr < most && s.lpr < units) s.lpr <<= 1;
   int per = 1;
   while (per * s.lpr < units) per <<= 1;
   s.nv = s.vec ? 4 * per : per;
@@ -637,7 +643,7 @@ Shape row_shape(int E, uintptr_t align) {
 // group of up to four steps is one chunk, whose workgroup needs no second
 // kernel to finish (512 x 8: 5 us in all against 11).
 int chunk_rows(int T, int E, int G) {
-  const Shape s = row_shape(E, 0);
+  const Shape s = row_shape(T, E, 0);
   const int64_t step = (int64_t)kBalWaves * (64 / s.lpr) * (s.nv >= 8 ? rows_at_once<8>() : rows_at_once<4>());
   if (G == 1 && T <= 4 * step) return (int)(4 * step);
   const int64_t n = (T + kBalWgs * step - 1) / (kBalWgs * step);
@@ -677,6 +683,7 @@ void launch_shape(const Shape& s, const BalArgs& a, hipStream_t st) {
   MOK_BAL(8, 4, true);
   MOK_BAL(16, 4, true);
   MOK_BAL(32, 4, true);
+  MOK_BAL(32, 8, true);
   MOK_BAL(64, 4, true);
   MOK_BAL(64, 8, true);
   MOK_BAL(1, 1, false);
@@ -729,7 +736,7 @@ mok_status launch_balance_fwd(int T, int E, int k, int G, const mok_balance& b, 
   a.ticket = (int32_t*)p;
   a.counts = counts, a.prob = prob, a.n_tok = n_tok, a.loss = loss;
   a.alpha = b.alpha, a.beta = b.beta;
-  launch_shape<false>(row_shape(E, (uintptr_t)logits), a, stream);
+  launch_shape<false>(row_shape(T, E, (uintptr_t)logits), a, stream);
   trace_mark(tr, "balance_fwd", stream);
   if (a.chunks > 1 || G > 1) {
     hipLaunchKernelGGL(balance_finish_kernel, dim3(G, fin_blocks(E)), dim3(kFinThreads), 0, stream, a);
@@ -760,7 +767,7 @@ mok_status launch_balance_bwd(int T, int E, int k, int G, const mok_balance& b, 
   // cache by the router's backward).
   a.stream = (int64_t)T * E * 8 >= (int64_t)256 << 20;
   a.alpha = b.alpha, a.beta = b.beta;
-  launch_shape<true>(row_shape(E, (uintptr_t)logits | (uintptr_t)d_logits), a, stream);
+  launch_shape<true>(row_shape(T, E, (uintptr_t)logits | (uintptr_t)d_logits), a, stream);
   trace_mark(tr, "balance_bwd", stream);
   return hipGetLastError() == hipSuccess ? MOK_OK : MOK_EDEVICE;
 }

@@ -421,8 +421,9 @@ size_t mok_balance_ws_bytes(const mok_config* cfg, int32_t T, const mok_balance*
  * group), n_tok [G+2] = N_g of every group, then N, then G+; loss [2] =
  * L_balance, L_z.  An id outside [0, E) latches MOK_EROUTE and is not
  * counted; offsets that do not ascend within [0, T] latch MOK_EGROUP and
- * nothing counts.  NaN logits of counted rows reach the losses; values
- * of rows that do not count are never used. */
+ * nothing counts.  NaN logits of counted rows reach the losses
+ * (with beta 0 loss[1] is 0); values of rows that do not count are never
+ * used. */
 mok_status mok_balance_fwd(const mok_config* cfg, int32_t T, const mok_balance* bal,
                            const float* logits, const int32_t* topk_idx, int32_t* counts,
                            float* prob, int32_t* n_tok, float* loss, void* ws,

@@ -157,6 +157,9 @@ BALANCE = [
     (3000, 256, 8, [0, 0, 0, 1, 2, 17, 17, 2900, 2990, 2990], 0.1, 0),
     (2500, 512, 2, [3] + list(range(3, 2400, 7)) + [2499], 0, 0),
     (40000, 16, 4, [0, 39999, 39999, 40000], 0, 0),
+    # many rows: two to a wave where 33 to 64 units of 16 bytes hold one
+    (65537, 132, 4, [5, 5, 21, 30000, 65530], 0.1, 7),
+    (65600, 256, 2, None, 0, 0),
 ]
 
 
