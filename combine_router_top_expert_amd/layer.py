@@ -200,14 +200,18 @@ class MoELayer:
                       self.dw_gate, self.dw_up, self.dw_down,
                       self.dw_router if router_grad else None, self.ws, self.status, stream)
 
+    def _torch_stream(self, stream):
+        """The torch stream of a call's `stream` (None: the current one, or a raw handle)."""
+        if isinstance(stream, int):
+            return torch.cuda.ExternalStream(stream, device=self.device)
+        return stream
+
     def _after_current(self, stream):
         """Work on `stream` waits for the current one: a new buffer may be
         memory that the current stream still works on."""
-        if stream is None:
-            return
-        s = torch.cuda.ExternalStream(stream, device=self.device) if isinstance(stream, int) else stream
+        s = self._torch_stream(stream)
         with torch.cuda.device(self.device):
-            if s != torch.cuda.current_stream():
+            if s is not None and s != torch.cuda.current_stream():
                 s.wait_stream(torch.cuda.current_stream())
 
     def balance_loss(self, alpha, beta=0.0, group_offsets=None, token_mask=None, stream=None):
@@ -252,11 +256,13 @@ class MoELayer:
             raise RuntimeError("balance_backward needs balance_loss and backward before it")
         T, lo = self.own_n * self.T_src, self.own_lo * self.T_src
         if getattr(self, "d_logits", None) is None:
-            # (zeros: rows outside every group keep theirs)
-            self.d_logits = torch.zeros(max(T, 1), self.E, dtype=torch.float32, device=self.device)
+            self.d_logits = torch.empty(max(T, 1), self.E, dtype=torch.float32, device=self.device)
             self.ws_router = torch.empty(mok_router_bwd_ws_bytes(self.cfg, self.own_n),
                                          dtype=torch.uint8, device=self.device)
             self._after_current(stream)
+        if self._bal.G > 0:      # rows outside every group are not written: they add nothing
+            with torch.cuda.stream(self._torch_stream(stream)):
+                self.d_logits.zero_()
         mok_balance_bwd(self.cfg, T, self._bal, self.logits[lo:], self.counts_all, self.n_tok,
                         d_loss, self.d_logits, self.status, stream)
         mok_router_bwd(self.cfg, self.own_lo, self.own_n, self.d_logits, self.xs, self.w_router,

@@ -35,6 +35,8 @@ class AdamW:
         self.params = list(params)
         if not self.params:
             raise ValueError("no parameters")
+        if max_norm is not None and not max_norm > 0.0:
+            raise ValueError(f"max_norm above zero (or None) expected, got {max_norm}")
         dev = self.params[0].device
         per = lambda v: list(v) if isinstance(v, (list, tuple)) else [v] * len(self.params)  # noqa: E731
         self.weight_decay, self.state_bits = per(weight_decay), per(state_bits)

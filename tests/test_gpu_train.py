@@ -1183,3 +1183,21 @@ def test_captured_balance_keeps_its_buffers():
         replayed = loss.clone()
         assert torch.equal(replayed, L.balance_loss(0.5, 0.01, off[0])), i
         assert torch.equal(other, L.balance_loss(0.5, 0.01, off[1])), i
+
+
+def test_balance_backward_forgets_rows_of_earlier_groups():
+    """Rows outside the groups of this call add nothing, though they were in
+    those of the call before."""
+    _log("balance rows outside")
+
+    def run(offs):
+        L, dout, _ = _balance_layer()
+        L.forward()
+        for o in offs:
+            L.balance_loss(0.5, 0.01, torch.tensor(o, dtype=torch.int32, device=DEV))
+            L.backward(dout)
+            L.balance_backward()
+        torch.cuda.synchronize()
+        return L.d_x[0].clone(), L.dw_router.clone()
+    for a, b in zip(run([[20, 120]]), run([[0, 300], [20, 120]])):
+        assert torch.equal(a, b)

@@ -275,3 +275,10 @@ def test_balance_misaligned_outputs_are_refused():
             mok.mok_balance_bwd(cfg, 8, bal, at, a["counts"], a["n_tok"], None, at, None, 0)
     with pytest.raises(RuntimeError):
         mok.mok_balance_fwd(cfg, 8, mok.make_balance(1e-2, 1e-3, 2, at + 2, None), at, at, at, at, at, at, at, None, 0)
+
+
+@pytest.mark.parametrize("max_norm", [0.0, -1.0, float("nan")])
+def test_optimizer_refuses_norms_that_do_not_clip(max_norm):
+    from combine_router_top_expert_amd.optim import AdamW
+    with pytest.raises(ValueError, match="max_norm"):
+        AdamW([torch.zeros(8)], max_norm=max_norm)
