@@ -25,7 +25,9 @@
 // split 6 us, both products 30, reduction 5.  4096 x 7168 x 256: the matrix
 // cores, 75 GFLOP in five parts: split 6 us, both products 81 (0.93 PFLOP/s; a
 // large library product reaches 1.23), reduction 9.  fp32, 512 x 256 x 8:
-// launch latency, 7 + 3 us.
+// launch latency, 7 + 3 us; 4096 x 7168 x 256: 360 us, 83 TFLOP/s of the 154
+// that a library product reaches (vector work for addresses and LDS stores
+// beside the matrix cores, which are 61 % busy).
 #include <math.h>
 
 #include <algorithm>
@@ -39,7 +41,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kTile = 64;   // fp32: tile side
-constexpr int kKB = 32;     // and contraction steps staged through LDS at a time
+constexpr int kKB = 16;     // and contraction steps staged through LDS at a time (32: up to 12 % slower, with half the waves)
 constexpr int kPitch = kTile + 4;
 constexpr int kDxWaves = 4;
 constexpr int kDwWaves = 4;         // dW: two workgroups per CU (one of eight waves: 54 against 49 us)
@@ -748,7 +750,9 @@ int expert_tile(int E) { return (E + 63) / 64 % 2 ? 64 : 128; }
 int padded_experts(int E) { return E <= 64 ? 64 : E <= 128 ? 128 : E <= 256 ? 256 : 512; }
 
 // Token chunks of the dW product, at least 64 tokens each, and the workspace
-// that follows from them.  fp32: workgroups for four per CU.
+// that follows from them.  fp32: workgroups for two per CU or a little more
+// (for four: 4 to 15 % slower but at 448 tiles, where this rule takes two
+// chunks as well).
 struct Plan {
   int chunks = 1, ew = 0, etiles = 0, db_parts = 0;
   int64_t chunk_rows = 0, split_rows = 0;
@@ -765,7 +769,7 @@ Plan make_plan(int prec, int64_t T, int d, int E) {
   const int64_t unit = f32 ? kKB : kBK;
   int64_t c;
   if (f32) {
-    c = 1024 / tiles;
+    c = (512 + tiles - 1) / tiles;
   } else {
     // a chunk costs E d 8 bytes (written and read) at about 5 TB/s, 16 tokens
     // of a workgroup 0.25 us while there are fewer workgroups than CUs hold:
