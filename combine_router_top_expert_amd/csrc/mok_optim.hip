@@ -13,8 +13,8 @@
 // fp32 gradient, master and moments and a bf16 copy, 30 bytes an element,
 // 3.16 ms (5.2 TB/s, the copy probe's rate); 352 million elements with 8-bit
 // moments, 18 bytes an element, 1.19 ms (5.3 TB/s).  120 bf16 tensors of 44
-// million elements in all with 8-bit moments, 10 bytes an element, take 114 us
-// in three launches (45 + 45 + 24): each start and end of a launch costs some
+// million elements in all with 8-bit moments, 10 bytes an element, take 116 us
+// in three launches (47 + 47 + 25): each start and end of a launch costs some
 // 7 us, and the arithmetic of two encodings nearly as much as the bytes.
 #include "mok_internal.h"
 #include "mok_lanes.h"
@@ -301,7 +301,7 @@ __device__ __forceinline__ int encode8(const float (&x)[8], const uint32_t (&rnd
 // hardware's reciprocal root (1 ulp) and one step of Newton's for the root,
 // whose residual v - r r is exact.  A v below 2^-126 gives v 2^63: above zero
 // too, and hidden by an eps of kEps or more; with a smaller one the library's
-// root is taken (8 us more on 43 million elements of 8-bit moments).
+// root is taken (6 us more on 43 million elements of 8-bit moments).
 constexpr float kEps = 1e-15f;
 __device__ __forceinline__ float root(float v) {
   const float h = __builtin_amdgcn_rsqf(__builtin_fmaxf(v, 0x1p-126f));
