@@ -11,12 +11,15 @@
 // bf16 layers: x and W are bf16, dz is fp32.  A fp32 value is the sum of
 // three bf16 parts (hi = bf16(v), mid = bf16(v - hi), lo = bf16(v - hi -
 // mid): 8 bits each, exact in between), so the products run on the bf16
-// matrix cores, eight times the fp32 rate, once per part: three parts for
-// dW, whose fp32 result keeps fp32's accuracy (2^-24 of each term), two for
-// dx, which is rounded to bf16 (2^-17 of each term against 2^-9).
+// matrix cores, eight times the fp32 rate, once per part: dz is exact in both
+// products, whose sums are fp32.  (Two parts are not enough for dx either,
+// though it is rounded to bf16: rows of dz that sum to about zero cancel what
+// the rows of W have in common, and the third part is what is left.)
 //   1. router_split_kernel writes the parts of dz once (and sums db);
-//   2. dx: a wave keeps the parts of its 32 token rows in registers for all
-//      experts and walks column steps of 64, W coming through LDS;
+//   2. dx: a wave keeps the parts of its 32 token rows in registers for up to
+//      128 experts (256 above 256) and walks column steps of 64, W coming
+//      through LDS; above 128 experts two waves share the rows, half of the
+//      experts each, and exchange halves of their sums;
 //   3. dW: 64 x 64 of dW per wave, both operands through an LDS ring filled by
 //      direct loads, split over the tokens; beside dx in one launch;
 //   4. router_reduce_kernel adds the token chunks in order.
@@ -263,6 +266,14 @@ __device__ __forceinline__ void barrier() {
   asm volatile("" ::: "memory");
 }
 
+// This wave's LDS work, and with LOADS its direct loads, are done; no access
+// moves across it.
+template <bool LOADS>
+__device__ __forceinline__ void complete() {
+  if constexpr (LOADS) asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+  else asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+}
+
 // ------------------------------------------------------------------ bf16: dx
 // Fragment of 32 columns from n (k = 16 s ..) of an LDS tile of 64 columns
 // (128-byte k-rows) read with ds_read_b64_tr_b16: in a 16-lane group lane a
@@ -281,20 +292,29 @@ __device__ __forceinline__ bf16x8_t frag64(const char* lds, int n0, int s) {
   return __builtin_bit_cast(bf16x8_t, __builtin_shufflevector(h[0], h[1], 0, 1, 2, 3, 4, 5, 6, 7));
 }
 
-// NK: 16-expert steps (E <= 16 NK); four waves of 32 token rows each, two
-// workgroups per CU up to NK = 16 (one computes while the other stores).
-// STREAM: nontemporal stores of d_x.
+// NK: 16-expert steps (E <= 16 NK); KS: waves that share 32 token rows, each
+// with NK / KS of the steps (three parts of 16 steps are all the registers of
+// a wave where two workgroups share a CU).  Four waves, two workgroups per CU
+// up to NK = 16 (one computes while the other stores).  STREAM: nontemporal
+// stores of d_x.
 template <int NK>
-constexpr int dx_lds() { return 2 * NK * 16 * 128 + kDxWaves * 4096; }
+constexpr int dx_split() { return NK >= 16 ? 2 : 1; }
+template <int NK>
+constexpr int dx_rows() { return 32 * kDxWaves / dx_split<NK>(); }
+template <int NK>
+constexpr int dx_lds() { return 2 * NK * 16 * 128 + dx_rows<NK>() / 32 * 4096; }
 
 template <int NK, bool STREAM>
 __device__ __forceinline__ void dx_bf16(const RArgs& a, int b, char* smem) {
+  constexpr int KS = dx_split<NK>(), NKW = NK / KS, ROWS = dx_rows<NK>();
   constexpr int STAGE = NK * 16 * 128;               // bytes of W per column step
   constexpr int LOADS = STAGE / 1024 / kDxWaves;     // direct loads per wave and step
+  static_assert(KS == 1 || STAGE >= kDxWaves * 4096, "the exchange takes a stage of W");
   const int lane = threadIdx.x & 63;
   const int wave = (int)g2::wave_id();
+  const int rg = wave / KS, kh = wave % KS;          // row group, part of the experts
   // workgroups of one row block on one XCD (b % 8), so its parts meet in an L2
-  const int rb_n = (a.T + 32 * kDxWaves - 1) / (32 * kDxWaves);
+  const int rb_n = (a.T + ROWS - 1) / ROWS;
   int rb, ch;
   const int full = rb_n / 8 * 8 * a.n_chunks;
   if (b < full) {
@@ -327,42 +347,42 @@ __device__ __forceinline__ void dx_bf16(const RArgs& a, int b, char* smem) {
       g2::load_lds16(wp[j] + (size_t)s * adv[j], lds0 + slot * STAGE + (wave * LOADS + j) * 1024);
   };
   if (s0 < s1) issue(s0, 0);
-  // the wave's rows: parts hi and mid of every expert, in registers
-  const int t0 = (rb * kDxWaves + wave) * 32;
-  bf16x8_t hi[NK], mid[NK];
+  // the wave's rows: all parts of its experts, in registers
+  const int t0 = rb * ROWS + rg * 32;
+  bf16x8_t part[3][NKW];
   {
     const bool there = t0 < a.T;
-    const bf16_t* p = a.parts + (size_t)(t0 / 32) * 3 * a.eblocks * 512 + lane * 8;
+    const bf16_t* p = a.parts + ((size_t)(t0 / 32) * 3 * a.eblocks + kh * NKW) * 512 + lane * 8;
 #pragma unroll
-    for (int k = 0; k < NK; ++k) {
-      uint4 u = make_uint4(0, 0, 0, 0), v = u;
-      if (there) {
-        u = ld16(p + k * 512);
-        v = ld16(p + (size_t)(a.eblocks + k) * 512);
+    for (int k = 0; k < NKW; ++k)
+#pragma unroll
+      for (int q = 0; q < 3; ++q) {
+        uint4 u = make_uint4(0, 0, 0, 0);
+        if (there) u = ld16(p + ((size_t)q * a.eblocks + k) * 512);
+        part[q][k] = __builtin_bit_cast(bf16x8_t, u);
       }
-      hi[k] = __builtin_bit_cast(bf16x8_t, u);
-      mid[k] = __builtin_bit_cast(bf16x8_t, v);
-    }
   }
-  // the rows this lane stores: 8 lanes per row, four rows; chunk c of a
-  // staged row (128 bytes) sits at c ^ (row & 7), so this lane's chunk of row
-  // 8 i + lane / 8 is LDS position 64 i + lane for the column chunk below
+  // the rows this lane stores: 8 lanes per row, 4 / KS rows from row 32 / KS
+  // kh of the row group; chunk c of a staged row (128 bytes) sits at c ^ (row
+  // & 7), so this lane's chunk of row 8 i + lane / 8 is LDS position 64 i +
+  // lane for the column chunk below
   const int col = ((lane % 8) ^ (lane / 8)) * 8;
-  bf16_t* out[4];
+  bf16_t* out[4 / KS];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int t = t0 + 8 * i + lane / 8;
+  for (int i = 0; i < 4 / KS; ++i) {
+    const int t = t0 + 32 / KS * kh + 8 * i + lane / 8;
     out[i] = t < a.T ? reinterpret_cast<bf16_t*>(a.d_x.p[a.own_lo + t / a.T_src]) + (size_t)(t % a.T_src) * a.d + col
                      : nullptr;
   }
-  char* stg = smem + 2 * STAGE + wave * 4096;
-  const unsigned stg_lds = lds0 + 2 * STAGE + wave * 4096;
+  char* stg = smem + 2 * STAGE + rg * 4096;                      // the row group's tile
+  const int stg_own = 4096 / KS * kh;                            // the rows that this wave stores
+  const unsigned stg_lds = lds0 + 2 * STAGE + rg * 4096 + stg_own;
   auto store = [&](int s) {  // the staged tile of column step s
-    uint4 u[4];
+    uint4 u[4 / KS];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) u[i] = *reinterpret_cast<const uint4*>(stg + i * 1024 + lane * 16);
+    for (int i = 0; i < 4 / KS; ++i) u[i] = *reinterpret_cast<const uint4*>(stg + stg_own + i * 1024 + lane * 16);
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < 4 / KS; ++i)
       if (out[i]) {
         if constexpr (STREAM)
           __builtin_nontemporal_store(__builtin_bit_cast(i32x4_t, u[i]), reinterpret_cast<i32x4_t*>(out[i] + (size_t)s * 64));
@@ -384,47 +404,68 @@ __device__ __forceinline__ void dx_bf16(const RArgs& a, int b, char* smem) {
       // has read into registers by now
       g2::wave_lds_fence();
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < 4 / KS; ++i)
         g2::load_lds16(out[i] ? (const void*)(out[i] + (size_t)s * 64) : (const void*)g2::g_zero, stg_lds + i * 1024);
     }
-    const char* W = smem + slot * STAGE;
+    const char* W = smem + slot * STAGE + kh * NKW * 16 * 128;
     f32x16_t acc[2];
 #pragma unroll
     for (int j = 0; j < 2; ++j)
 #pragma unroll
       for (int r = 0; r < 16; ++r) acc[j][r] = 0.0f;
-    // fragments are read kAhead k16 steps before their use
+    // fragments are read kAhead k16 steps before their use; acc[0] holds
+    // columns 32 kh.., acc[1] the other 32
     constexpr int kAhead = 2;
     bf16x8_t f[kAhead + 1][2];
 #pragma unroll
     for (int k = 0; k < kAhead; ++k)
 #pragma unroll
-      for (int j = 0; j < 2; ++j) f[k][j] = frag64(W, 32 * j, k);
+      for (int j = 0; j < 2; ++j) f[k][j] = frag64(W, 32 * (j ^ kh), k);
     __builtin_amdgcn_sched_group_barrier(0x100, 4 * kAhead, 0);
 #pragma unroll
-    for (int k = 0; k < NK; ++k) {
-      if (k + kAhead < NK) {
+    for (int k = 0; k < NKW; ++k) {
+      if (k + kAhead < NKW) {
 #pragma unroll
-        for (int j = 0; j < 2; ++j) f[(k + kAhead) % (kAhead + 1)][j] = frag64(W, 32 * j, k + kAhead);
+        for (int j = 0; j < 2; ++j) f[(k + kAhead) % (kAhead + 1)][j] = frag64(W, 32 * (j ^ kh), k + kAhead);
       }
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
-        acc[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f[k % (kAhead + 1)][j], mid[k], acc[j], 0, 0, 0);
+      for (int q = 2; q >= 0; --q)
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
-        acc[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f[k % (kAhead + 1)][j], hi[k], acc[j], 0, 0, 0);
-      if (k + kAhead < NK) __builtin_amdgcn_sched_group_barrier(0x100, 4, 0);
-      __builtin_amdgcn_sched_group_barrier(0x008, 4, 0);
+        for (int j = 0; j < 2; ++j)
+          acc[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f[k % (kAhead + 1)][j], part[q][k], acc[j], 0, 0, 0);
+      if (k + kAhead < NKW) __builtin_amdgcn_sched_group_barrier(0x100, 4, 0);
+      __builtin_amdgcn_sched_group_barrier(0x008, 6, 0);
     }
-    // lane holds row lane % 32, columns 32 j + 8 g + 4 (lane / 32) + 0..3
-    if (a.add) g2::wait_vmcnt_lgkm0<0>();
-    asm volatile("" ::: "memory");
-    const int r = lane & 31;
+    if constexpr (KS == 2) {
+      // This step's W is read by all behind the first barrier, so its buffer
+      // takes the exchange: a wave gives acc[1] to the one with the other
+      // experts of its rows and adds what that one gives.  Behind the second
+      // barrier the pair's base rows are in place too.
+      barrier();
+      f32x4_t* ex = reinterpret_cast<f32x4_t*>(smem + slot * STAGE);
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
+      for (int g = 0; g < 4; ++g)
+        ex[(wave * 4 + g) * 64 + lane] = f32x4_t{acc[1][4 * g], acc[1][4 * g + 1], acc[1][4 * g + 2], acc[1][4 * g + 3]};
+      if (a.add) complete<true>();
+      else complete<false>();
+      barrier();
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
-        const int c = 32 * j + 8 * g + 4 * (lane >> 5);
+        const f32x4_t o = ex[((wave ^ 1) * 4 + g) * 64 + lane];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[0][4 * g + i] += o[i];
+      }
+    } else {
+      if (a.add) g2::wait_vmcnt_lgkm0<0>();
+      asm volatile("" ::: "memory");
+    }
+    // lane holds row lane % 32, columns 32 (j ^ kh) + 8 g + 4 (lane / 32) + 0..3
+    const int r = lane & 31;
+#pragma unroll
+    for (int j = 0; j < 2 / KS; ++j)
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const int c = 32 * (j ^ kh) + 8 * g + 4 * (lane >> 5);
         uint2* p = reinterpret_cast<uint2*>(stg + r * 128 + ((c >> 3) ^ (r & 7)) * 16 + (c & 7) * 2);
         float v[4] = {acc[j][4 * g], acc[j][4 * g + 1], acc[j][4 * g + 2], acc[j][4 * g + 3]};
         if (a.add) {
@@ -434,8 +475,10 @@ __device__ __forceinline__ void dx_bf16(const RArgs& a, int b, char* smem) {
         }
         *p = g2::pack4_bf16(v[0], v[1], v[2], v[3]);
       }
-    g2::wave_lds_fence();
+    if constexpr (KS == 2) complete<false>();
+    else g2::wave_lds_fence();
   }
+  if (KS == 2) barrier();   // the other wave's half of the staged rows
   if (s0 < s1) store(s1 - 1);
 }
 
@@ -802,8 +845,9 @@ Plan make_plan(int prec, int64_t T, int d, int E) {
 
 // Workgroups of dx: for every CU as often as they fit, as far as there are
 // column steps.
+template <int NK>
 int64_t plan_dx(RArgs& a, int per_cu) {
-  const int64_t rb = ((int64_t)a.T + 32 * kDxWaves - 1) / (32 * kDxWaves);
+  const int64_t rb = ((int64_t)a.T + dx_rows<NK>() - 1) / dx_rows<NK>();
   int64_t n = (256 * per_cu + rb - 1) / rb;
   if (n > a.d / 64) n = a.d / 64;
   a.n_chunks = (int)n;
@@ -820,7 +864,7 @@ bool stream_dx(const RArgs& a) { return (int64_t)a.T * a.d * 2 > (int64_t)32 << 
 
 template <int NK>
 void launch_dx(RArgs& a, hipStream_t stream) {
-  const dim3 grid((unsigned)plan_dx(a, NK <= 4 ? 4 : NK <= 16 ? 2 : 1));
+  const dim3 grid((unsigned)plan_dx<NK>(a, NK <= 4 ? 4 : NK <= 16 ? 2 : 1));
   if (stream_dx(a)) hipLaunchKernelGGL((router_dx_bf16_kernel<NK, true>), grid, dim3(kThreads), 0, stream, a);
   else hipLaunchKernelGGL((router_dx_bf16_kernel<NK, false>), grid, dim3(kThreads), 0, stream, a);
 }
@@ -833,7 +877,7 @@ void launch_dw(const RArgs& a, hipStream_t stream) {
 template <int NK, int EW>
 void launch_both(RArgs& a, hipStream_t stream) {
   const unsigned dw = dw_workgroups<EW>(a);
-  const dim3 grid(dw + (unsigned)plan_dx(a, 2));
+  const dim3 grid(dw + (unsigned)plan_dx<NK>(a, 2));
   if (stream_dx(a)) hipLaunchKernelGGL((router_both_bf16_kernel<NK, EW, true>), grid, dim3(kThreads), 0, stream, a, (int)dw);
   else hipLaunchKernelGGL((router_both_bf16_kernel<NK, EW, false>), grid, dim3(kThreads), 0, stream, a, (int)dw);
 }

@@ -454,9 +454,8 @@ size_t mok_router_bwd_ws_bytes(const mok_config* cfg, int32_t own_n);
  *   dw_router = d_logits^T x            ([E, d] fp32, or NULL)
  *   d_bias    = sum_t d_logits          ([E] fp32, or NULL)
  * overwritten, or with accumulate != 0 added to what the buffers hold (after
- * mok_layer_bwd; d_x is then rounded once more, from the fp32 sum).  Sums in
- * fp32 at least, in a fixed order; a bf16 d_x carries 2^-17 of its terms
- * beside its rounding.  No output may overlap an input.  src_x is needed for dw_router, w_router
+ * mok_layer_bwd; d_x is then rounded once more, from the fp32 sum).  Every
+ * bit of d_logits counts; sums in fp32 at least, in a fixed order.  No output may overlap an input.  src_x is needed for dw_router, w_router
  * for d_x; fp32 for MOK_F32, else bf16, 16-byte aligned like the outputs;
  * d at most 2^26.  Without own rows dw_router and d_bias become zero (or
  * stay, with accumulate).  A NaN or infinity in d_logits (for bf16 layers
