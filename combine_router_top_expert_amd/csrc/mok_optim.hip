@@ -297,17 +297,31 @@ __device__ __forceinline__ int encode8(const float (&x)[8], const uint32_t (&rnd
   return s;
 }
 
-// The square root of v, rounded to nearest but for rare last bits: the
-// hardware's reciprocal root (1 ulp) and one step of Newton's for the root,
-// whose residual v - r r is exact.  A v below 2^-126 gives v 2^63: above zero
-// too, and hidden by an eps of kEps or more; with a smaller one the library's
-// root is taken (6 us more on 43 million elements of 8-bit moments).
-constexpr float kEps = 1e-15f;
+// The square root of v, rounded to nearest but for rare last bits, where v is
+// zero or at least kRootMin: the hardware's reciprocal root (1 ulp) and one
+// step of Newton's for the root, whose residual v - r r is exact there (a
+// multiple of 2^-46 of r's power of two squared, which fp32 still holds).
+// Below, the residual and from 2^-126 on the reciprocal root go wrong, so a
+// wave with such a v takes the library's root (all waves: 6 us more on 43
+// million elements of 8-bit moments).
+constexpr float kRootMin = 0x1p-102f;
 __device__ __forceinline__ float root(float v) {
-  const float h = __builtin_amdgcn_rsqf(__builtin_fmaxf(v, 0x1p-126f));
+  const float h = __builtin_amdgcn_rsqf(__builtin_fmaxf(v, kRootMin));
   const float r = v * h;
   const float e = __builtin_fmaf(-r, r, v);
   return v < __builtin_inff() ? __builtin_fmaf(e, 0.5f * h, r) : v;
+}
+__device__ __forceinline__ void roots8(const float (&v)[8], float (&r)[8]) {
+  uint32_t least = ~0u;   // of the bits less one: zero comes last
+#pragma unroll
+  for (int j = 0; j < 8; ++j) least = min(least, __float_as_uint(v[j]) - 1);
+  if (__any(least < __float_as_uint(kRootMin) - 1)) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) r[j] = sqrtf(v[j]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) r[j] = root(v[j]);
+  }
 }
 
 // The moments are formed as the formula says, each product and sum rounded by
@@ -358,13 +372,7 @@ __device__ __forceinline__ void adam_step(const Desc& d, const AdamArgs& a, int6
     m[j] = a.b1 * m[j] + a.c1 * gj;
     v[j] = a.b2 * v[j] + a.c2 * (gj * gj);
   }
-  if (a.eps >= kEps) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) r[j] = root(v[j]);
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) r[j] = sqrtf(v[j]);
-  }
+  roots8(v, r);
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     const float u = m[j] * __builtin_amdgcn_rcpf(__builtin_fmaf(r[j], inv_sbc2, a.eps));

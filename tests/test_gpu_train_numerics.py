@@ -11,7 +11,7 @@ import pytest
 import torch
 
 import combine_router_top_expert_amd as mok
-from test_gpu_train import DEV, U, _gen, _log, _within
+from test_gpu_train import DEV, U, _codes32, _e4m3, _gen, _log, _scales, _within, _words
 
 pytestmark = pytest.mark.gpu
 
@@ -73,3 +73,71 @@ def test_router_bwd_dx_repeats_itself(E):
                 ref = zd @ wd
                 _within(dx, ref, 2.0 ** -8 * ref.abs() + (3 * E + 2) * U * (zd.abs() @ wd.abs()), (T, d))
             assert torch.equal(dx, first), (T, d)
+
+
+# ------------------------------------------------------------------ AdamW
+def _tiny_grads(n, seed):
+    """Gradients whose second moments lie on both sides of 2^-102 and of
+    2^-126, blocks of 32 of one size and blocks of all."""
+    g = _gen(seed)
+    size = 10.0 ** (torch.rand(n // 32, 1, generator=g).double() * 10 - 22)
+    size = torch.where(torch.rand(n // 32, 1, generator=g) < 0.3,
+                       10.0 ** (torch.rand(n // 32, 32, generator=g).double() * 10 - 22), size)
+    return (torch.randn(n // 32, 32, generator=g).double() * size).float().view(-1)
+
+
+def test_adamw_8bit_roots_of_tiny_second_moments():
+    """Codes and scales of both moments, bit for bit against the formula with
+    every operation rounded to fp32 by itself, for |g| down to 1e-22 and an
+    eps that hides nothing of what is stored; gradients, then none (the roots
+    decay by sqrt(beta2) and no faster)."""
+    _log("adamw tiny 8 bits")
+    n, seed = 32 * 500, 3
+    grads = _tiny_grads(n, 5)
+    z8 = lambda k: torch.zeros(k, dtype=torch.uint8, device=DEV)  # noqa: E731
+    p, g = torch.zeros(n, device=DEV), grads.to(DEV)
+    mc, vc, ms, vs = z8(n), z8(n), z8(n // 32), z8(n // 32)
+    params = mok.make_params([mok.make_param(p=p, g=g, m=mc, v=vc, m_scale=ms, v_scale=vs)])
+    f = lambda v: torch.tensor(v, dtype=torch.float32)  # noqa: E731
+    b1, b2, c1, c2 = f(0.9), f(0.999), f(1 - 0.9), f(1 - 0.999)
+    m, r = torch.zeros(n), torch.zeros(n)
+    for step in range(1, 9):
+        if step == 4:
+            g.zero_()
+            grads = torch.zeros(n)
+        mok.mok_adamw(params, mok.make_adamw(1e-3, 0.9, 0.999, 1e-8, step=step, seed=seed))
+        torch.cuda.synchronize()
+        m, r = b1 * m + c1 * grads, torch.sqrt(b2 * (r * r) + c2 * (grads * grads))
+        w = torch.from_numpy(_words(n, 0, step, seed)[0])
+        for x, u, code, sc, name in ((m, w & 0xFFFF, mc, ms, "m"), (r, w >> 16, vc, vs, "v")):
+            want, exps = _codes32(x, u.double() / 65536, x is r)
+            assert torch.equal(sc.cpu(), exps), (step, name)
+            assert torch.equal(code.cpu() & 0x7F, want), (step, name)
+        m = _e4m3(mc).float() * _scales(ms, n).float()
+        r = _e4m3(vc).float() * _scales(vs, n).float()
+    assert float(r[r > 0].min()) < 2.0 ** -63
+
+
+@pytest.mark.parametrize("eps", [0.0, 1e-20, 1e-15, 1e-12])
+@pytest.mark.parametrize("bits", [32, 8])
+def test_adamw_update_of_tiny_second_moments(eps, bits):
+    """The first step's update for the same gradients: m and v are products
+    rounded to fp32 (v by up to half of fp32's smallest subnormal), root,
+    correction, sum, reciprocal and the last two products add a few U: 16 U
+    of the update and the root's share of v's own rounding."""
+    _log("adamw tiny update", eps, bits)
+    n = 32 * 500
+    grads = _tiny_grads(n, 6)
+    p, g = torch.zeros(n, device=DEV), grads.to(DEV)
+    z = lambda k, dt: torch.zeros(k, dtype=dt, device=DEV)  # noqa: E731
+    dt, sc = (torch.uint8, n // 32) if bits == 8 else (torch.float32, None)
+    params = mok.make_params([mok.make_param(p=p, g=g, m=z(n, dt), v=z(n, dt),
+                                             m_scale=sc and z(sc, dt), v_scale=sc and z(sc, dt))])
+    mok.mok_adamw(params, mok.make_adamw(1.0, 0.9, 0.999, eps, step=1))
+    torch.cuda.synchronize()
+    f = lambda v: torch.tensor(v, dtype=torch.float32)  # noqa: E731
+    m, v = (f(1 - 0.9) * grads).double(), (f(1 - 0.999) * (grads * grads)).double()   # as they are rounded
+    keep = v > 0
+    assert float(v[keep].min()) < 2.0 ** -126 and int((v[keep] > 2.0 ** -102).sum()) > n // 10
+    want = -m / (1 - 0.9) / (v.sqrt() / math.sqrt(1 - 0.999) + eps)
+    _within(p.cpu()[keep], want[keep], 16 * U * want[keep].abs(), "p")
