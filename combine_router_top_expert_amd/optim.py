@@ -7,6 +7,7 @@ the norm's launches (with ``max_norm``) and the update's.
 """
 from __future__ import annotations
 
+import contextlib
 from typing import Optional, Sequence, Union
 
 import torch
@@ -25,6 +26,12 @@ class AdamW:
     whose norm is not finite is left out.  capturable: the step number (and the
     learning rate, see set_lr) live on the device, so a step captured in a
     graph advances at every replay; the number counts left-out steps too.
+
+    Steps may run on several streams: a step, set_lr, bind and the two
+    state_dict calls (these on the current stream) come after whatever the
+    optimizer did before on another stream, and after a call other than a step
+    the next step also waits for the current stream.  Replays of captured
+    steps are ordered by the caller.
     """
 
     def __init__(self, params: Sequence[torch.Tensor], lr: float = 1e-3, betas=(0.9, 0.999),
@@ -68,13 +75,46 @@ class AdamW:
                                dev_scale=self.norm[1:] if max_norm is not None else None,
                                dev_lr=self.dev_lr, dev_step=self.dev_step)
         self._grads = self._ws = None
+        # The stream of the last call, and an event behind a step on another
+        # stream than the current one (a handle its owner may take down; 4 us
+        # that steps on the current stream do not pay).
+        self._last = self._event = None
         self._behind = True      # the current stream holds work that a step has to see
+        if dev.type == "cuda":
+            with torch.cuda.device(dev):
+                self._last = torch.cuda.current_stream()
+
+    def _after_last(self, s):
+        """Work on `s` from here on comes after the calls before.  Not in a
+        capture, which waits for nothing outside it."""
+        if s != self._last:
+            if self._event is not None:
+                s.wait_event(self._event)
+            else:
+                s.wait_stream(self._last)
+
+    @contextlib.contextmanager
+    def _on_current(self):
+        """Work of a call other than a step, on the current stream."""
+        self._behind = True
+        if self.device.type != "cuda":
+            yield
+            return
+        with torch.cuda.device(self.device):
+            cur = torch.cuda.current_stream()
+            eager = not torch.cuda.is_current_stream_capturing()
+            if eager:
+                self._after_last(cur)
+            yield
+            if eager:
+                self._last, self._event = cur, None
 
     def state_dict(self) -> dict:
         """Moments, fp32 copies and step number (the tensors themselves)."""
-        return {"step": int(self.dev_step.item()) if self.dev_step is not None else self.step_count,
-                "m": self.m, "v": self.v, "m_scale": self.m_scale, "v_scale": self.v_scale,
-                "master": self.master}
+        with self._on_current():
+            step = int(self.dev_step.item()) if self.dev_step is not None else self.step_count
+        return {"step": step, "m": self.m, "v": self.v, "m_scale": self.m_scale,
+                "v_scale": self.v_scale, "master": self.master}
 
     def load_state_dict(self, state: dict):
         """Copies a state_dict of an optimizer over tensors of the same sizes
@@ -85,20 +125,20 @@ class AdamW:
                     (a is None) != (b is None) or (a is not None and (a.numel() != b.numel() or a.dtype != b.dtype))
                     for a, b in zip(mine, theirs)):
                 raise ValueError(f"state of other tensors: {name}")
-        for name in ("m", "v", "m_scale", "v_scale", "master"):
-            for a, b in zip(getattr(self, name), state[name]):
-                if a is not None:
-                    a.copy_(b.view(a.shape))
-        self.step_count = int(state["step"])
-        if self.dev_step is not None:
-            self.dev_step.fill_(self.step_count)
-        self._behind = True
+        with self._on_current():
+            for name in ("m", "v", "m_scale", "v_scale", "master"):
+                for a, b in zip(getattr(self, name), state[name]):
+                    if a is not None:
+                        a.copy_(b.view(a.shape))
+            self.step_count = int(state["step"])
+            if self.dev_step is not None:
+                self.dev_step.fill_(self.step_count)
 
     def set_lr(self, lr: float):
         self.args.lr = lr
         if self.dev_lr is not None:
-            self.dev_lr.fill_(lr)
-            self._behind = True
+            with self._on_current():
+                self.dev_lr.fill_(lr)
 
     def bind(self, grads: Sequence[torch.Tensor]):
         """Descriptors for these gradient tensors (kept: step() without
@@ -117,9 +157,9 @@ class AdamW:
                                                  self.m_scale, self.v_scale, self.weight_decay)])
         self._grads = grads
         if self.max_norm is not None and self._ws is None:   # (its size follows from the parameters')
-            self._ws = torch.empty(mok_grad_norm_ws_bytes(self._desc), dtype=torch.uint8,
-                                   device=self.device)
-            self._behind = True
+            with self._on_current():
+                self._ws = torch.empty(mok_grad_norm_ws_bytes(self._desc), dtype=torch.uint8,
+                                       device=self.device)
 
     def step(self, grads: Optional[Sequence[torch.Tensor]] = None, grad_scale: float = 1.0,
              stream=None):
@@ -135,12 +175,16 @@ class AdamW:
             raise RuntimeError("step() before any gradients were bound")
         if self.device.type != "cuda":
             raise ValueError(f"a step needs parameters on a GPU, not on {self.device}")
-        if self.dev_step is None and torch.cuda.is_current_stream_capturing():
-            raise RuntimeError("a captured step needs AdamW(capturable=True): its number would stand still")
         with torch.cuda.device(self.device):
             cur = torch.cuda.current_stream()
             s = cur if stream is None else stream
-            if self._behind and s != cur:
+            side = s != cur
+            capturing = torch.cuda.is_current_stream_capturing()
+            if self.dev_step is None and capturing:
+                raise RuntimeError("a captured step needs AdamW(capturable=True): its number would stand still")
+            if not capturing:
+                self._after_last(s)
+            if side and (self._behind or capturing):
                 s.wait_stream(cur)
             self._behind = False
             if self.max_norm is not None:
@@ -152,3 +196,9 @@ class AdamW:
                 with torch.cuda.stream(s):
                     self.dev_step.add_(1)
             mok_adamw(self._desc, self.args, s)
+            if capturing:
+                if side:             # a capture's branches come together again
+                    cur.wait_stream(s)
+            else:
+                self._last = s
+                self._event = s.record_event() if side else None

@@ -1,0 +1,140 @@
+"""Order of the training calls over streams: AdamW used from several streams,
+each behind work that keeps it busy, gives the bytes of the same calls on one
+stream."""
+import pytest
+import torch
+
+from combine_router_top_expert_amd.optim import AdamW
+from test_gpu_train import DEV, _gen, _log
+
+pytestmark = pytest.mark.gpu
+
+SIZES = (70000, 333, 4096)
+
+
+def _busy(stream, n=20):
+    """Some milliseconds of work on the stream."""
+    with torch.cuda.stream(stream):
+        t = torch.ones(1 << 26, device=DEV)
+        for _ in range(n):
+            t.mul_(1.0)
+
+
+def _make(**kw):
+    gen = _gen(8)
+    ps = [torch.randn(n, generator=gen).to(DEV, dt) for n, dt in zip(SIZES, (torch.float32, torch.bfloat16, torch.float32))]
+    return ps, AdamW(ps, lr=1e-2, state_bits=[32, 32, 8], max_norm=0.5, seed=4, **kw)
+
+
+def _grads(k):
+    gen = _gen(100)
+    return [[torch.randn(n, generator=gen).to(DEV) for n in SIZES] for _ in range(k)]
+
+
+def _state(ps, opt):
+    torch.cuda.synchronize()
+    return [t.clone().view(torch.uint8) for t in (*ps, *opt.m, *opt.v, opt.norm, *(w for w in opt.master if w is not None))]
+
+
+def _same(a, b):
+    for i, (x, y) in enumerate(zip(a, b)):
+        assert torch.equal(x, y), i
+
+
+@pytest.mark.parametrize("capturable", [False, True])
+def test_adamw_steps_on_several_streams(capturable):
+    _log("adamw streams", capturable)
+    gs = _grads(4)
+    ps, opt = _make(capturable=capturable)
+    for g in gs:
+        opt.step(g)
+    want = _state(ps, opt)
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    ps, opt = _make(capturable=capturable)
+    torch.cuda.synchronize()
+    _busy(torch.cuda.current_stream())
+    opt.step(gs[0])                      # behind the busy stream,
+    opt.step(gs[1], stream=s1)           # after it though s1 is idle,
+    _busy(s1)
+    opt.step(gs[2], stream=s2)           # after s1's,
+    _busy(s2)
+    opt.step(gs[3])                      # and after s2's
+    _same(_state(ps, opt), want)
+
+
+def test_adamw_set_lr_after_a_step_on_a_busy_stream():
+    _log("adamw set_lr stream")
+    gs = _grads(3)
+    rates = (1e-2, 1e-3, 1e-1)
+
+    def run(stream):
+        ps, opt = _make(capturable=True)
+        torch.cuda.synchronize()
+        for g, lr in zip(gs, rates):
+            opt.set_lr(lr)
+            if stream is not None:
+                _busy(stream)
+            opt.step(g, stream=stream)
+        return _state(ps, opt)
+    _same(run(torch.cuda.Stream()), run(None))
+
+
+def test_adamw_state_after_a_step_on_a_busy_stream():
+    """state_dict and load_state_dict right behind a step on another stream,
+    and a step on it right behind them."""
+    _log("adamw state stream")
+    gs = _grads(4)
+
+    def run(stream):
+        ps, opt = _make(capturable=True)
+        other = _make(capturable=True)[1]
+        other.step(gs[3])
+        torch.cuda.synchronize()
+        out = []
+        for g in gs[:2]:
+            if stream is not None:
+                _busy(stream)
+            opt.step(g, stream=stream)
+            d = opt.state_dict()
+            out.append([t.clone().view(torch.uint8) for n in ("m", "v") for t in d[n]] +
+                       [torch.tensor([d["step"]], dtype=torch.uint8)])
+        if stream is not None:
+            _busy(stream)
+        opt.step(gs[2], stream=stream)
+        opt.load_state_dict(other.state_dict())
+        _busy(torch.cuda.current_stream())
+        opt.step(gs[3], stream=stream)
+        return sum(out, []) + _state(ps, opt)
+    _same(run(torch.cuda.Stream()), run(None))
+
+
+def test_adamw_captured_step_on_a_second_stream():
+    """A step on another stream of a capture, with set_lr around it, joins the
+    capture again and replays as eager steps do."""
+    _log("adamw capture stream")
+    gs = _grads(4)
+    eager_ps, eager = _make(capturable=True)
+    ps, opt = _make(capturable=True)
+    slot = [t.clone() for t in gs[0]]
+    opt.bind(slot)
+    opt.step()
+    eager.step(gs[0])
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        opt.set_lr(1e-3)
+        opt.step(stream=side)
+        opt.set_lr(1e-1)
+        opt.step(stream=side)
+    for i in range(1, 4):
+        for s, g in zip(slot, gs[i]):
+            s.copy_(g)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        for lr in (1e-3, 1e-1):
+            eager.set_lr(lr)
+            eager.step(gs[i])
+        _same(_state(ps, opt), _state(eager_ps, eager))
+    del graph
