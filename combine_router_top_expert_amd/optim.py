@@ -80,9 +80,11 @@ class AdamW:
         # that steps on the current stream do not pay).
         self._last = self._event = None
         self._behind = True      # the current stream holds work that a step has to see
+        self._seen, self._grads_seen = set(), set()   # streams that _hold has named
         if dev.type == "cuda":
             with torch.cuda.device(dev):
                 self._last = torch.cuda.current_stream()
+                self._seen.add(self._last)
 
     def _after_last(self, s):
         """Work on `s` from here on comes after the calls before.  Not in a
@@ -92,6 +94,21 @@ class AdamW:
                 s.wait_event(self._event)
             else:
                 s.wait_stream(self._last)
+
+    def _hold(self, s):
+        """Memory of what a step on `s` works on is not given to others before
+        it is done, though every owner lets it go."""
+        if s not in self._seen:
+            self._seen.add(s)
+            for ts in (self.params, self.m, self.v, self.m_scale, self.v_scale, self.master,
+                       [self.norm, self.dev_step, self.dev_lr, self._ws]):
+                for t in ts:
+                    if t is not None:
+                        t.record_stream(s)
+        if s not in self._grads_seen:
+            self._grads_seen.add(s)
+            for g in self._grads:
+                g.record_stream(s)
 
     @contextlib.contextmanager
     def _on_current(self):
@@ -156,10 +173,12 @@ class AdamW:
             for p, g, m, v, w, ms, vs, wd in zip(self.params, grads, self.m, self.v, self.master,
                                                  self.m_scale, self.v_scale, self.weight_decay)])
         self._grads = grads
+        self._grads_seen.clear()
         if self.max_norm is not None and self._ws is None:   # (its size follows from the parameters')
             with self._on_current():
                 self._ws = torch.empty(mok_grad_norm_ws_bytes(self._desc), dtype=torch.uint8,
                                        device=self.device)
+                self._seen.clear()
 
     def step(self, grads: Optional[Sequence[torch.Tensor]] = None, grad_scale: float = 1.0,
              stream=None):
@@ -184,6 +203,8 @@ class AdamW:
                 raise RuntimeError("a captured step needs AdamW(capturable=True): its number would stand still")
             if not capturing:
                 self._after_last(s)
+                if side or s not in self._seen:
+                    self._hold(s)
             if side and (self._behind or capturing):
                 s.wait_stream(cur)
             self._behind = False

@@ -138,3 +138,53 @@ def test_adamw_captured_step_on_a_second_stream():
             eager.step(gs[i])
         _same(_state(ps, opt), _state(eager_ps, eager))
     del graph
+
+
+def _churn(sizes):
+    """New tensors of these sizes on the current stream, all NaN, so memory
+    that was given back too early is written over."""
+    return [torch.full((n,), float("nan"), device=DEV) for n in sizes for _ in range(4)]
+
+
+def test_adamw_keeps_gradients_of_a_busy_stream():
+    """Gradients that the caller lets go of right after a step on another
+    stream are read before their memory serves others."""
+    _log("adamw gradients stream")
+    gs = _grads(3)
+
+    def run(stream):
+        ps, opt = _make()
+        torch.cuda.synchronize()
+        for g in gs:
+            mine = [t.clone() for t in g]
+            if stream is not None:
+                stream.wait_stream(torch.cuda.current_stream())
+                _busy(stream)
+            opt.step(mine, stream=stream)
+            del mine
+            opt.bind(gs[0])
+            junk = _churn(SIZES)
+            del junk
+        return _state(ps, opt)
+    _same(run(torch.cuda.Stream()), run(None))
+
+
+def test_adamw_goes_before_its_step_is_done():
+    """The optimizer is deleted while its step waits on a busy stream: its
+    workspace and moments serve others only afterwards."""
+    _log("adamw deleted")
+    g = _grads(1)[0]
+
+    def run(stream):
+        ps, opt = _make()
+        opt.bind(g)
+        torch.cuda.synchronize()
+        if stream is not None:
+            _busy(stream)
+        opt.step(stream=stream)
+        del opt
+        junk = _churn((*SIZES, 64, 2, 128, 3, 11))
+        torch.cuda.synchronize()
+        assert all(bool(torch.isnan(t).all()) for t in junk)
+        return [p.clone().view(torch.uint8) for p in ps]
+    _same(run(torch.cuda.Stream()), run(None))
