@@ -206,13 +206,23 @@ class MoELayer:
             return torch.cuda.ExternalStream(stream, device=self.device)
         return stream
 
-    def _after_current(self, stream):
-        """Work on `stream` waits for the current one: a new buffer may be
+    def _after_current(self, stream, *new):
+        """Work on `stream` waits for the current one: the buffers `new` may be
         memory that the current stream still works on."""
         s = self._torch_stream(stream)
         with torch.cuda.device(self.device):
             if s is not None and s != torch.cuda.current_stream():
                 s.wait_stream(torch.cuda.current_stream())
+        self._hold(stream, *new)
+
+    def _hold(self, stream, *tensors):
+        """Memory of tensors that work on `stream` reads or writes is not given
+        to others before it is done, though every owner lets it go."""
+        s = self._torch_stream(stream)
+        if s is not None:
+            for t in tensors:
+                if t is not None:
+                    t.record_stream(s)
 
     def balance_loss(self, alpha, beta=0.0, group_offsets=None, token_mask=None, stream=None):
         """Balance loss and z-loss of the last forward's own tokens (fp32 [2]
@@ -240,7 +250,8 @@ class MoELayer:
             self._bal_bufs[rows] = (e(torch.int32, rows, self.E), e(torch.float32, rows, self.E),
                                     e(torch.int32, rows + 2), e(torch.float32, 2),
                                     e(torch.uint8, mok_balance_ws_bytes(self.cfg, T, self._bal)))
-            self._after_current(stream)
+            self._after_current(stream, *self._bal_bufs[rows])
+        self._hold(stream, group_offsets, token_mask)
         self.counts_all, self.prob, self.n_tok, self.loss, self.ws_bal = self._bal_bufs[rows]
         lo = self.own_lo * self.T_src
         mok_balance_fwd(self.cfg, T, self._bal, self.logits[lo:], self.topk_idx[lo * self.k:],
@@ -259,7 +270,8 @@ class MoELayer:
             self.d_logits = torch.empty(max(T, 1), self.E, dtype=torch.float32, device=self.device)
             self.ws_router = torch.empty(mok_router_bwd_ws_bytes(self.cfg, self.own_n),
                                          dtype=torch.uint8, device=self.device)
-            self._after_current(stream)
+            self._after_current(stream, self.d_logits, self.ws_router)
+        self._hold(stream, *self._bal_keep, d_loss)
         if self._bal.G > 0:      # rows outside every group are not written: they add nothing
             with torch.cuda.stream(self._torch_stream(stream)):
                 self.d_logits.zero_()

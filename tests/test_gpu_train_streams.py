@@ -5,7 +5,7 @@ import pytest
 import torch
 
 from combine_router_top_expert_amd.optim import AdamW
-from test_gpu_train import DEV, _gen, _log
+from test_gpu_train import DEV, _balance_layer, _gen, _log
 
 pytestmark = pytest.mark.gpu
 
@@ -187,4 +187,36 @@ def test_adamw_goes_before_its_step_is_done():
         torch.cuda.synchronize()
         assert all(bool(torch.isnan(t).all()) for t in junk)
         return [p.clone().view(torch.uint8) for p in ps]
+    _same(run(torch.cuda.Stream()), run(None))
+
+
+@pytest.mark.parametrize("raw", [False, True])
+def test_balance_keeps_offsets_masks_and_weights_of_a_busy_stream(raw):
+    """Tensors that the caller lets go of right after a call on another stream
+    (a torch stream or its handle) are read before their memory serves others."""
+    _log("balance stream", raw)
+
+    def run(stream):
+        L, dout, _ = _balance_layer()
+        L.forward()
+        L.backward(dout)
+        mask = torch.ones(300, dtype=torch.uint8)
+        mask[40:70] = 0
+        torch.cuda.synchronize()
+        arg = stream.cuda_stream if raw and stream is not None else stream
+        for off in ([0, 100, 300], [0, 50, 290]):
+            o, m, w = (t.to(DEV) for t in (torch.tensor(off, dtype=torch.int32), mask, torch.tensor([2.0, 0.5])))
+            if stream is not None:
+                stream.wait_stream(torch.cuda.current_stream())
+                _busy(stream)
+            loss = L.balance_loss(0.5, 0.01, o, m, stream=arg)
+            L.balance_backward(w, stream=arg)
+            L._bal_keep = None
+            del o, m, w
+            junk = [torch.full((n,), 7, dtype=dt, device=DEV) for n, dt in
+                    ((3, torch.int32), (300, torch.uint8), (2, torch.float32)) for _ in range(8)]
+            del junk
+        torch.cuda.synchronize()
+        L.check_status()
+        return [t.clone() for t in (loss, L.counts_all, L.d_x[0], L.dw_router)]
     _same(run(torch.cuda.Stream()), run(None))
