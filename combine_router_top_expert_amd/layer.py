@@ -224,6 +224,14 @@ class MoELayer:
                 if t is not None:
                     t.record_stream(s)
 
+    def _check(self, t, dt, n=None):
+        """Refuses a tensor that a kernel could not read as n (any) values dt."""
+        dev = self.logits.device
+        if t is not None and (t.dtype != dt or not t.is_contiguous() or t.device != dev
+                              or (n is not None and t.numel() != n) or t.numel() < 1):
+            raise ValueError(f"contiguous {dt} tensor{'' if n is None else f' of {n}'} on {dev} expected, "
+                             f"got {t.dtype} {tuple(t.shape)} on {t.device}")
+
     def balance_loss(self, alpha, beta=0.0, group_offsets=None, token_mask=None, stream=None):
         """Balance loss and z-loss of the last forward's own tokens (fp32 [2]
         on the device; needs keep_logits).  group_offsets: int32 [G+1] over
@@ -236,10 +244,8 @@ class MoELayer:
             raise RuntimeError("balance_loss needs MoELayer(keep_logits=True)")
         T, dev = self.own_n * self.T_src, self.logits.device
         G = 0 if group_offsets is None else group_offsets.numel() - 1
-        for t, dt, n in ((group_offsets, torch.int32, None), (token_mask, torch.uint8, T)):
-            if t is not None and (t.dtype != dt or not t.is_contiguous() or t.device != dev
-                                  or (n is not None and t.numel() != n) or t.numel() < 1):
-                raise ValueError(f"contiguous {dt} tensor on {dev} expected, got {t.dtype} {tuple(t.shape)}")
+        self._check(group_offsets, torch.int32)
+        self._check(token_mask, torch.uint8, T)
         if group_offsets is not None and G < 1:
             raise ValueError("group_offsets needs at least two entries")
         self._bal = make_balance(alpha, beta, G, group_offsets, token_mask)
@@ -265,6 +271,7 @@ class MoELayer:
         after backward()."""
         if getattr(self, "_bal", None) is None or not self.with_bwd:
             raise RuntimeError("balance_backward needs balance_loss and backward before it")
+        self._check(d_loss, torch.float32, 2)
         T, lo = self.own_n * self.T_src, self.own_lo * self.T_src
         if getattr(self, "d_logits", None) is None:
             self.d_logits = torch.empty(max(T, 1), self.E, dtype=torch.float32, device=self.device)
