@@ -139,14 +139,15 @@ class MoELayer:
         forms what the layer keeps beside them again -- the backward's
         transposed copies, the MX codes -- in the same buffers.  A layer in
         fp32, or in bf16 without transposed weights, keeps nothing."""
-        w = (self.w_gate, self.w_up, self.w_down)
-        if self.prec == "mxfp8":
-            for t, (codes, scales) in zip(w, self.wq):
-                mok_mx_quantize(t.numel() // t.shape[-1], t.shape[-1], t, codes, scales, stream)
-            if self.with_bwd:
-                mok_prepare_bwd(self.cfg, *w, *self.wt, stream)
-        elif self.prec == "bf16" and self.with_bwd and self.transposed_weights:
-            mok_prepare_bwd(self.cfg, *w, self.wt[0], None, self.wt[1], None, stream)
+        with torch.cuda.device(self.device):
+            w = (self.w_gate, self.w_up, self.w_down)
+            if self.prec == "mxfp8":
+                for t, (codes, scales) in zip(w, self.wq):
+                    mok_mx_quantize(t.numel() // t.shape[-1], t.shape[-1], t, codes, scales, stream)
+                if self.with_bwd:
+                    mok_prepare_bwd(self.cfg, *w, *self.wt, stream)
+            elif self.prec == "bf16" and self.with_bwd and self.transposed_weights:
+                mok_prepare_bwd(self.cfg, *w, self.wt[0], None, self.wt[1], None, stream)
 
     def _quantize_weights(self):
         """MX-quantise the expert weights (off the timed path)."""
@@ -210,9 +211,8 @@ class MoELayer:
         """Work on `stream` waits for the current one: the buffers `new` may be
         memory that the current stream still works on."""
         s = self._torch_stream(stream)
-        with torch.cuda.device(self.device):
-            if s is not None and s != torch.cuda.current_stream():
-                s.wait_stream(torch.cuda.current_stream())
+        if s is not None and s != torch.cuda.current_stream():
+            s.wait_stream(torch.cuda.current_stream())
         self._hold(stream, *new)
 
     def _hold(self, stream, *tensors):
@@ -250,19 +250,20 @@ class MoELayer:
             raise ValueError("group_offsets needs at least two entries")
         self._bal = make_balance(alpha, beta, G, group_offsets, token_mask)
         self._bal_keep = (group_offsets, token_mask)
-        rows = max(G, 1)
-        if rows not in self._bal_bufs:
-            e = lambda t, *n: torch.empty(*n, dtype=t, device=dev)  # noqa: E731
-            self._bal_bufs[rows] = (e(torch.int32, rows, self.E), e(torch.float32, rows, self.E),
-                                    e(torch.int32, rows + 2), e(torch.float32, 2),
-                                    e(torch.uint8, mok_balance_ws_bytes(self.cfg, T, self._bal)))
-            self._after_current(stream, *self._bal_bufs[rows])
-        self._hold(stream, group_offsets, token_mask)
-        self.counts_all, self.prob, self.n_tok, self.loss, self.ws_bal = self._bal_bufs[rows]
-        lo = self.own_lo * self.T_src
-        mok_balance_fwd(self.cfg, T, self._bal, self.logits[lo:], self.topk_idx[lo * self.k:],
-                        self.counts_all, self.prob, self.n_tok, self.loss, self.ws_bal,
-                        self.status, stream)
+        with torch.cuda.device(self.device):
+            rows = max(G, 1)
+            if rows not in self._bal_bufs:
+                e = lambda t, *n: torch.empty(*n, dtype=t, device=dev)  # noqa: E731
+                self._bal_bufs[rows] = (e(torch.int32, rows, self.E), e(torch.float32, rows, self.E),
+                                        e(torch.int32, rows + 2), e(torch.float32, 2),
+                                        e(torch.uint8, mok_balance_ws_bytes(self.cfg, T, self._bal)))
+                self._after_current(stream, *self._bal_bufs[rows])
+            self._hold(stream, group_offsets, token_mask)
+            self.counts_all, self.prob, self.n_tok, self.loss, self.ws_bal = self._bal_bufs[rows]
+            lo = self.own_lo * self.T_src
+            mok_balance_fwd(self.cfg, T, self._bal, self.logits[lo:], self.topk_idx[lo * self.k:],
+                            self.counts_all, self.prob, self.n_tok, self.loss, self.ws_bal,
+                            self.status, stream)
         return self.loss
 
     def balance_backward(self, d_loss=None, stream=None):
@@ -272,20 +273,21 @@ class MoELayer:
         if getattr(self, "_bal", None) is None or not self.with_bwd:
             raise RuntimeError("balance_backward needs balance_loss and backward before it")
         self._check(d_loss, torch.float32, 2)
-        T, lo = self.own_n * self.T_src, self.own_lo * self.T_src
-        if getattr(self, "d_logits", None) is None:
-            self.d_logits = torch.empty(max(T, 1), self.E, dtype=torch.float32, device=self.device)
-            self.ws_router = torch.empty(mok_router_bwd_ws_bytes(self.cfg, self.own_n),
-                                         dtype=torch.uint8, device=self.device)
-            self._after_current(stream, self.d_logits, self.ws_router)
-        self._hold(stream, *self._bal_keep, d_loss)
-        if self._bal.G > 0:      # rows outside every group are not written: they add nothing
-            with torch.cuda.stream(self._torch_stream(stream)):
-                self.d_logits.zero_()
-        mok_balance_bwd(self.cfg, T, self._bal, self.logits[lo:], self.counts_all, self.n_tok,
-                        d_loss, self.d_logits, self.status, stream)
-        mok_router_bwd(self.cfg, self.own_lo, self.own_n, self.d_logits, self.xs, self.w_router,
-                       self.d_x, self.dw_router, None, True, self.ws_router, stream)
+        with torch.cuda.device(self.device):
+            T, lo = self.own_n * self.T_src, self.own_lo * self.T_src
+            if getattr(self, "d_logits", None) is None:
+                self.d_logits = torch.empty(max(T, 1), self.E, dtype=torch.float32, device=self.device)
+                self.ws_router = torch.empty(mok_router_bwd_ws_bytes(self.cfg, self.own_n),
+                                             dtype=torch.uint8, device=self.device)
+                self._after_current(stream, self.d_logits, self.ws_router)
+            self._hold(stream, *self._bal_keep, d_loss)
+            if self._bal.G > 0:      # rows outside every group are not written: they add nothing
+                with torch.cuda.stream(self._torch_stream(stream)):
+                    self.d_logits.zero_()
+            mok_balance_bwd(self.cfg, T, self._bal, self.logits[lo:], self.counts_all, self.n_tok,
+                            d_loss, self.d_logits, self.status, stream)
+            mok_router_bwd(self.cfg, self.own_lo, self.own_n, self.d_logits, self.xs, self.w_router,
+                           self.d_x, self.dw_router, None, True, self.ws_router, stream)
 
     def check_status(self):
         st = int(self.status.item())

@@ -49,3 +49,22 @@ def test_balance_backward_refuses_wrong_loss_weights(calls):
     L.balance_backward(torch.ones(2))
     L.balance_backward()
     assert [c[0] for c in calls] == ["mok_balance_bwd", "mok_router_bwd"] * 2
+
+
+def test_calls_run_on_the_layers_device(calls, monkeypatch):
+    """The kernels are launched with the layer's device current, whichever was."""
+    for name in ("mok_mx_quantize", "mok_prepare_bwd"):
+        monkeypatch.setattr(layer_mod, name, lambda *a, _n=name: calls.append((_n, a, _Device.current)))
+    L = _layer()
+    L.xs, L.w_router, L.bias = [torch.zeros(4, 64)], torch.zeros(4, 64), None
+    off = torch.tensor([0, 4], dtype=torch.int32)
+    L.balance_loss(0.1, 0.1, off)
+    L.balance_backward()
+    for prec in ("bf16", "mxfp8"):
+        L = MoELayer(1, 4, 64, 4, 1, 64, 4, prec, 4, 0, 1, device="cpu", two_streams=False)
+        L.w_gate = L.w_up = L.w_down = torch.zeros(4, 64, 64)
+        L.wt, L.wq = [None] * 4, [(None, None)] * 3
+        L.update_weights()
+    assert {c[0] for c in calls} == {"mok_balance_fwd", "mok_balance_bwd", "mok_router_bwd", "mok_mx_quantize",
+                                     "mok_prepare_bwd"}
+    assert all(c[2] == L.device for c in calls)
