@@ -79,6 +79,7 @@ class MoELayer:
                                 self.logits)
         self.with_bwd = with_bwd
         self._bal_bufs = {}
+        self.d_bias = None       # the balance losses' gradient of a router bias
         # bf16 backward: the weights also transposed (mok_prepare_bwd), so dh
         # and dx read them k-contiguous (bit-identical either way)
         self.transposed_weights = transposed_weights
@@ -269,7 +270,9 @@ class MoELayer:
     def balance_backward(self, d_loss=None, stream=None):
         """Adds the gradient of d_loss[0] * balance loss + d_loss[1] * z-loss
         (d_loss fp32 [2] on the device, None = ones) to d_x and dw_router,
-        after backward()."""
+        after backward().  With a router bias, d_bias [E] becomes these
+        losses' gradient of it; backward() forms none, so the share that comes
+        through the gates is not in it."""
         if getattr(self, "_bal", None) is None or not self.with_bwd:
             raise RuntimeError("balance_backward needs balance_loss and backward before it")
         self._check(d_loss, torch.float32, 2)
@@ -280,14 +283,20 @@ class MoELayer:
                 self.ws_router = torch.empty(mok_router_bwd_ws_bytes(self.cfg, self.own_n),
                                              dtype=torch.uint8, device=self.device)
                 self._after_current(stream, self.d_logits, self.ws_router)
+            if self.bias is not None and self.d_bias is None:
+                self.d_bias = torch.empty(self.E, dtype=torch.float32, device=self.device)
+                self._after_current(stream, self.d_bias)
+            d_bias = self.d_bias if self.bias is not None else None
             self._hold(stream, *self._bal_keep, d_loss)
-            if self._bal.G > 0:      # rows outside every group are not written: they add nothing
-                with torch.cuda.stream(self._torch_stream(stream)):
+            with torch.cuda.stream(self._torch_stream(stream)):
+                if self._bal.G > 0:  # rows outside every group are not written: they add nothing
                     self.d_logits.zero_()
+                if d_bias is not None:
+                    d_bias.zero_()
             mok_balance_bwd(self.cfg, T, self._bal, self.logits[lo:], self.counts_all, self.n_tok,
                             d_loss, self.d_logits, self.status, stream)
             mok_router_bwd(self.cfg, self.own_lo, self.own_n, self.d_logits, self.xs, self.w_router,
-                           self.d_x, self.dw_router, None, True, self.ws_router, stream)
+                           self.d_x, self.dw_router, d_bias, True, self.ws_router, stream)
 
     def check_status(self):
         st = int(self.status.item())
