@@ -172,7 +172,7 @@ bool own_sources_set(const void* const* p, int own_lo, int own_n, int T_src) {
 
 extern "C" {
 
-const char* mok_version(void) { return "mok 0.1 gfx950"; }
+const char* mok_version(void) { return MOK_VERSION; }
 
 size_t mok_workspace_bytes(const mok_config* cfg) {
   if (!valid_cfg(cfg)) return 0;

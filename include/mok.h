@@ -182,7 +182,10 @@ typedef struct mok_expert_weights {
   const uint8_t* st_gu;
 } mok_expert_weights;
 
-/* State the forward pass leaves for the backward pass (all caller-owned). */
+/* State the forward pass leaves for the backward pass (all caller-owned).
+ * Zero it before setting fields: a NULL field is one that is not kept, and a
+ * caller compiled before `logits` was there has to be compiled again
+ * (MOK_VERSION). */
 typedef struct mok_fwd_state {
   int32_t* topk_idx;   /* [S*T_src*k]: in for non-own sources, out for own sources */
   float* topk_gate;    /* [S*T_src*k] fp32, same split */
@@ -617,7 +620,13 @@ mok_status mok_mx_quantize(int64_t rows, int64_t K, const void* src, uint8_t* co
 mok_status mok_mx_quantize_f32(int64_t rows, int64_t K, const float* src, uint8_t* codes,
                                uint8_t* scales, void* stream);
 
-/* Library version string (static storage). */
+/* Version of this header's structures and entry points.  A caller compiled
+ * against another one passes structures of other sizes, which the library
+ * reads past their end: compare with mok_version() before the first call.
+ * 0.2: mok_fwd_state ends with `logits`. */
+#define MOK_VERSION "mok 0.2 gfx950"
+
+/* MOK_VERSION of the header that the library was built with (static storage). */
 const char* mok_version(void);
 
 #ifdef __cplusplus

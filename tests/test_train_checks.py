@@ -1,8 +1,12 @@
 """What the Python side of the training calls refuses and hands on, on the
 CPU: nothing here reaches a kernel."""
+import os
+import re
+
 import pytest
 import torch
 
+import combine_router_top_expert_amd as mok
 import combine_router_top_expert_amd.layer as layer_mod
 from combine_router_top_expert_amd.layer import MoELayer
 
@@ -68,3 +72,12 @@ def test_calls_run_on_the_layers_device(calls, monkeypatch):
     assert {c[0] for c in calls} == {"mok_balance_fwd", "mok_balance_bwd", "mok_router_bwd", "mok_mx_quantize",
                                      "mok_prepare_bwd"}
     assert all(c[2] == L.device for c in calls)
+
+
+def test_version_tells_the_structures_apart():
+    """mok_fwd_state grew by the logits after "mok 0.1": a caller can tell."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    header = open(os.path.join(root, "include", "mok.h")).read()
+    assert mok.mok_version() == re.search(r'#define MOK_VERSION "([^"]+)"', header).group(1)
+    assert mok.mok_version() != "mok 0.1 gfx950"
+    assert [f for f, _ in mok.mok_fwd_state._fields_][-1] == "logits"
