@@ -58,7 +58,7 @@ class AdamW:
                 raise ValueError(f"state_bits 8 or 32 expected, got {bits}")
         self.device, self.max_norm = dev, max_norm
         self.step_count = 0
-        self.master = [p.float() if master and p.dtype == torch.bfloat16 else None
+        self.master = [p.detach().float() if master and p.dtype == torch.bfloat16 else None
                        for p in self.params]
         z = lambda n, t: torch.zeros(n, dtype=t, device=dev)  # noqa: E731
         self.m, self.v, self.m_scale, self.v_scale = [], [], [], []
@@ -146,7 +146,7 @@ class AdamW:
             for name in ("m", "v", "m_scale", "v_scale", "master"):
                 for a, b in zip(getattr(self, name), state[name]):
                     if a is not None:
-                        a.copy_(b.view(a.shape))
+                        a.copy_(b.detach().view(a.shape))
             self.step_count = int(state["step"])
             if self.dev_step is not None:
                 self.dev_step.fill_(self.step_count)

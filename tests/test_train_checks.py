@@ -9,6 +9,7 @@ import torch
 import combine_router_top_expert_amd as mok
 import combine_router_top_expert_amd.layer as layer_mod
 from combine_router_top_expert_amd.layer import MoELayer
+from combine_router_top_expert_amd.optim import AdamW
 
 
 def _layer(**kw):
@@ -81,3 +82,16 @@ def test_version_tells_the_structures_apart():
     assert mok.mok_version() == re.search(r'#define MOK_VERSION "([^"]+)"', header).group(1)
     assert mok.mok_version() != "mok 0.1 gfx950"
     assert [f for f, _ in mok.mok_fwd_state._fields_][-1] == "logits"
+
+
+def test_optimizer_keeps_no_autograd_graph():
+    """fp32 copies of leaves that autograd knows are values: a graph kept with
+    them would hold the leaves' accumulators for as long as the optimizer."""
+    ps = [torch.nn.Parameter(torch.randn(40).bfloat16()), torch.nn.Parameter(torch.randn(7))]
+    opt = AdamW(ps)
+    state = opt.state_dict()
+    assert opt.master[0].grad_fn is None and not opt.master[0].requires_grad
+    state["master"] = [ps[0].float(), None]        # another optimizer's, with its graph
+    opt.load_state_dict(state)
+    assert opt.master[0].grad_fn is None and not opt.master[0].requires_grad
+    assert torch.equal(opt.master[0], ps[0].detach().float())
