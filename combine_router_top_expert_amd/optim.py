@@ -21,7 +21,8 @@ class AdamW:
 
     weight_decay, state_bits: one value, or one per tensor.  state_bits 32 or 8
     (moments of a tensor in fp32, or in 8 bits).  master: keep fp32 copies of
-    bf16 parameters; without them a bf16 parameter is rounded to nearest, or at
+    bf16 parameters, taken here: a step writes the parameters from them, so
+    call take_params after writing parameters by other means; without them a bf16 parameter is rounded to nearest, or at
     random with random_params.  max_norm: clip the global gradient norm; a step
     whose norm is not finite is left out.  capturable: the step number (and the
     learning rate, see set_lr) live on the device, so a step captured in a
@@ -150,6 +151,14 @@ class AdamW:
             self.step_count = int(state["step"])
             if self.dev_step is not None:
                 self.dev_step.fill_(self.step_count)
+
+    def take_params(self):
+        """Takes the parameters as they are now (weights loaded into them, say)
+        into the fp32 copies, whose next step would write the former ones."""
+        with self._on_current():
+            for p, w in zip(self.params, self.master):
+                if w is not None:
+                    w.copy_(p.detach())
 
     def set_lr(self, lr: float):
         self.args.lr = lr

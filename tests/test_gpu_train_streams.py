@@ -220,3 +220,36 @@ def test_balance_keeps_offsets_masks_and_weights_of_a_busy_stream(raw):
         L.check_status()
         return [t.clone() for t in (loss, L.counts_all, L.d_x[0], L.dw_router)]
     _same(run(torch.cuda.Stream()), run(None))
+
+
+def test_adamw_steps_from_loaded_parameters():
+    """Parameters loaded before a step on a busy stream, and taken over: the
+    step of an optimizer made of them."""
+    _log("adamw take_params")
+    gs = _grads(2)
+    gen = _gen(55)
+    new = [torch.randn(n, generator=gen).to(DEV) for n in SIZES]
+
+    def run(stream):
+        ps, opt = _make()
+        torch.cuda.synchronize()
+        if stream is not None:
+            _busy(stream)
+        opt.step(gs[0], stream=stream)
+        torch.cuda.synchronize()
+        for p, w in zip(ps, new):
+            p.copy_(w)
+        opt.take_params()
+        _busy(torch.cuda.current_stream())
+        opt.step(gs[1], stream=stream)
+        return ps, opt
+    ps, opt = run(torch.cuda.Stream())
+    fresh = [t.to(p.dtype) for t, p in zip(new, ps)]
+    other = AdamW(fresh, lr=1e-2, state_bits=[32, 32, 8], max_norm=0.5, seed=4)
+    first = _make()[1]
+    first.step(gs[0])
+    state = first.state_dict()
+    state["master"] = other.master
+    other.load_state_dict(state)
+    other.step(gs[1])
+    _same(_state(ps, opt), _state(fresh, other))

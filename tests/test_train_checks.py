@@ -95,3 +95,16 @@ def test_optimizer_keeps_no_autograd_graph():
     opt.load_state_dict(state)
     assert opt.master[0].grad_fn is None and not opt.master[0].requires_grad
     assert torch.equal(opt.master[0], ps[0].detach().float())
+
+
+def test_optimizer_takes_loaded_parameters_over():
+    """Weights written into bf16 parameters after construction reach the fp32
+    copies, which the next step starts from, in place."""
+    ps = [torch.randn(3, 40).bfloat16(), torch.randn(7), torch.randn(0).bfloat16()]
+    opt = AdamW(ps)
+    at = opt.master[0].data_ptr()
+    ps[0].copy_(torch.randn(3, 40))
+    opt.take_params()
+    assert torch.equal(opt.master[0], ps[0].float()) and opt.master[0].data_ptr() == at
+    assert opt.master[1] is None
+    AdamW(ps, master=False).take_params()          # nothing is kept
