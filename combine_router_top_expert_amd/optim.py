@@ -128,15 +128,17 @@ class AdamW:
                 self._last, self._event = cur, None
 
     def state_dict(self) -> dict:
-        """Moments, fp32 copies and step number (the tensors themselves)."""
+        """Moments and fp32 copies (the tensors themselves), step number and
+        the seed of the random rounding."""
         with self._on_current():
             step = int(self.dev_step.item()) if self.dev_step is not None else self.step_count
-        return {"step": step, "m": self.m, "v": self.v, "m_scale": self.m_scale,
+        return {"step": step, "seed": self.args.seed, "m": self.m, "v": self.v, "m_scale": self.m_scale,
                 "v_scale": self.v_scale, "master": self.master}
 
     def load_state_dict(self, state: dict):
         """Copies a state_dict of an optimizer over tensors of the same sizes
-        and kinds into this one's buffers (their addresses stay)."""
+        and kinds into this one's buffers (their addresses stay) and goes on
+        with its step number and seed (steps captured before keep theirs)."""
         for name in ("m", "v", "m_scale", "v_scale", "master"):
             mine, theirs = getattr(self, name), state[name]
             if len(mine) != len(theirs) or any(
@@ -149,6 +151,7 @@ class AdamW:
                     if a is not None:
                         a.copy_(b.detach().view(a.shape))
             self.step_count = int(state["step"])
+            self.args.seed = int(state.get("seed", self.args.seed))   # (older states hold none)
             if self.dev_step is not None:
                 self.dev_step.fill_(self.step_count)
 

@@ -108,3 +108,16 @@ def test_optimizer_takes_loaded_parameters_over():
     assert torch.equal(opt.master[0], ps[0].float()) and opt.master[0].data_ptr() == at
     assert opt.master[1] is None
     AdamW(ps, master=False).take_params()          # nothing is kept
+
+
+def test_optimizer_state_holds_the_seed():
+    """A resumed run rounds as the run would have gone on."""
+    p = [torch.randn(40).bfloat16()]
+    a, b = AdamW(p, state_bits=8, seed=(1 << 63) + 5), AdamW([p[0].clone()], state_bits=8)
+    b.load_state_dict(a.state_dict())
+    assert b.args.seed == (1 << 63) + 5
+    old = a.state_dict()
+    del old["seed"]
+    c = AdamW([p[0].clone()], state_bits=8, seed=9)
+    c.load_state_dict(old)
+    assert c.args.seed == 9
