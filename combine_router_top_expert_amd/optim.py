@@ -57,6 +57,10 @@ class AdamW:
                 raise TypeError(f"float32 or bfloat16 expected, got {p.dtype}")
             if bits not in (8, 32):
                 raise ValueError(f"state_bits 8 or 32 expected, got {bits}")
+        ends = sorted((p.data_ptr(), p.data_ptr() + p.numel() * p.element_size())
+                      for p in self.params if p.numel())
+        if any(a[1] > b[0] for a, b in zip(ends, ends[1:])):
+            raise ValueError("parameters overlap (the same one twice?): a step writes each by itself")
         self.device, self.max_norm = dev, max_norm
         self.step_count = 0
         self.master = [p.detach().float() if master and p.dtype == torch.bfloat16 else None

@@ -121,3 +121,12 @@ def test_optimizer_state_holds_the_seed():
     c = AdamW([p[0].clone()], state_bits=8, seed=9)
     c.load_state_dict(old)
     assert c.args.seed == 9
+
+
+def test_optimizer_refuses_parameters_that_overlap():
+    """Two updates of one element would race."""
+    w = torch.zeros(100)
+    for bad in ([w, torch.zeros(3), w], [w[:60], w[50:]], [w.bfloat16().view(-1), w, w[99:]]):
+        with pytest.raises(ValueError, match="overlap"):
+            AdamW(bad)
+    AdamW([w[50:], w[:50], w[50:50], torch.zeros(0), torch.zeros(0)])     # neighbours and empty ones
