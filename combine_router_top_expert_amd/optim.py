@@ -8,6 +8,8 @@ the norm's launches (with ``max_norm``) and the update's.
 from __future__ import annotations
 
 import contextlib
+import ctypes
+import math
 from typing import Optional, Sequence, Union
 
 import torch
@@ -201,9 +203,14 @@ class AdamW:
         """One step on `stream` (a torch stream; None: the device's current
         one).  grads: gradients to bind, or None for those bound before.
         Gradients are multiplied by grad_scale > 0 (the norm is taken
-        before)."""
-        if not grad_scale > 0.0:
-            raise ValueError(f"grad_scale above zero expected, got {grad_scale}")
+        before, and clipped to max_norm / grad_scale; both have to be fp32
+        values)."""
+        f32 = ctypes.c_float(grad_scale).value       # as the kernels take it
+        if not 0.0 < f32 < math.inf:
+            raise ValueError(f"grad_scale above zero, finite in fp32, expected, got {grad_scale}")
+        limit = 0.0 if self.max_norm is None else self.max_norm / grad_scale
+        if self.max_norm is not None and not ctypes.c_float(limit).value > 0.0:
+            raise ValueError(f"max_norm / grad_scale = {limit} is zero in fp32: nothing would be clipped")
         if grads is not None:
             self.bind(grads)
         if self._grads is None:
@@ -225,7 +232,7 @@ class AdamW:
                 s.wait_stream(cur)
             self._behind = False
             if self.max_norm is not None:
-                mok_grad_norm(self._desc, self.max_norm / grad_scale, self.norm, self._ws, s)
+                mok_grad_norm(self._desc, limit, self.norm, self._ws, s)
             self.step_count += 1
             self.args.step = self.step_count
             self.args.grad_scale = grad_scale

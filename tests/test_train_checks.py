@@ -130,3 +130,20 @@ def test_optimizer_refuses_parameters_that_overlap():
         with pytest.raises(ValueError, match="overlap"):
             AdamW(bad)
     AdamW([w[50:], w[:50], w[50:50], torch.zeros(0), torch.zeros(0)])     # neighbours and empty ones
+
+
+@pytest.mark.parametrize("max_norm, scale", [(None, float("inf")), (None, 1e39), (None, 1e-46), (1e-30, 1e20),
+                                             (1e-44, 64.0), (1e-50, 1.0)])
+def test_optimizer_refuses_scales_beyond_fp32(max_norm, scale):
+    """A scale that is infinite or zero to the kernels, or a limit that is:
+    a norm limit of zero would turn the clipping off."""
+    opt = AdamW([torch.zeros(8)], max_norm=max_norm)
+    with pytest.raises(ValueError, match="fp32"):
+        opt.step([torch.zeros(8)], grad_scale=scale)
+
+
+@pytest.mark.parametrize("max_norm, scale", [(None, 1e38), (1e-30, 1e10), (1.0, 1e-40), (float("inf"), 2.0)])
+def test_optimizer_takes_scales_within_fp32(max_norm, scale):
+    opt = AdamW([torch.zeros(8)], max_norm=max_norm)
+    with pytest.raises(ValueError, match="GPU"):      # the next thing that is looked at
+        opt.step([torch.zeros(8)], grad_scale=scale)
