@@ -1,5 +1,6 @@
 // C ABI of the library (declared in include/mok.h): argument validation,
 // workspace carving and launch sequencing.  No allocation, no host sync.
+#include <float.h>
 #include <string.h>
 
 #include <mutex>
@@ -1008,6 +1009,9 @@ mok_status mok_adamw(int32_t n_params, const mok_param* params, const mok_adamw_
   if (!(args->beta1 >= 0.0 && args->beta1 < 1.0) || !(args->beta2 >= 0.0 && args->beta2 < 1.0) ||
       !(args->eps >= 0.0) || !(args->lr >= 0.0))
     return MOK_EINVAL;
+  // in fp32: a finite rate, and an eps whose reciprocal is finite too (else an
+  // element without gradients yet, 0 / eps, would become NaN)
+  if (!((float)args->lr <= FLT_MAX) || (args->eps > 0.0 && (float)args->eps < FLT_MIN)) return MOK_EINVAL;
   if (!args->dev_step && args->step < 1) return MOK_EINVAL;
   if (!aligned(args->dev_scale, 4) || !aligned(args->dev_lr, 8) || !aligned(args->dev_step, 8))
     return MOK_EINVAL;

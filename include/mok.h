@@ -533,7 +533,9 @@ typedef struct mok_adamw_args {
  * for p, where a, b are the halves of mix(key + (i / 8 + 1) G), key =
  * mix(mix(seed + t) + step G), G = 0x9E3779B97F4A7C15; the same inputs give
  * the same bytes.  Non-finite gradients make the element's m, v and p
- * non-finite (E4M3 NaN; sqrt(v) saturates). */
+ * non-finite (E4M3 NaN; sqrt(v) saturates).  lr is finite in fp32, and eps 0
+ * or at least 2^-126; with eps 0 an element that has had no gradient yet
+ * becomes NaN, the formula's 0 / 0. */
 mok_status mok_adamw(int32_t n_params, const mok_param* params, const mok_adamw_args* args,
                      void* stream);
 

@@ -147,3 +147,14 @@ def test_optimizer_takes_scales_within_fp32(max_norm, scale):
     opt = AdamW([torch.zeros(8)], max_norm=max_norm)
     with pytest.raises(ValueError, match="GPU"):      # the next thing that is looked at
         opt.step([torch.zeros(8)], grad_scale=scale)
+
+
+@pytest.mark.parametrize("bad", [dict(eps=1e-39), dict(eps=1e-50), dict(lr=1e39), dict(lr=float("inf"))], ids=str)
+def test_adamw_refuses_constants_beyond_fp32(bad):
+    """An eps below 2^-126 has no finite reciprocal in fp32: elements without
+    gradients would become NaN."""
+    q = mok.mok_param(16, 16, None, 16, 16, None, None, 8, mok.MOK_F32, mok.MOK_F32, 32, 0.0)
+    with pytest.raises(mok.MokError, match="EINVAL"):
+        mok.mok_adamw(mok.make_params([q]), mok.make_adamw(**{**dict(lr=1e-3, eps=1e-8), **bad}), 0)
+    mok.mok_adamw(mok.make_params([]), mok.make_adamw(1e-3, eps=2.0 ** -126), 0)      # nothing to do
+    mok.mok_adamw(mok.make_params([]), mok.make_adamw(1e-3, eps=0.0), 0)
