@@ -221,16 +221,20 @@ class AdamW:
             cur = torch.cuda.current_stream()
             s = cur if stream is None else stream
             side = s != cur
-            capturing = torch.cuda.is_current_stream_capturing()
-            if self.dev_step is None and capturing:
+            joins = captured = torch.cuda.is_current_stream_capturing()
+            if side and not captured:
+                with torch.cuda.stream(s):
+                    captured = torch.cuda.is_current_stream_capturing()
+            if self.dev_step is None and captured:
                 raise RuntimeError("a captured step needs AdamW(capturable=True): its number would stand still")
-            if not capturing:
+            if not captured:
                 self._after_last(s)
                 if side or s not in self._seen:
                     self._hold(s)
-            if side and (self._behind or capturing):
+            if side and (joins or (self._behind and not captured)):
                 s.wait_stream(cur)
-            self._behind = False
+            if not captured:
+                self._behind = False
             if self.max_norm is not None:
                 mok_grad_norm(self._desc, limit, self.norm, self._ws, s)
             self.step_count += 1
@@ -240,9 +244,8 @@ class AdamW:
                 with torch.cuda.stream(s):
                     self.dev_step.add_(1)
             mok_adamw(self._desc, self.args, s)
-            if capturing:
-                if side:             # a capture's branches come together again
-                    cur.wait_stream(s)
-            else:
+            if joins and side:       # a capture's branches come together again
+                cur.wait_stream(s)
+            if not captured:
                 self._last = s
                 self._event = s.record_event() if side else None

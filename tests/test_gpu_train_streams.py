@@ -253,3 +253,35 @@ def test_adamw_steps_from_loaded_parameters():
     other.load_state_dict(state)
     other.step(gs[1])
     _same(_state(ps, opt), _state(fresh, other))
+
+
+def test_adamw_step_on_a_captured_stream_that_is_not_the_current_one():
+    """The capture of the step's own stream counts: refused with a host step
+    number, replayed like eager steps with one on the device."""
+    _log("adamw captured other")
+    gs = _grads(4)
+    frozen = _make()[1]
+    frozen.bind(gs[0])
+    eager_ps, eager = _make(capturable=True)
+    ps, opt = _make(capturable=True)
+    slot = [t.clone() for t in gs[0]]
+    opt.bind(slot)
+    opt.step()
+    eager.step(gs[0])
+    torch.cuda.synchronize()
+    main, cap = torch.cuda.current_stream(), torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=cap):
+        with torch.cuda.stream(main):
+            with pytest.raises(RuntimeError, match="capturable"):
+                frozen.step(stream=cap)
+            opt.step(stream=cap)
+    for i in range(1, 4):
+        for s, g in zip(slot, gs[i]):
+            s.copy_(g)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        eager.step(gs[i])
+        _same(_state(ps, opt), _state(eager_ps, eager))
+    del graph
