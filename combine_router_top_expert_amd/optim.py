@@ -220,6 +220,8 @@ class AdamW:
         with torch.cuda.device(self.device):
             cur = torch.cuda.current_stream()
             s = cur if stream is None else stream
+            if s.device != self.device:
+                raise ValueError(f"stream on {s.device}, parameters on {self.device}")
             side = s != cur
             joins = captured = torch.cuda.is_current_stream_capturing()
             if side and not captured:

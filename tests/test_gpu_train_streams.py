@@ -285,3 +285,13 @@ def test_adamw_step_on_a_captured_stream_that_is_not_the_current_one():
         eager.step(gs[i])
         _same(_state(ps, opt), _state(eager_ps, eager))
     del graph
+
+
+def test_adamw_refuses_a_stream_of_another_device():
+    """A stream that is no stream of the parameters' GPU cannot order the step."""
+    _, opt = _make()
+
+    class Other:
+        device = torch.device("cuda", 7)
+    with pytest.raises(ValueError, match="cuda:7"):
+        opt.step(_grads(1)[0], stream=Other())
