@@ -57,7 +57,7 @@ struct BalArgs {
   // workspace of the forward; slots = chunks + G
   float* part;           // [slots][E] column sums
   int32_t* cnt;          // [slots][E]
-  float* zz;             // [slots]
+  double* zz;            // [slots]
   int32_t* nrow;         // [slots]
   int32_t* ticket;       // [0] workgroups of the finishing kernel that are done, [1] the offsets are good
   double* lossp;         // [G * ceil(E / kFinCols)]
@@ -298,7 +298,7 @@ __global__ __launch_bounds__(kBalThreads) void balance_fwd_kernel(BalArgs a) {
   constexpr int U = rows_at_once<NV>(), KJ = slots_per_lane<LPR, VEC>();
   __shared__ float s_sum[kBalWaves][kMaxE];
   __shared__ int s_cnt[kMaxE];
-  __shared__ float s_zz[kBalWaves];
+  __shared__ double s_zz[kBalWaves];
   __shared__ int s_n[kBalWaves];
   const int chunk = blockIdx.x;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -333,10 +333,11 @@ __global__ __launch_bounds__(kBalThreads) void balance_fwd_kernel(BalArgs a) {
     if (lo >= hi && !lone) continue;
     for (int e = tid; e < a.E; e += kBalThreads) s_cnt[e] = 0;
     __syncthreads();
+    // squares of lse would overflow in fp32 where their mean does not
     float acc[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i) acc[i] = 0.0f;
-    float zz = 0.0f;
+    double zz = 0.0;
     int n = 0;
     Rows<LPR, NV, VEC> now, next;
     int id[U][KJ], id_next[U][KJ];
@@ -353,7 +354,7 @@ __global__ __launch_bounds__(kBalThreads) void balance_fwd_kernel(BalArgs a) {
       for (int u = 0; u < U; ++u) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) acc[i] += now.v[u][i];
-        zz = __builtin_fmaf(lse[u], lse[u], zz);   // every lane of the row: lane 0's is used
+        zz = __builtin_fma((double)lse[u], (double)lse[u], zz);   // every lane of the row: lane 0's is used
         n += live[u];
       }
 #pragma unroll
@@ -392,7 +393,7 @@ __global__ __launch_bounds__(kBalThreads) void balance_fwd_kernel(BalArgs a) {
     }
     __syncthreads();
     const int rows = s_n[0] + s_n[1] + s_n[2] + s_n[3];
-    const float zsum = (s_zz[0] + s_zz[1]) + (s_zz[2] + s_zz[3]);
+    const double zsum = (s_zz[0] + s_zz[1]) + (s_zz[2] + s_zz[3]);
     auto column = [&](int e) { return (s_sum[0][e] + s_sum[1][e]) + (s_sum[2][e] + s_sum[3][e]); };
     if (lone) {  // nothing is left to add up
       const double cp = block_sum<double, kBalThreads>(a.E, [&](int e) {
@@ -449,7 +450,7 @@ __global__ __launch_bounds__(kFinThreads) void balance_finish_kernel(BalArgs a) 
   int cn[4] = {0, 0, 0, 0}, n = 0;
   for (int i = threadIdx.x; i < slots; i += kFinThreads) {
     n += a.nrow[s0 + i];
-    zz += (double)a.zz[s0 + i];
+    zz += a.zz[s0 + i];
   }
   const int ec = e0 + 4 * c;
   if (a.E % 4 == 0) {
@@ -703,7 +704,7 @@ void launch_shape(const Shape& s, const BalArgs& a, hipStream_t st) {
 
 size_t balance_ws_bytes(int T, int E, int G) {
   const size_t slots = (size_t)G + chunk_count(T, E, G);
-  return 2 * align256(slots * E * 4) + 2 * align256(slots * 4) + align256((size_t)G * fin_blocks(E) * 8) +
+  return 2 * align256(slots * E * 4) + align256(slots * 8) + align256(slots * 4) + align256((size_t)G * fin_blocks(E) * 8) +
          align256((size_t)G * 8) + 256;
 }
 
@@ -729,7 +730,7 @@ mok_status launch_balance_fwd(int T, int E, int k, int G, const mok_balance& b, 
   };
   a.part = (float*)take(slots * E * 4);
   a.cnt = (int32_t*)take(slots * E * 4);
-  a.zz = (float*)take(slots * 4);
+  a.zz = (double*)take(slots * 8);
   a.nrow = (int32_t*)take(slots * 4);
   a.lossp = (double*)take((size_t)G * fin_blocks(E) * 8);
   a.zzp = (double*)take((size_t)G * 8);

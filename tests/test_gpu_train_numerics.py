@@ -141,3 +141,33 @@ def test_adamw_update_of_tiny_second_moments(eps, bits):
     assert float(v[keep].min()) < 2.0 ** -126 and int((v[keep] > 2.0 ** -102).sum()) > n // 10
     want = -m / (1 - 0.9) / (v.sqrt() / math.sqrt(1 - 0.999) + eps)
     _within(p.cpu()[keep], want[keep], 16 * U * want[keep].abs(), "p")
+
+
+# ------------------------------------------------------------------ balance
+def _balance_fwd(z, topk, k, beta, off=None):
+    T, E = z.shape
+    G = 1 if off is None else len(off) - 1
+    cfg = mok.make_config(1, T, 64, E, k, 64, 1, "f32", 0)
+    offd = None if off is None else torch.tensor(off, dtype=torch.int32, device=DEV)
+    bal = mok.make_balance(1.0, beta, 0 if off is None else G, offd)
+    i32 = lambda *s: torch.zeros(*s, dtype=torch.int32, device=DEV)  # noqa: E731
+    counts, n_tok, st = i32(G, E), i32(G + 2), i32(1)
+    prob, loss = torch.zeros(G, E, device=DEV), torch.zeros(2, device=DEV)
+    ws = torch.full((mok.mok_balance_ws_bytes(cfg, T, bal),), 0xFF, dtype=torch.uint8, device=DEV)
+    mok.mok_balance_fwd(cfg, T, bal, z, topk, counts, prob, n_tok, loss, ws, st)
+    torch.cuda.synchronize()
+    assert int(st.item()) == 0
+    return prob.cpu(), loss.cpu()
+
+
+@pytest.mark.parametrize("T, off", [(200, None), (5000, None), (5000, [0, 100, 4990])], ids=str)
+def test_balance_z_loss_of_large_logits(T, off):
+    """lse^2 = 1.6e37 in every row: the mean is an fp32 value though the sum
+    over a chunk is not.  lse is off by 2 U, its square by 4 U, and the loss
+    is rounded once."""
+    _log("balance large lse", T, off)
+    E = 8
+    z = torch.full((T, E), 4e18, device=DEV)
+    _, loss = _balance_fwd(z, torch.zeros(T, 1, dtype=torch.int32, device=DEV), 1, 1.0, off)
+    want = (z[0, 0].double().cpu() + math.log(E)) ** 2
+    _within(loss[1], want, 6 * U * want, "z-loss")
