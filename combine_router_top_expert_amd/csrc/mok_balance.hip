@@ -43,6 +43,7 @@ constexpr int kBalThreads = 256;
 constexpr int kBalWaves = kBalThreads / 64;
 constexpr int kBalWgs = 1024;   // chunks at most: four workgroups per CU
 constexpr int kMaxE = 512;
+constexpr int kFold = 16;       // steps of a lane's fp32 sums
 constexpr int kFinCols = 64;    // experts per workgroup of the finishing kernel
 constexpr int kFinThreads = 512;
 
@@ -299,6 +300,7 @@ __global__ __launch_bounds__(kBalThreads) void balance_fwd_kernel(BalArgs a) {
   __shared__ float s_sum[kBalWaves][kMaxE];
   __shared__ int s_cnt[kMaxE];
   __shared__ double s_zz[kBalWaves];
+  __shared__ double s_fold[NV][kBalThreads];
   __shared__ int s_n[kBalWaves];
   const int chunk = blockIdx.x;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -333,12 +335,15 @@ __global__ __launch_bounds__(kBalThreads) void balance_fwd_kernel(BalArgs a) {
     if (lo >= hi && !lone) continue;
     for (int e = tid; e < a.E; e += kBalThreads) s_cnt[e] = 0;
     __syncthreads();
+    // a lane adds kFold steps' probabilities in fp32, and those sums in 64
+    // bits, so that the error does not grow with the chunk (in LDS: as
+    // registers they cost 8 % of 131072 x 256, where no chunk is that long);
     // squares of lse would overflow in fp32 where their mean does not
     float acc[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i) acc[i] = 0.0f;
     double zz = 0.0;
-    int n = 0;
+    int n = 0, steps = 0;
     Rows<LPR, NV, VEC> now, next;
     int id[U][KJ], id_next[U][KJ];
     int r0 = lo + wave * RL::kRows * U;
@@ -367,6 +372,13 @@ __global__ __launch_bounds__(kBalThreads) void balance_fwd_kernel(BalArgs a) {
           bad = bad || (slot && !known);
         }
       if (!more) break;
+      if (++steps % kFold == 0) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+          s_fold[i][tid] = (steps > kFold ? s_fold[i][tid] : 0.0) + (double)acc[i];
+          acc[i] = 0.0f;
+        }
+      }
       r0 += step;
       now = next;
 #pragma unroll
@@ -377,6 +389,7 @@ __global__ __launch_bounds__(kBalThreads) void balance_fwd_kernel(BalArgs a) {
     // the wave's row groups, then the four waves
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
+      if (steps >= kFold) acc[i] = (float)(s_fold[i][tid] + (double)acc[i]);
 #pragma unroll
       for (int o = LPR; o < 64; o <<= 1) acc[i] += __shfl_xor(acc[i], o, 64);
       const int e = RL::expert(l, i);

@@ -160,6 +160,19 @@ def _balance_fwd(z, topk, k, beta, off=None):
     return prob.cpu(), loss.cpu()
 
 
+def test_balance_column_sums_of_many_rows():
+    """A million equal rows: every lane adds the same value again and again,
+    whose rounding then goes one way.  The mean is a single row's p but for
+    32 additions in fp32 (31 U), a rounding to fp32 before and after two sums
+    over waves (4 U) and the mean's own (U): 36 U."""
+    T, E = 1 << 20, 512
+    _log("balance many rows", T, E)
+    row = torch.randn(1, E, generator=_gen(2)).to(DEV)
+    one, _ = _balance_fwd(row, torch.zeros(1, 1, dtype=torch.int32, device=DEV), 1, 0.0)
+    many, _ = _balance_fwd(row.expand(T, E).contiguous(), torch.zeros(T, 1, dtype=torch.int32, device=DEV), 1, 0.0)
+    _within(many, one.double(), 36 * U * one.double(), "prob")
+
+
 @pytest.mark.parametrize("T, off", [(200, None), (5000, None), (5000, [0, 100, 4990])], ids=str)
 def test_balance_z_loss_of_large_logits(T, off):
     """lse^2 = 1.6e37 in every row: the mean is an fp32 value though the sum
