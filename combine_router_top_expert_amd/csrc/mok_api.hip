@@ -882,6 +882,8 @@ bool valid_balance(const mok_config* cfg, int32_t T, const mok_balance* b) {
   // counts are int32, group rows of the outputs are indexed by int32; row
   // numbers stay clear of int32's end by a workgroup's step
   if (T > 1 << 30 || (int64_t)T * cfg->k > 0x7FFFFFFF || (int64_t)b->G * cfg->E > 0x7FFFFFFF) return false;
+  // the finishing launch has 512 threads a group, and a launch fewer than 2^32
+  if (b->G >= 1 << 23) return false;
   return true;
 }
 

@@ -396,8 +396,8 @@ mok_status mok_prepare_bwd(const mok_config* cfg, const void* w_gate, const void
                            uint8_t* st_gu, void* stream);
 
 /* Balance loss of the router and its gradient, for training.  The T tokens
- * (at most 2^30, T * k and G * E at most 2^31 - 1) come in G groups of consecutive rows (the sequences of a batch, or one
- * group); rows outside [group_offsets[0], group_offsets[G]) belong to no
+ * (at most 2^30, T * k and G * E at most 2^31 - 1) come in G < 2^23 groups of
+ * consecutive rows (the sequences of a batch, or one group); rows outside [group_offsets[0], group_offsets[G]) belong to no
  * group.  A row counts if its mask byte is nonzero and not all of its logits
  * are -inf.  With p = softmax(z) of a counted row, N_g the counted rows of
  * group g, c_ge its chosen slots that name expert e, G+ the groups with

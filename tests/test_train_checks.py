@@ -1,5 +1,6 @@
 """What the Python side of the training calls refuses and hands on, on the
 CPU: nothing here reaches a kernel."""
+import ctypes
 import os
 import re
 
@@ -158,3 +159,15 @@ def test_adamw_refuses_constants_beyond_fp32(bad):
         mok.mok_adamw(mok.make_params([q]), mok.make_adamw(**{**dict(lr=1e-3, eps=1e-8), **bad}), 0)
     mok.mok_adamw(mok.make_params([]), mok.make_adamw(1e-3, eps=2.0 ** -126), 0)      # nothing to do
     mok.mok_adamw(mok.make_params([]), mok.make_adamw(1e-3, eps=0.0), 0)
+
+
+def test_balance_refuses_more_groups_than_a_launch_holds():
+    """Refused before the first launch, not by the second one's failure."""
+    cfg = mok.make_config(1, 8, 64, 2, 1, 64, 1, "f32", 0)
+    for G, ok in (((1 << 23) - 1, True), (1 << 23, False), (1 << 29, False)):
+        bal = mok.mok_balance(0.1, 0.1, G, 16, None)
+        assert (mok.mok_balance_ws_bytes(cfg, 8, bal) > 0) == ok
+    at = 1 << 20
+    for call in (mok.lib().mok_balance_fwd, mok.lib().mok_balance_bwd):
+        bal = mok.mok_balance(0.1, 0.1, 1 << 23, at, None)
+        assert call(ctypes.byref(cfg), 8, ctypes.byref(bal), *[at] * (len(call.argtypes) - 5), None, None) == -1
