@@ -887,6 +887,12 @@ bool valid_balance(const mok_config* cfg, int32_t T, const mok_balance* b) {
   return true;
 }
 
+// The router's backward counts token rows in int32 and past the last one by
+// up to a block of them.
+bool router_rows_ok(const mok_config* cfg, int32_t own_n) {
+  return (int64_t)own_n * cfg->T_src <= 0x7FFFFFFF - 4096;
+}
+
 bool valid_type(int t) { return t == MOK_F32 || t == MOK_BF16; }
 int type_bytes(int t) { return t == MOK_F32 ? 4 : 2; }
 
@@ -950,7 +956,7 @@ mok_status mok_balance_bwd(const mok_config* cfg, int32_t T, const mok_balance* 
 }
 
 size_t mok_router_bwd_ws_bytes(const mok_config* cfg, int32_t own_n) {
-  if (!valid_cfg(cfg) || own_n < 0 || own_n > cfg->S) return 0;
+  if (!valid_cfg(cfg) || own_n < 0 || own_n > cfg->S || !router_rows_ok(cfg, own_n)) return 0;
   return router_bwd_ws_bytes(cfg->prec, (int64_t)own_n * cfg->T_src, cfg->d, cfg->E);
 }
 
@@ -959,6 +965,7 @@ mok_status mok_router_bwd(const mok_config* cfg, int32_t own_lo, int32_t own_n,
                           void* const* d_x, float* dw_router, float* d_bias, int32_t accumulate,
                           void* ws, void* stream) {
   if (!valid_cfg(cfg) || !own_range_ok(cfg, own_lo, own_n)) return MOK_EINVAL;
+  if (!router_rows_ok(cfg, own_n)) return MOK_EINVAL;
   if (cfg->d > 1 << 26) return MOK_EINVAL;   // byte offsets within 16 token rows fit 32 bits
   const int64_t T = (int64_t)own_n * cfg->T_src;
   if (T > 0 && (!d_logits || !aligned(d_logits, 4))) return MOK_EINVAL;

@@ -460,7 +460,7 @@ size_t mok_router_bwd_ws_bytes(const mok_config* cfg, int32_t own_n);
  * mok_layer_bwd; d_x is then rounded once more, from the fp32 sum).  Every
  * bit of d_logits counts; sums in fp32 at least, in a fixed order.  No output may overlap an input.  src_x is needed for dw_router, w_router
  * for d_x; fp32 for MOK_F32, else bf16, 16-byte aligned like the outputs;
- * d at most 2^26.  Without own rows dw_router and d_bias become zero (or
+ * d at most 2^26, own rows at most 2^31 - 4097.  Without own rows dw_router and d_bias become zero (or
  * stay, with accumulate).  A NaN or infinity in d_logits (for bf16 layers
  * also a value that bf16 rounds to infinity, from 3.39e38 on) makes its row
  * of d_x and its expert's dw_router and d_bias not finite. */

@@ -171,3 +171,17 @@ def test_balance_refuses_more_groups_than_a_launch_holds():
     for call in (mok.lib().mok_balance_fwd, mok.lib().mok_balance_bwd):
         bal = mok.mok_balance(0.1, 0.1, 1 << 23, at, None)
         assert call(ctypes.byref(cfg), 8, ctypes.byref(bal), *[at] * (len(call.argtypes) - 5), None, None) == -1
+
+
+def test_router_bwd_refuses_rows_at_the_end_of_int32():
+    """Row numbers run past the last row by up to a block: from 2^31 - 16 on
+    they would wrap."""
+    for prec in ("f32", "bf16"):
+        for T, ok in (((1 << 31) - 1, False), ((1 << 31) - 4096, False), ((1 << 31) - 4097, True)):
+            cfg = mok.make_config(1, T, 64, 1, 1, 64, 1, prec, 0)
+            assert (mok.mok_router_bwd_ws_bytes(cfg, 1) > 0) == ok
+            assert mok.mok_router_bwd_ws_bytes(cfg, 0) > 0
+            if not ok:
+                with pytest.raises(mok.MokError, match="EINVAL"):
+                    mok.mok_router_bwd(cfg, 0, 1, torch.zeros(4), None, None, None, None, torch.zeros(1), False,
+                                       torch.zeros(64), 0)
