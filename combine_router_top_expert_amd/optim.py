@@ -81,13 +81,13 @@ class AdamW:
         self.args = make_adamw(lr, betas[0], betas[1], eps, seed=seed, random_params=random_params,
                                dev_scale=self.norm[1:] if max_norm is not None else None,
                                dev_lr=self.dev_lr, dev_step=self.dev_step)
-        self._grads = self._ws = None
+        self._held = self._ws = None
         # The stream of the last call, and an event behind a step on another
         # stream than the current one (a handle its owner may take down; 4 us
         # that steps on the current stream do not pay).
         self._last = self._event = None
         self._behind = True      # the current stream holds work that a step has to see
-        self._seen, self._grads_seen = set(), set()   # streams that _hold has named
+        self._seen, self._held_seen = set(), set()   # streams that _hold has named
         if dev.type == "cuda":
             with torch.cuda.device(dev):
                 self._last = torch.cuda.current_stream()
@@ -107,14 +107,15 @@ class AdamW:
         it is done, though every owner lets it go."""
         if s not in self._seen:
             self._seen.add(s)
-            for ts in (self.params, self.m, self.v, self.m_scale, self.v_scale, self.master,
+            for ts in (self.m, self.v, self.m_scale, self.v_scale, self.master,
                        [self.norm, self.dev_step, self.dev_lr, self._ws]):
                 for t in ts:
                     if t is not None:
                         t.record_stream(s)
-        if s not in self._grads_seen:
-            self._grads_seen.add(s)
-            for g in self._grads:
+        if s not in self._held_seen:
+            self._held_seen.add(s)
+            for p, g in self._held:
+                p.record_stream(s)
                 g.record_stream(s)
 
     @contextlib.contextmanager
@@ -177,21 +178,23 @@ class AdamW:
 
     def bind(self, grads: Sequence[torch.Tensor]):
         """Descriptors for these gradient tensors (kept: step() without
-        arguments reads them again)."""
+        arguments reads them again).  They name the memory that parameters and
+        gradients have now, which is held: a tensor that is given other memory
+        afterwards (its .data) has to be bound again."""
         grads = list(grads)
         if len(grads) != len(self.params):
             raise ValueError("one gradient per parameter")
         for p, g in zip(self.params, grads):
             if g.device != self.device:
                 raise ValueError(f"gradient on {g.device}, parameters on {self.device}")
-        flat = lambda t: None if t is None else t.view(-1)  # noqa: E731
+        flat = lambda t: None if t is None else t.detach().view(-1)  # noqa: E731
+        held = [(flat(p), flat(g)) for p, g in zip(self.params, grads)]
         self._desc = make_params([
-            make_param(p=flat(p), g=flat(g), m=m, v=v, master=flat(w), m_scale=ms, v_scale=vs,
-                       weight_decay=wd)
-            for p, g, m, v, w, ms, vs, wd in zip(self.params, grads, self.m, self.v, self.master,
-                                                 self.m_scale, self.v_scale, self.weight_decay)])
-        self._grads = grads
-        self._grads_seen.clear()
+            make_param(p=p, g=g, m=m, v=v, master=flat(w), m_scale=ms, v_scale=vs, weight_decay=wd)
+            for (p, g), m, v, w, ms, vs, wd in zip(held, self.m, self.v, self.master, self.m_scale,
+                                                   self.v_scale, self.weight_decay)])
+        self._held = held
+        self._held_seen.clear()
         if self.max_norm is not None and self._ws is None:   # (its size follows from the parameters')
             with self._on_current():
                 self._ws = torch.empty(mok_grad_norm_ws_bytes(self._desc), dtype=torch.uint8,
@@ -213,7 +216,7 @@ class AdamW:
             raise ValueError(f"max_norm / grad_scale = {limit} is zero in fp32: nothing would be clipped")
         if grads is not None:
             self.bind(grads)
-        if self._grads is None:
+        if self._held is None:
             raise RuntimeError("step() before any gradients were bound")
         if self.device.type != "cuda":
             raise ValueError(f"a step needs parameters on a GPU, not on {self.device}")

@@ -295,3 +295,22 @@ def test_adamw_refuses_a_stream_of_another_device():
         device = torch.device("cuda", 7)
     with pytest.raises(ValueError, match="cuda:7"):
         opt.step(_grads(1)[0], stream=Other())
+
+
+def test_adamw_step_writes_no_memory_that_was_given_back():
+    """A parameter that gets other memory after bind: the step writes the
+    memory that was bound, which nobody else has been given."""
+    _log("adamw .data")
+    gs = _grads(1)[0]
+    ps, opt = _make()
+    opt.bind(gs)
+    for p in ps:
+        p.data = torch.zeros_like(p)
+    junk = _churn(SIZES) + [torch.full((SIZES[1],), float("nan"), dtype=torch.bfloat16, device=DEV) for _ in range(4)]
+    opt.step()
+    torch.cuda.synchronize()
+    assert all(bool(torch.isnan(t).all()) for t in junk) and not any(p.any() for p in ps)
+    opt.take_params()
+    opt.step(gs)
+    torch.cuda.synchronize()
+    assert all(bool(p.any()) for p in ps)

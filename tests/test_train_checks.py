@@ -185,3 +185,19 @@ def test_router_bwd_refuses_rows_at_the_end_of_int32():
                 with pytest.raises(mok.MokError, match="EINVAL"):
                     mok.mok_router_bwd(cfg, 0, 1, torch.zeros(4), None, None, None, None, torch.zeros(1), False,
                                        torch.zeros(64), 0)
+
+
+def test_optimizer_holds_the_memory_it_bound():
+    """A bound step names memory by address: giving a parameter or a gradient
+    other memory leaves the former one held until the next bind."""
+    n = 1 << 20
+    p, g = torch.nn.Parameter(torch.randn(n)), torch.randn(n)
+    opt = AdamW([p])
+    opt.bind([g])
+    old = p.data_ptr(), g.data_ptr()
+    p.data, g.data = torch.zeros(n), torch.zeros(n)
+    others = [torch.zeros(n) for _ in range(8)]             # would be handed the former memory
+    assert not {t.data_ptr() for t in others} & set(old)
+    assert (opt._desc[0].p, opt._desc[0].g) == old
+    opt.bind([g])
+    assert (opt._desc[0].p, opt._desc[0].g) == (p.data_ptr(), g.data_ptr())
