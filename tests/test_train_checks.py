@@ -1,9 +1,12 @@
 """What the Python side of the training calls refuses and hands on, on the
 CPU: nothing here reaches a kernel."""
 import ctypes
+import gc
 import os
 import re
+import weakref
 
+import numpy as np
 import pytest
 import torch
 
@@ -190,14 +193,16 @@ def test_router_bwd_refuses_rows_at_the_end_of_int32():
 def test_optimizer_holds_the_memory_it_bound():
     """A bound step names memory by address: giving a parameter or a gradient
     other memory leaves the former one held until the next bind."""
-    n = 1 << 20
-    p, g = torch.nn.Parameter(torch.randn(n)), torch.randn(n)
+    arrays = [np.ones(40, dtype=np.float32) for _ in range(2)]
+    alive = [weakref.ref(a) for a in arrays]
+    p, g = (torch.from_numpy(a) for a in arrays)
+    del arrays
     opt = AdamW([p])
     opt.bind([g])
-    old = p.data_ptr(), g.data_ptr()
-    p.data, g.data = torch.zeros(n), torch.zeros(n)
-    others = [torch.zeros(n) for _ in range(8)]             # would be handed the former memory
-    assert not {t.data_ptr() for t in others} & set(old)
-    assert (opt._desc[0].p, opt._desc[0].g) == old
+    p.data, g.data = torch.zeros(40), torch.zeros(40)
+    gc.collect()
+    assert all(a() is not None for a in alive)
     opt.bind([g])
+    gc.collect()
+    assert all(a() is None for a in alive)
     assert (opt._desc[0].p, opt._desc[0].g) == (p.data_ptr(), g.data_ptr())
