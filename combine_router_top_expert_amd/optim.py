@@ -187,10 +187,9 @@ class AdamW:
         for p, g in zip(self.params, grads):
             if g.device != self.device:
                 raise ValueError(f"gradient on {g.device}, parameters on {self.device}")
-        flat = lambda t: None if t is None else t.detach().view(-1)  # noqa: E731
-        held = [(flat(p), flat(g)) for p, g in zip(self.params, grads)]
+        held = [(p.detach(), g.detach()) for p, g in zip(self.params, grads)]
         self._desc = make_params([
-            make_param(p=p, g=g, m=m, v=v, master=flat(w), m_scale=ms, v_scale=vs, weight_decay=wd)
+            make_param(p=p, g=g, m=m, v=v, master=w, m_scale=ms, v_scale=vs, weight_decay=wd)
             for (p, g), m, v, w, ms, vs, wd in zip(held, self.m, self.v, self.master, self.m_scale,
                                                    self.v_scale, self.weight_decay)])
         self._held = held
