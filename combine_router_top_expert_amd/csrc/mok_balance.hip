@@ -178,11 +178,8 @@ struct RowLayout {
   }
 };
 
-// Values of a lane in U rows at once, so their loads are in flight together.
-template <int NV>
-constexpr int rows_at_once() {
-  return 2;
-}
+// Rows of a lane at once, so their loads are in flight together.
+constexpr int kRowsAtOnce = 2;
 // Chosen slots of a row per lane (k <= 16 and k <= E).
 template <int LPR, bool VEC>
 constexpr int slots_per_lane() {
@@ -193,7 +190,7 @@ constexpr int slots_per_lane() {
 // one of the slice (a row past its end reads the last row instead).
 template <int LPR, int NV, bool VEC>
 struct Rows {
-  static constexpr int U = rows_at_once<NV>();
+  static constexpr int U = kRowsAtOnce;
   float v[U][NV];
   uint32_t mask[U];
   bool in[U];
@@ -296,7 +293,7 @@ __device__ __forceinline__ double group_term(const BalArgs& a, int n, double cp)
 template <int LPR, int NV, bool VEC>
 __global__ __launch_bounds__(kBalThreads) void balance_fwd_kernel(BalArgs a) {
   typedef RowLayout<LPR, NV, VEC> RL;
-  constexpr int U = rows_at_once<NV>(), KJ = slots_per_lane<LPR, VEC>();
+  constexpr int U = kRowsAtOnce, KJ = slots_per_lane<LPR, VEC>();
   __shared__ float s_sum[kBalWaves][kMaxE];
   __shared__ int s_cnt[kMaxE];
   __shared__ double s_zz[kBalWaves];
@@ -561,7 +558,7 @@ __global__ __launch_bounds__(kFinThreads) void balance_finish_kernel(BalArgs a) 
 template <int LPR, int NV, bool VEC, bool STREAM>
 __global__ __launch_bounds__(kBalThreads) void balance_bwd_kernel(BalArgs a) {
   typedef RowLayout<LPR, NV, VEC> RL;
-  constexpr int U = rows_at_once<NV>();
+  constexpr int U = kRowsAtOnce;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int l = lane & (LPR - 1), sub = lane / LPR;
   const int c_lo = blockIdx.x * a.rows, c_hi = min(a.T, c_lo + a.rows);
@@ -658,7 +655,7 @@ Shape row_shape(int T, int E, uintptr_t align) {
 // kernel to finish (512 x 8: 5 us in all against 11).
 int chunk_rows(int T, int E, int G) {
   const Shape s = row_shape(T, E, 0);
-  const int64_t step = (int64_t)kBalWaves * (64 / s.lpr) * (s.nv >= 8 ? rows_at_once<8>() : rows_at_once<4>());
+  const int64_t step = (int64_t)kBalWaves * (64 / s.lpr) * kRowsAtOnce;
   if (G == 1 && T <= 4 * step) return (int)(4 * step);
   const int64_t n = (T + kBalWgs * step - 1) / (kBalWgs * step);
   return (int)(step * (n < 1 ? 1 : n));

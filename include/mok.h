@@ -463,7 +463,10 @@ size_t mok_router_bwd_ws_bytes(const mok_config* cfg, int32_t own_n);
  * d at most 2^26, own rows at most 2^31 - 4097.  Without own rows dw_router and d_bias become zero (or
  * stay, with accumulate).  A NaN or infinity in d_logits (for bf16 layers
  * also a value that bf16 rounds to infinity, from 3.39e38 on) makes its row
- * of d_x and its expert's dw_router and d_bias not finite. */
+ * of d_x and its expert's dw_router and d_bias not finite.  One in w_router
+ * or src_x does the same to its column of d_x or dw_router; bf16 layers give
+ * NaN there also where the formula gives an infinity (d_logits is multiplied
+ * in three parts, and a part that is zero makes it 0 * infinity). */
 mok_status mok_router_bwd(const mok_config* cfg, int32_t own_lo, int32_t own_n,
                           const float* d_logits, const void* const* src_x, const void* w_router,
                           void* const* d_x, float* dw_router, float* d_bias, int32_t accumulate,
