@@ -30,8 +30,9 @@
 // (138 MB of logits and ids, 4.6 TB/s: the counts' LDS atomics and the row
 // reductions are not hidden entirely), finishing kernel 7, backward 46 (134 MB
 // read and as much written, 5.8 TB/s; part of the logits comes from the
-// memory-side cache).  Bound by latency when small: 16384 x 64 takes 7 + 7 + 7
-// us, 512 x 8 6 + 4.
+// memory-side cache); in one group the finishing kernel has E / 64 workgroups
+// for all chunks and takes 12.  Bound by latency when small: 16384 x 64 takes
+// 8 + 7 + 7 us, 512 x 8 6 + 4.
 #include "mok_internal.h"
 #include "mok_lanes.h"
 
@@ -634,9 +635,9 @@ struct Shape {
 // at most 64 lanes, the fewest that hold the row with one unit (value) each.
 // Rows of 33 to 64 units take 32 lanes when there are many: two rows of a
 // wave then share the steps of the row reductions (131072 x 256: 87 us against
-// 90, forward 30 against 35; 16 lanes: 29, but the backward 48 against 46),
-// while fewer rows are over sooner with twice the waves (16384 x 256: 27
-// against 29, equal at 50000).
+// 91, in one group 90 against 94; 65536 x 256: 54.7 against 55.3), while fewer
+// rows are over sooner with twice the waves (16384 x 256: 27.4 against 28.9;
+// at 50000 the 32 lanes would take 44.3 against 45.3).
 Shape row_shape(int T, int E, uintptr_t align) {
   Shape s;
   s.vec = E % 4 == 0 && align % 16 == 0;
@@ -652,7 +653,7 @@ Shape row_shape(int T, int E, uintptr_t align) {
 
 // Rows per chunk: whole steps of a workgroup, at most kBalWgs chunks; one
 // group of up to four steps is one chunk, whose workgroup needs no second
-// kernel to finish (512 x 8: 5 us in all against 11).
+// kernel to finish (512 x 8, forward and backward: 13.6 us against 17.4).
 int chunk_rows(int T, int E, int G) {
   const Shape s = row_shape(T, E, 0);
   const int64_t step = (int64_t)kBalWaves * (64 / s.lpr) * kRowsAtOnce;
@@ -774,7 +775,7 @@ mok_status launch_balance_bwd(int T, int E, int k, int G, const mok_balance& b, 
   // Logits and gradients that the 256 MiB memory-side cache cannot hold
   // together: left in it, the gradients are written back under whatever runs
   // next, and push out the logits (131072 x 256, forward and backward: 100
-  // us, 90 us with streaming stores; smaller ones are read again from the
+  // us, 87 us with streaming stores; smaller ones are read again from the
   // cache by the router's backward).
   a.stream = (int64_t)T * E * 8 >= (int64_t)256 << 20;
   a.alpha = b.alpha, a.beta = b.beta;

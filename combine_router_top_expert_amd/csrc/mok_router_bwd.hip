@@ -25,12 +25,12 @@
 //   4. router_reduce_kernel adds the token chunks in order.
 //
 // What bounds it.  16384 x 2048 x 64: HBM (x read, d_x written, 67 MB each):
-// split 6 us, both products 30, reduction 5.  4096 x 7168 x 256: the matrix
-// cores, 75 GFLOP in five parts: split 6 us, both products 81 (0.93 PFLOP/s; a
-// large library product reaches 1.23), reduction 9.  fp32, 512 x 256 x 8:
-// launch latency, 7 + 3 us; 4096 x 7168 x 256: 360 us, 83 TFLOP/s of the 154
-// that a library product reaches (vector work for addresses and LDS stores
-// beside the matrix cores, which are 61 % busy).
+// split 6 us, both products 33, reduction 5.  4096 x 7168 x 256, added: the
+// matrix cores, 90 GFLOP in six parts: split 6 us, both products 95 (0.95
+// PFLOP/s; a large library product reaches 1.23), reduction 9.  fp32, 512 x
+// 256 x 8: launch latency, 7 + 3 us; 4096 x 7168 x 256: 306 us call after
+// call, 98 TFLOP/s of the 154 that a library product reaches (vector work for
+// addresses and LDS stores beside the matrix cores, which are 68 % busy).
 #include <math.h>
 
 #include <algorithm>
@@ -47,7 +47,7 @@ constexpr int kTile = 64;   // fp32: tile side
 constexpr int kKB = 16;     // and contraction steps staged through LDS at a time (32: up to 12 % slower, with half the waves)
 constexpr int kPitch = kTile + 4;
 constexpr int kDxWaves = 4;
-constexpr int kDwWaves = 4;         // dW: two workgroups per CU (one of eight waves: 54 against 49 us)
+constexpr int kDwWaves = 4;         // dW: two workgroups per CU (one of eight waves took a tenth longer in a launch of its own)
 constexpr int kBf16Threads = 64 * kDwWaves;
 constexpr int kBK = 16;             // token rows per LDS stage of dW
 
@@ -726,9 +726,9 @@ __global__ __launch_bounds__(kBf16Threads, 2) void router_dw_bf16_kernel(RArgs a
 }
 // Both products in one launch, dW's workgroups first: they are the longer
 // ones, and the dx workgroups that fill the CUs beside and after them store
-// under their loads (16384 x 2048 x 64: 49 us in all against 55 one after the
-// other; taking turns 60; 4096 x 7168 x 256, which the matrix cores bound:
-// no difference).
+// under their loads (16384 x 2048 x 64: 51 us in all against 58 one after the
+// other; 4096 x 7168 x 128: 65 against 69; x 256, which the matrix cores
+// bound: 114 against 116).
 template <int NK, int EW, bool STREAM>
 __global__ __launch_bounds__(kThreads, 2) void router_both_bf16_kernel(RArgs a, int dw_wgs) {
   __shared__ __attribute__((aligned(16))) char smem[std::max(dx_lds<NK>(), dw_lds<EW>())];
@@ -786,8 +786,8 @@ __global__ __launch_bounds__(kThreads) void router_reduce_kernel(RArgs a, int dw
 
 size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
-// Experts of a dW tile (128, or 64 where fewer experts are padded: both within
-// 2 % on 256 experts; 256 was 5 % slower), and experts of the parts
+// Experts of a dW tile (128, or 64 where fewer experts are padded: 4096 x 7168
+// x 128 takes 65 us in all against 84, x 256 114 against 116), and experts of the parts
 // of dz: a power of two from 64 on, so that dx has whole operands.
 int expert_tile(int E) { return (E + 63) / 64 % 2 ? 64 : 128; }
 int padded_experts(int E) { return E <= 64 ? 64 : E <= 128 ? 128 : E <= 256 ? 256 : 512; }
@@ -817,8 +817,8 @@ Plan make_plan(int prec, int64_t T, int d, int E) {
     // a chunk costs E d 8 bytes (written and read) at about 5 TB/s, 16 tokens
     // of a workgroup 0.25 us while there are fewer workgroups than CUs hold:
     // least in all at the root below.  From one workgroup per CU on, whole
-    // rounds of the CUs, at most two (16384 x 2048 x 64: 32 chunks 55 us, 64
-    // chunks 59)
+    // rounds of the CUs, at most two (16384 x 2048 x 64: 32 chunks 51 us in
+    // all, 64 chunks 60)
     c = (int64_t)(sqrt(9766.0 * (double)T / ((double)E * d)) + 0.5);
     const int64_t rounds = (c * tiles + 128) / 256;
     if (rounds > 0) c = 256 * (rounds < 2 ? rounds : 2) / tiles;
@@ -858,8 +858,8 @@ unsigned dw_workgroups(const RArgs& a) {
   return (unsigned)((a.d + DwCfg<EW>::EN - 1) / DwCfg<EW>::EN) * a.etiles * a.chunks;
 }
 // d_x beyond the 32 MiB of the L2s is stored past them: kept, it is written
-// back under the dW product's loads (16384 x 2048 x 64: 62 us in all against
-// 59).
+// back under the dW product's loads (16384 x 2048 x 64: 53 us in all against
+// 51; 4096 x 7168 x 128: 68 against 65).
 bool stream_dx(const RArgs& a) { return (int64_t)a.T * a.d * 2 > (int64_t)32 << 20; }
 
 template <int NK>

@@ -5,6 +5,8 @@ weights, forward state, staging rows, outputs, gradients, workspace, device
 status word) and calls ``mok_layer_fwd`` / ``mok_layer_bwd``, and for training the
 balance loss (``mok_balance_fwd`` / ``mok_balance_bwd``) with the router
 projection's backward (``mok_router_bwd``).  It does no arithmetic of its own.
+The calls share the layer's buffers: the caller orders calls on different
+streams, and replays of captured ones.
 """
 from __future__ import annotations
 
