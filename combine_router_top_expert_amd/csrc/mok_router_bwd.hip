@@ -441,6 +441,7 @@ __device__ __forceinline__ void dx_bf16(const RArgs& a, int b, char* smem) {
       // takes the exchange: a wave gives acc[1] to the one with the other
       // experts of its rows and adds what that one gives.  Behind the second
       // barrier the pair's base rows are in place too.
+      complete<false>();
       barrier();
       f32x4_t* ex = reinterpret_cast<f32x4_t*>(smem + slot * STAGE);
 #pragma unroll
