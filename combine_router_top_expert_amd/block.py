@@ -131,15 +131,27 @@ class MoEBlock:
             self.layer.forward(stream)
         return [self.layer.out[s] for s in self.own]
 
-    def backward(self, d_out, d_res=None, stream=None, router_grad=True):
+    def backward(self, d_out, d_res=None, stream=None, router_grad=True, balance=False, d_loss=None):
         """d_out: per source of the layer, the gradient of its outputs; d_res:
         per own source, the gradient that reaches the residual stream behind
         this block's addition, or None.  Returns the gradients of res and delta
         (the stream's type; ``norms[i].d_x`` in the layer's); dw_norm and the
-        layer's gradients are overwritten."""
+        layer's gradients are overwritten.  balance: the gradient of the
+        layer's last ``balance_loss`` (d_loss its weights, None = ones) is in
+        all of them; the layer's own ``balance_backward`` would come after the
+        norm has read d_x, and refuses."""
         L = self.layer
+        if balance:
+            if not router_grad:
+                raise ValueError("balance adds to the router's gradient: router_grad")
+            if getattr(L, "_bal", None) is None:
+                raise RuntimeError("balance needs the layer's balance_loss before it")
+            L._check(d_loss, torch.float32, 2)
         with torch.cuda.device(L.device):
             L.backward(d_out, stream, router_grad)
+            if balance:
+                L.balance_backward(d_loss, stream)
+            L._d_x_read = True
             return [n.backward(L.d_x[s], None if d_res is None else d_res[i], i > 0, stream)
                     for i, (s, n) in enumerate(zip(self.own, self.norms))]
 

@@ -104,6 +104,7 @@ class MoELayer(StreamUser):
                                 self.logits)
         self.with_bwd = with_bwd
         self._bal_bufs = {}
+        self._d_x_read = False   # a block's norm has taken d_x on
         self.d_bias = None       # the balance losses' gradient of a router bias
         # bf16 backward: the weights also transposed (mok_prepare_bwd), so dh
         # and dx read them k-contiguous (bit-identical either way)
@@ -230,6 +231,7 @@ class MoELayer(StreamUser):
 
     def backward(self, d_out: List[torch.Tensor], stream=None, router_grad=True):
         dw_router = self.dw_router if router_grad else None
+        self._d_x_read = False
         if self.checkpoint and self.prec == "bf16" and not self.cfg.bwd_ring_bytes:
             mok_layer_bwd_checkpoint(self.cfg, self.own_lo, self.own_n, d_out, self.xs, self.w_router, self.e2l,
                                      self.weights, self.state, self.ck_codes, self.ck_scales, self.staging,
@@ -288,11 +290,13 @@ class MoELayer(StreamUser):
     def balance_backward(self, d_loss=None, stream=None):
         """Adds the gradient of d_loss[0] * balance loss + d_loss[1] * z-loss
         (d_loss fp32 [2] on the device, None = ones) to d_x and dw_router,
-        after backward().  With a router bias, d_bias [E] becomes these
+        after backward() (in a block: MoEBlock.backward(balance=True)).  With a router bias, d_bias [E] becomes these
         losses' gradient of it; backward() forms none, so the share that comes
         through the gates is not in it."""
         if getattr(self, "_bal", None) is None or not self.with_bwd:
             raise RuntimeError("balance_backward needs balance_loss and backward before it")
+        if self._d_x_read:
+            raise RuntimeError("the block's norm has read d_x already: MoEBlock.backward(balance=True)")
         self._check(d_loss, torch.float32, 2)
         with torch.cuda.device(self.device):
             T, lo = self.own_n * self.T_src, self.own_lo * self.T_src

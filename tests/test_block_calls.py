@@ -1,0 +1,74 @@
+"""The order and the arguments of the calls that a block makes, on the CPU:
+nothing here reaches a kernel."""
+import pytest
+import torch
+
+import combine_router_top_expert_amd.block as block_mod
+import combine_router_top_expert_amd.layer as layer_mod
+from combine_router_top_expert_amd.block import MoEBlock
+from combine_router_top_expert_amd.layer import MoELayer
+
+BF, F = torch.bfloat16, torch.float32
+
+
+class _Device:
+    def __init__(self, device):
+        pass
+
+    def __enter__(self):
+        pass
+
+    def __exit__(self, *exc):
+        pass
+
+
+@pytest.fixture
+def calls(monkeypatch):
+    """The ABI calls are noted instead of made."""
+    seen = []
+    monkeypatch.setattr(torch.cuda, "device", _Device)
+    monkeypatch.setattr(torch.cuda, "stream", _Device)
+    note = lambda n: (lambda *a, **k: seen.append((n, a)))  # noqa: E731
+    for m, names in ((block_mod, ("mok_norm_fwd", "mok_norm_bwd")),
+                     (layer_mod, ("mok_layer_fwd", "mok_layer_bwd", "mok_balance_fwd", "mok_balance_bwd",
+                                  "mok_router_bwd"))):
+        for n in names:
+            monkeypatch.setattr(m, n, note(n))
+    return seen
+
+
+def _block(own=(0, 1), S=1, T=4, d=64, E=4, **kw):
+    L = MoELayer(S, T, d, E, 2, 64, E, "bf16", 8, own[0], own[1], device="cpu", two_streams=False,
+                 transposed_weights=False, **kw)
+    b = MoEBlock(L, torch.ones(d, dtype=BF), "f32")
+    L.xs, L.w_router, L.bias, L.e2l = [n.y for n in b.norms], torch.zeros(E, d, dtype=BF), None, None
+    L.weights = None
+    return b
+
+
+def test_block_backward_adds_the_balance_gradient_before_the_norm(calls):
+    """The norm's backward reads d_x: the losses' gradient has to be in it by then."""
+    b = _block(keep_logits=True)
+    dout = [torch.zeros(4, 64, dtype=BF)]
+    b.forward([torch.zeros(4, 64)])
+    with pytest.raises(RuntimeError, match="balance_loss"):
+        b.backward(dout, balance=True)
+    b.layer.balance_loss(0.1, 0.1)
+    calls.clear()
+    with pytest.raises(ValueError, match="router_grad"):
+        b.backward(dout, balance=True, router_grad=False)
+    for bad in (torch.ones(3), torch.ones(2, dtype=BF)):
+        with pytest.raises(ValueError, match="expected"):
+            b.backward(dout, balance=True, d_loss=bad)
+    assert not calls
+    w = torch.ones(2)
+    b.backward(dout, balance=True, d_loss=w)
+    assert [n for n, _ in calls] == ["mok_layer_bwd", "mok_balance_bwd", "mok_router_bwd", "mok_norm_bwd"]
+    assert any(t is w for t in calls[1][1])
+    # behind the norm's backward the gradient would be lost
+    with pytest.raises(RuntimeError, match="balance=True"):
+        b.layer.balance_backward()
+    calls.clear()
+    b.layer.backward(dout)
+    b.layer.balance_backward()
+    assert [n for n, _ in calls] == ["mok_layer_bwd", "mok_balance_bwd", "mok_router_bwd"]

@@ -1,0 +1,77 @@
+"""Blocks with the calls around them that a training program makes."""
+import pytest
+import torch
+
+from combine_router_top_expert_amd.block import MoEBlock
+from combine_router_top_expert_amd.layer import MoELayer
+from test_gpu_train import DEV, _gen, _log
+
+pytestmark = pytest.mark.gpu
+
+
+def _block_in_64(res, delta, wn, wr, wg, wu, wd, k, eps):
+    """r, out, balance loss (times 1 / alpha) and z-loss (times 1 / beta) of a block, all its rows one group."""
+    r = res + delta
+    y = r * (r.square().mean(1, keepdim=True) + eps).rsqrt() * wn
+    z = y @ wr.t()
+    top = z.topk(k, 1)
+    gate = torch.softmax(top.values, 1)
+    out = 0.0
+    for e in range(wr.shape[0]):
+        g = (gate * (top.indices == e)).sum(1, keepdim=True)
+        a, b = y @ wg[e].t(), y @ wu[e].t()
+        out = out + g * ((a * torch.sigmoid(a) * b) @ wd[e].t())
+    n, E = z.shape
+    share = torch.bincount(top.indices.reshape(-1), minlength=E).double() / (k * n)
+    return r, out, E * (share * torch.softmax(z, 1).mean(0)).sum(), torch.logsumexp(z, 1).square().mean()
+
+
+def test_block_gradients_with_balance_losses():
+    """Two fp32 blocks whose layers have balance and z-losses, against autograd in 64 bits: the losses' gradients
+    reach the residual stream, the first block and the norms' weights.  Errors as without the losses (a chain of
+    about ten products of at most 192 terms: below 1e-4 of a result's norm); their own are those of a softmax row,
+    96 u.  The losses weigh enough for every gradient to differ by a hundredth without them (asserted)."""
+    _log("block balance")
+    S, T, d, E, k, I, eps, alpha, beta = 2, 70, 128, 8, 2, 192, 1e-6, 4000.0, 300.0
+    gen = _gen(22)
+    rnd = lambda *s, std=1.0: (std * torch.randn(*s, generator=gen)).to(DEV)  # noqa: E731
+    blocks, refs, plain = [], [], []
+    for _ in range(2):
+        L = MoELayer(S, T, d, E, k, I, E, "f32", S * T * k, 0, S, device=DEV, keep_logits=True)
+        wn = 1 + rnd(d, std=0.2)
+        w = [rnd(E, d, std=d ** -0.5), rnd(E, I, d, std=d ** -0.5), rnd(E, I, d, std=d ** -0.5), rnd(E, d, I, std=I ** -0.5)]
+        b = MoEBlock(L, wn, "f32", eps)
+        b.set_inputs(w[0], None, torch.arange(E, dtype=torch.int32, device=DEV), *w[1:])
+        blocks.append(b)
+        refs.append([t.double().requires_grad_() for t in (wn, *w)])
+        plain.append([t.double().requires_grad_() for t in (wn, *w)])
+    res, delta = [rnd(T, d, std=2.0) for _ in range(S)], [rnd(T, d) for _ in range(S)]
+    dout, dres = [rnd(T, d) for _ in range(S)], [rnd(T, d) for _ in range(S)]
+    dl = torch.tensor([2.0, 0.5], device=DEV)
+    o1 = blocks[0].forward(res, delta)
+    blocks[1].forward(blocks[0].res, o1)
+    losses = [b.layer.balance_loss(alpha, beta) for b in blocks]
+    g2 = blocks[1].backward(dout, dres, balance=True, d_loss=dl)
+    g1 = blocks[0].backward([n.d_x for n in blocks[1].norms], g2, balance=True)
+    torch.cuda.synchronize()
+    for b in blocks:
+        b.layer.check_status()
+
+    def in_64(ws, weight):
+        R, D = (torch.cat(t).double().requires_grad_() for t in (res, delta))
+        r, out, b1, z1 = _block_in_64(R, D, *ws[0], k, eps)
+        r, out, b2, z2 = _block_in_64(r, out, *ws[1], k, eps)
+        total = (out * torch.cat(dout).double()).sum() + (r * torch.cat(dres).double()).sum()
+        (total + weight * (alpha * b1 + beta * z1 + 2.0 * alpha * b2 + 0.5 * beta * z2)).backward()
+        return R.grad, D.grad, torch.stack([alpha * b1, beta * z1, alpha * b2, beta * z2]).detach().cpu().view(2, 2)
+    R, D, want = in_64(refs, 1.0)
+    R0, _, _ = in_64(plain, 0.0)
+    near = lambda a, b: float((a.double() - b).norm() / b.norm())  # noqa: E731
+    assert near(R0, R) > 1e-2
+    for got, ref in ((torch.cat(g1), R), (torch.cat(g1), D), (torch.stack(losses).cpu(), want)):
+        assert near(got, ref) < 1e-4
+    for b, ref, bare in zip(blocks, refs, plain):
+        L = b.layer
+        for i, (got, w) in enumerate(zip((b.dw_norm, L.dw_router, L.dw_gate, L.dw_up, L.dw_down), ref)):
+            assert near(got, w.grad) < 1e-4, i
+        assert all(near(bare[i].grad, ref[i].grad) > 1e-2 for i in (0, 1))
