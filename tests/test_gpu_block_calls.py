@@ -2,8 +2,10 @@
 import pytest
 import torch
 
+import combine_router_top_expert_amd as mok
 from combine_router_top_expert_amd.block import MoEBlock
 from combine_router_top_expert_amd.layer import MoELayer
+from test_gpu_block import _grads, _layer
 from test_gpu_train import DEV, _gen, _log
 
 pytestmark = pytest.mark.gpu
@@ -75,3 +77,34 @@ def test_block_gradients_with_balance_losses():
         for i, (got, w) in enumerate(zip((b.dw_norm, L.dw_router, L.dw_gate, L.dw_up, L.dw_down), ref)):
             assert near(got, w.grad) < 1e-4, i
         assert all(near(bare[i].grad, ref[i].grad) > 1e-2 for i in (0, 1))
+
+
+@pytest.mark.parametrize("mb,slots", [(64, 3), (128, 1)])
+def test_layers_that_checkpoint_with_a_ring_backward(mb, slots):
+    """Two layers that share ab and h, whose backward goes through a ring: both unpack their checkpoint into the shared
+    buffers.  The gradients are the bytes of the ring's and of the one-launch backward on what the checkpoints stand
+    for, and of the backward that reads the checkpoint itself."""
+    _log("ring checkpoint", mb, slots)
+    d, I, E = 128, 192, 8
+    ring = dict(minibatch_rows=mb, bwd_ring_bytes=(64 * E + 64) * d * 2 + 768 + slots * mb * (2 * d + 2 * I) * 2)
+    A, dout = _layer("bf16", 3, checkpoint=True, **ring)
+    B, _ = _layer("bf16", 4, checkpoint=True, scratch=A, **ring)
+    A.forward()
+    B.forward()                                # ab and h now hold B's
+    for L in (B, A):
+        L.backward(dout)
+    got = [_grads(L) for L in (A, B)]
+    for L, seed, g in ((A, 3, got[0]), (B, 4, got[1])):
+        L.check_status()
+        for kw in (ring, {}):
+            P, _ = _layer("bf16", seed, **kw)
+            P.forward()
+            mok.mok_checkpoint_unpack(P.cfg, P.offsets, L.ck_codes, L.ck_scales, P.ab, P.h)
+            P.backward(dout)
+            for i, (a, b) in enumerate(zip(g, _grads(P))):
+                assert torch.equal(a, b), i
+        C, _ = _layer("bf16", seed, checkpoint=True)
+        C.forward()
+        C.backward(dout)
+        for i, (a, b) in enumerate(zip(g, _grads(C))):
+            assert torch.equal(a, b), i
