@@ -55,6 +55,16 @@ class RMSNorm(StreamUser):
         one of them may be None.  Returns y [T, d]; res, rstd, codes and scales
         hold the rest in their first T rows.  All are overwritten by the next
         call."""
+        T = self._rows_of(x, res)
+        with torch.cuda.device(self.device):
+            self._hold(stream, x, res)
+            mok_norm_fwd(self.cfg, T, x, res, self.weight, self.eps, self.res, self.y, self.codes, self.scales,
+                         self.rstd, stream)
+        self.T = T
+        return self.y[:T]
+
+    def _rows_of(self, x, res) -> int:
+        """How many rows a forward of x and res has; refuses what it could not read."""
         first = x if x is not None else res
         if first is None or first.dim() != 2:
             raise ValueError("rows [T, d] expected")
@@ -65,13 +75,7 @@ class RMSNorm(StreamUser):
             self._expect("x", x, self.act, (T, self.d))
         if res is not None:
             self._expect("res", res, self.res_dt, (T, self.d))
-        self.T = T
-        cut = lambda t: None if t is None else t[:T]  # noqa: E731
-        with torch.cuda.device(self.device):
-            self._hold(stream, x, res)
-            mok_norm_fwd(self.cfg, T, x, res, self.weight, self.eps, self.res, self.y, self.codes, self.scales,
-                         self.rstd, stream)
-        return cut(self.y)
+        return T
 
     def backward(self, dy: torch.Tensor, d_res: Optional[torch.Tensor] = None, accumulate=False, stream=None):
         """The gradient of the last forward's res (and x): dy [T, d] reaches
@@ -118,6 +122,10 @@ class MoEBlock:
             xs[s] = x
         self.layer.set_inputs(xs, w_router, bias, e2l, w_gate, w_up, w_down, other_topk)
 
+    def _per_source(self, what, rows):
+        if len(rows) != len(self.norms):
+            raise ValueError(f"{what}: one tensor for each of {len(self.norms)} own sources expected, got {len(rows)}")
+
     @property
     def res(self) -> List[torch.Tensor]:
         """The residual stream behind this block's addition, per own source."""
@@ -125,9 +133,16 @@ class MoEBlock:
 
     def forward(self, res, delta=None, stream=None):
         """res, delta: per own source [T_src, d]; delta None for the first block.  Returns the layer's outputs."""
+        delta = [None] * len(self.norms) if delta is None else delta
+        self._per_source("res", res)
+        self._per_source("delta", delta)
+        for n, r, x in zip(self.norms, res, delta):
+            T = n._rows_of(x, r)
+            if T != self.layer.T_src:         # the layer routes all rows of n.y
+                raise ValueError(f"{T} rows, and the layer has {self.layer.T_src} of every source")
         with torch.cuda.device(self.layer.device):
             for i, n in enumerate(self.norms):
-                n.forward(None if delta is None else delta[i], res[i], stream)
+                n.forward(delta[i], res[i], stream)
             self.layer.forward(stream)
         return [self.layer.out[s] for s in self.own]
 

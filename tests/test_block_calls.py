@@ -72,3 +72,21 @@ def test_block_backward_adds_the_balance_gradient_before_the_norm(calls):
     b.layer.backward(dout)
     b.layer.balance_backward()
     assert [n for n, _ in calls] == ["mok_layer_bwd", "mok_balance_bwd", "mok_router_bwd"]
+
+
+@pytest.mark.parametrize("own", [(0, 1), (0, 2)])
+def test_block_refuses_rows_that_the_layer_would_not_have(calls, own):
+    """The layer routes all rows of its sources: rows that the norm does not write would be an earlier call's."""
+    b = _block(own, S=2)
+    n = own[1]
+    res, delta = [torch.zeros(4, 64) for _ in range(n)], [torch.zeros(4, 64, dtype=BF) for _ in range(n)]
+    short, narrow = res[:-1] + [torch.zeros(3, 64)], res[:-1] + [torch.zeros(4, 32)]
+    for args in ((short,), (short, delta[:-1] + [torch.zeros(3, 64, dtype=BF)]), (res, delta[:-1] + [torch.zeros(3, 64, dtype=BF)]),
+                 (narrow,), (res[:-1],), (res + res[:1],), (res, delta[:-1]), (res, delta + delta), ([None] * n,),
+                 (res[:-1] + [torch.zeros(5, 64)],), ([t.to(BF) for t in res],), (res, res)):
+        with pytest.raises(ValueError):
+            b.forward(*args)
+    assert not calls
+    b.forward(res, delta)
+    b.forward([None] * n, delta)
+    assert [c for c, _ in calls] == (["mok_norm_fwd"] * n + ["mok_layer_fwd"]) * 2
