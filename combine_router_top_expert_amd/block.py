@@ -156,6 +156,14 @@ class MoEBlock:
         all of them; the layer's own ``balance_backward`` would come after the
         norm has read d_x, and refuses."""
         L = self.layer
+        for n in self.norms:                  # (all of it before the layer's gradients are written)
+            if n.T != L.T_src:
+                raise RuntimeError(f"backward of the block's own forward: a norm's last one had {n.T} rows, not {L.T_src}")
+        if d_res is not None:
+            self._per_source("d_res", d_res)
+            for n, t in zip(self.norms, d_res):
+                if t is not None:
+                    n._expect("d_res", t, n.res_dt, (n.T, n.d))
         if balance:
             if not router_grad:
                 raise ValueError("balance adds to the router's gradient: router_grad")

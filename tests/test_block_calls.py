@@ -90,3 +90,25 @@ def test_block_refuses_rows_that_the_layer_would_not_have(calls, own):
     b.forward(res, delta)
     b.forward([None] * n, delta)
     assert [c for c, _ in calls] == (["mok_norm_fwd"] * n + ["mok_layer_fwd"]) * 2
+
+
+def test_block_backward_refuses_before_it_writes_gradients(calls):
+    """Refused arguments leave the layer's gradients as they were."""
+    b = _block((0, 2), S=2)
+    dout, dres = [torch.zeros(4, 64, dtype=BF)] * 2, [torch.zeros(4, 64)] * 2
+    with pytest.raises(RuntimeError, match="forward"):
+        b.backward(dout)
+    b.forward(dres)
+    calls.clear()
+    for bad in ((dout, dres[:1]), (dout, dres + dres), (dout, [torch.zeros(3, 64)] * 2), (dout, dout),
+                (dout, [dres[0], torch.zeros(64, 4).t()])):
+        with pytest.raises(ValueError):
+            b.backward(*bad)
+    b.norms[1].forward(torch.zeros(3, 64, dtype=BF))
+    calls.clear()
+    with pytest.raises(RuntimeError, match="3 rows"):
+        b.backward(dout, dres)
+    assert not calls
+    b.forward(dres)
+    b.backward(dout, [None, dres[1]])
+    assert [c for c, _ in calls] == ["mok_norm_fwd", "mok_norm_fwd", "mok_layer_fwd", "mok_layer_bwd", "mok_norm_bwd", "mok_norm_bwd"]
