@@ -95,13 +95,13 @@ class RMSNorm(StreamUser):
         return self.d_r[:self.T]
 
 
-class MoEBlock:
+class MoEBlock(StreamUser):
     """res <- res + delta, out = layer(norm(res)): the norm of the layer's own
     sources, then the layer; ``decode`` for the rows of a few tokens.  ``out`` is the next block's delta.  Other sources'
     rows are given to the layer by their owners (``layer.xs``)."""
 
     def __init__(self, layer: MoELayer, weight: torch.Tensor, res_type="bf16", eps=1e-6):
-        self.layer = layer
+        self.layer, self.device = layer, layer.device
         self.own = list(range(layer.own_lo, layer.own_lo + layer.own_n))
         prec = "f32" if layer.prec == "f32" else "bf16"
         if weight.numel() != layer.d:
@@ -175,6 +175,9 @@ class MoEBlock:
             if balance:
                 L.balance_backward(d_loss, stream)
             L._d_x_read = True
+            if not self.norms:                # no rows: the sum over them is zero
+                with torch.cuda.stream(self._torch_stream(stream)):
+                    self.dw_norm.zero_()
             return [n.backward(L.d_x[s], None if d_res is None else d_res[i], i > 0, stream)
                     for i, (s, n) in enumerate(zip(self.own, self.norms))]
 

@@ -112,3 +112,12 @@ def test_block_backward_refuses_before_it_writes_gradients(calls):
     b.forward(dres)
     b.backward(dout, [None, dres[1]])
     assert [c for c, _ in calls] == ["mok_norm_fwd", "mok_norm_fwd", "mok_layer_fwd", "mok_layer_bwd", "mok_norm_bwd", "mok_norm_bwd"]
+
+
+def test_block_without_own_sources(calls):
+    """A rank that holds experts and no tokens: the norm's weight has no gradient, whatever an earlier step left."""
+    b = _block((0, 0), S=2)
+    b.dw_norm.fill_(float("nan"))
+    assert b.forward([]) == []
+    assert b.backward([torch.zeros(4, 64, dtype=BF)] * 2) == []
+    assert (b.dw_norm == 0).all()
