@@ -49,6 +49,7 @@ class RMSNorm(StreamUser):
             self.dw = torch.zeros(self.d, dtype=torch.float32, device=self.device)
             with torch.cuda.device(self.device):
                 self.ws = new(torch.uint8, mok_norm_bwd_ws_bytes(self.cfg, max(rows, 1)))
+        self._ready()
 
     def forward(self, x: Optional[torch.Tensor], res: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
         """x [T, d] (the layer's type) added to res [T, d] (the stream's type);
@@ -57,6 +58,7 @@ class RMSNorm(StreamUser):
         call."""
         T = self._rows_of(x, res)
         with torch.cuda.device(self.device):
+            self._enter(stream)
             self._hold(stream, x, res)
             mok_norm_fwd(self.cfg, T, x, res, self.weight, self.eps, self.res, self.y, self.codes, self.scales,
                          self.rstd, stream)
@@ -89,6 +91,7 @@ class RMSNorm(StreamUser):
         if d_res is not None:
             self._expect("d_res", d_res, self.res_dt, (self.T, self.d))
         with torch.cuda.device(self.device):
+            self._enter(stream)
             self._hold(stream, dy, d_res)
             mok_norm_bwd(self.cfg, self.T, dy, self.res, self.weight, self.rstd, d_res, self.d_r,
                          None if self.d_x is self.d_r else self.d_x, self.dw, accumulate, self.ws, stream)
@@ -106,12 +109,14 @@ class MoEBlock(StreamUser):
         prec = "f32" if layer.prec == "f32" else "bf16"
         if weight.numel() != layer.d:
             raise ValueError(f"norm weight of {layer.d} elements expected, got {weight.numel()}")
+        # (before the norms: their calls come after what made them)
+        self.dw_norm = torch.zeros(layer.d, dtype=torch.float32, device=weight.device) if layer.with_bwd else None
         self.norms = [RMSNorm(weight, layer.T_src, prec, res_type, eps, with_bwd=layer.with_bwd) for _ in self.own]
         self.weight, self.eps = weight, eps
         self._decode_norms = {}
-        self.dw_norm = torch.zeros(layer.d, dtype=torch.float32, device=weight.device) if layer.with_bwd else None
         for n in self.norms:
             n.dw = self.dw_norm
+        self._ready()
 
     def set_inputs(self, w_router, bias, e2l, w_gate, w_up, w_down, other_xs=None, other_topk=None):
         """The layer's weights; other_xs: {source: rows} of the sources that are not its own."""
@@ -176,6 +181,7 @@ class MoEBlock(StreamUser):
                 L.balance_backward(d_loss, stream)
             L._d_x_read = True
             if not self.norms:                # no rows: the sum over them is zero
+                self._enter(stream)
                 with torch.cuda.stream(self._torch_stream(stream)):
                     self.dw_norm.zero_()
             return [n.backward(L.d_x[s], None if d_res is None else d_res[i], i > 0, stream)

@@ -3,8 +3,8 @@
 ``MoEDecoder`` owns the 4-bit weights and the buffers of ``mok_route`` and
 ``mok_decode_ffn`` for up to ``tokens`` tokens.  It does no arithmetic of its
 own.  Its weights are laid out on the stream that is current when it is made,
-and its calls share their buffers: the caller orders calls on different
-streams, and replays of captured ones.
+which its calls on other streams come after; its calls share their buffers: the
+caller orders calls on different streams, and replays of captured ones.
 """
 from __future__ import annotations
 
@@ -43,6 +43,7 @@ class MoEDecoder(StreamUser):
         self.status = torch.zeros(1, dtype=torch.int32, device=self.device)
         self.weights: Optional[mok_w4] = None
         self.update_weights(w_gate, w_up, w_down)
+        self._ready()
 
     def update_weights(self, w_gate, w_up, w_down, stream=None):
         """Other expert weights of the same sizes in the place of the ones
@@ -50,6 +51,7 @@ class MoEDecoder(StreamUser):
         read them."""
         s = self._torch_stream(stream)
         with torch.cuda.device(self.device), torch.cuda.stream(s):
+            self._enter(stream)
             rows = []
             for name, w, shape in (("w_gate", w_gate, (self.E_local, self.I, self.d)),
                                    ("w_up", w_up, (self.E_local, self.I, self.d)),
@@ -78,6 +80,7 @@ class MoEDecoder(StreamUser):
             self._expect("codes", codes, torch.uint8, (T, self.d))
             self._expect("scales", scales, torch.uint8, (T, self.d // 32))
         with torch.cuda.device(self.device):
+            self._enter(stream)
             self._hold(stream, x, codes, scales)
             mok_route(self.cfg, T, x, self.w_router, self.bias, self.topk_idx, self.topk_gate, stream)
             mok_decode_ffn(self.cfg, T, x if codes is None else codes, scales, self.topk_idx, self.topk_gate, self.e2l,

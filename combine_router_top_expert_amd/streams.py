@@ -4,10 +4,43 @@ from __future__ import annotations
 
 import torch
 
+from . import _stream
+
 
 class StreamUser:
     """A class with a ``device`` whose calls take ``stream``: None (the current
     one), a torch stream or a raw handle."""
+
+    _streams = _made = None
+
+    def _ready(self):
+        """The object is made: its buffers are filled, or may be memory that
+        others used, by work of the current stream, which calls on other
+        streams come after (_enter)."""
+        self._streams = set()
+        if self.device.type == "cuda":
+            with torch.cuda.device(self.device):
+                s = torch.cuda.current_stream()
+                self._streams.add(s.cuda_stream)
+                if not torch.cuda.is_current_stream_capturing():
+                    self._made = s.record_event()
+
+    def _enter(self, stream):
+        """A call on `stream` begins, with the device current.  The first one on
+        a stream comes after what made the object.  Not in a capture, which
+        waits for nothing outside it."""
+        if self._streams is None or self.device.type != "cuda":
+            return
+        handle = _stream(stream)
+        if handle in self._streams:
+            return
+        s = torch.cuda.current_stream() if stream is None else self._torch_stream(stream)
+        with torch.cuda.stream(s):
+            if torch.cuda.is_current_stream_capturing():
+                return
+        self._streams.add(handle)
+        if self._made is not None:
+            s.wait_event(self._made)
 
     def _torch_stream(self, stream):
         """The torch stream of a call's `stream` (None: the current one, or a raw handle)."""

@@ -1,0 +1,116 @@
+"""How the classes around the layer order themselves over streams, on
+the CPU with streams that note what is asked of them."""
+import pytest
+import torch
+
+import combine_router_top_expert_amd as mok
+import combine_router_top_expert_amd.block as block_mod
+import combine_router_top_expert_amd.decode as decode_mod
+import combine_router_top_expert_amd.streams as streams_mod
+from combine_router_top_expert_amd.block import RMSNorm
+from combine_router_top_expert_amd.decode import MoEDecoder
+from combine_router_top_expert_amd.streams import StreamUser
+
+BF = torch.bfloat16
+
+
+class _Stream:
+    def __init__(self, handle, notes):
+        self.cuda_stream, self.notes, self.captured = handle, notes, False
+
+    def record_event(self):
+        return f"event of {self.cuda_stream}"
+
+    def wait_event(self, e):
+        self.notes.append((self.cuda_stream, "waits for", e))
+
+
+@pytest.fixture
+def gpu(monkeypatch):
+    """Three streams, the first of them current."""
+    notes = []
+    streams = [_Stream(i, notes) for i in range(3)]
+    now = [streams[0]]
+
+    class Context:
+        def __init__(self, what):
+            self.what = what
+
+        def __enter__(self):
+            self.before = now[0]
+            if isinstance(self.what, _Stream):
+                now[0] = self.what
+
+        def __exit__(self, *exc):
+            now[0] = self.before
+    monkeypatch.setattr(torch.cuda, "device", Context)
+    monkeypatch.setattr(torch.cuda, "stream", Context)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda: now[0])
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: now[0].captured)
+    monkeypatch.setattr(streams_mod, "_stream", lambda s: (now[0] if s is None else s).cuda_stream, raising=False)
+    return streams, notes, Context
+
+
+def test_first_call_on_a_stream_comes_after_the_making(gpu):
+    streams, notes, on = gpu
+
+    class User(StreamUser):
+        device = torch.device("cuda", 0)
+    u = User()
+    u._ready()
+    u._enter(None)
+    u._enter(streams[0])
+    assert not notes
+    u._enter(streams[1])
+    first = [(1, "waits for", "event of 0")]
+    assert notes == first
+    u._enter(streams[1])
+    with on(streams[1]):
+        u._enter(None)
+    assert notes == first
+    # a capture waits for nothing outside it, and its stream's first eager call does
+    streams[2].captured = True
+    u._enter(streams[2])
+    assert notes == first
+    streams[2].captured = False
+    with on(streams[2]):
+        u._enter(None)
+    assert notes[1:] == [(2, "waits for", "event of 0")]
+    # made within a capture: no event to wait for outside it
+    notes.clear()
+    streams[0].captured = True
+    u = User()
+    u._ready()
+    streams[0].captured = False
+    u._enter(streams[1])
+    assert not notes
+
+
+@pytest.fixture
+def entered(monkeypatch, gpu):
+    """What enters on which stream, and the ABI calls, in their order."""
+    seen = []
+    monkeypatch.setattr(StreamUser, "_enter", lambda self, s: seen.append((type(self).__name__, s)), raising=False)
+    monkeypatch.setattr(StreamUser, "_hold", lambda self, s, *t: None)
+    for m, names in ((block_mod, ("mok_norm_fwd", "mok_norm_bwd")),
+                     (decode_mod, ("mok_route", "mok_decode_ffn", "mok_mxfp4_quantize")), (mok, ("mok_mxfp4_tile",))):
+        for n in names:
+            monkeypatch.setattr(m, n, lambda *a, _n=n, **k: seen.append(_n))
+    return seen
+
+
+def test_calls_enter_on_their_stream(entered, gpu):
+    s = gpu[0][1]
+    n = RMSNorm(torch.ones(64, dtype=BF), 4, mx=True)
+    x = torch.zeros(3, 64, dtype=BF)
+    n.forward(x, stream=s)
+    n.backward(x, stream=s)
+    assert entered == [("RMSNorm", s), "mok_norm_fwd", ("RMSNorm", s), "mok_norm_bwd"]
+    w = [torch.zeros(2, 128, 128, dtype=BF)] * 3
+    d = MoEDecoder(torch.zeros(8, 128, dtype=BF), torch.zeros(8), torch.zeros(8, dtype=torch.int32), *w, 2, 4)
+    entered.clear()
+    d(torch.zeros(3, 128, dtype=BF), stream=s)
+    assert entered == [("MoEDecoder", s), "mok_route", "mok_decode_ffn"]
+    entered.clear()
+    d.update_weights(*w, stream=s)
+    assert entered[0] == ("MoEDecoder", s) and "mok_mxfp4_quantize" in entered

@@ -1,0 +1,73 @@
+"""The norm and the 4-bit experts on another stream than the one that made
+them, behind work that keeps either busy: the bytes of the same calls on one
+stream."""
+import pytest
+import torch
+
+from combine_router_top_expert_amd.block import RMSNorm
+from combine_router_top_expert_amd.decode import MoEDecoder
+from test_gpu_train import DEV, _gen, _log
+from test_gpu_train_streams import _busy, _same
+
+pytestmark = pytest.mark.gpu
+
+BF = torch.bfloat16
+
+
+def _norm_inputs():
+    g = _gen(3)
+    rnd = lambda *s: torch.randn(*s, generator=g).to(DEV)  # noqa: E731
+    return (1 + 0.2 * rnd(512)).to(BF), rnd(700, 512).to(BF), rnd(700, 512), rnd(700, 512).to(BF), rnd(700, 512)
+
+
+def _make_norm(w):
+    return RMSNorm(w, 700, "bf16", "f32", mx=True)
+
+
+def _norm_calls(n, x, res, dy, up, stream):
+    y = n.forward(x, res, stream)
+    d_r = n.backward(dy, up, stream=stream)
+    return [y, d_r, n.dw, n.d_x, n.codes, n.scales]
+
+
+def _decoder_inputs(tokens=37):
+    g = _gen(4)
+    E, d, I = 8, 256, 384
+    rnd = lambda *s: torch.randn(*s, generator=g).to(DEV, BF)  # noqa: E731
+    w = [rnd(E, d), rnd(E, I, d), rnd(E, I, d), rnd(E, d, I)]
+    return w, rnd(tokens, d)
+
+
+def _make_decoder(w):
+    return MoEDecoder(w[0], None, torch.arange(8, dtype=torch.int32, device=DEV), *w[1:], 2, 64)
+
+
+def _bytes(ts):
+    torch.cuda.synchronize()
+    return [t.clone().view(torch.uint8) for t in ts]
+
+
+@pytest.mark.parametrize("raw", [False, True])
+def test_first_call_on_another_stream(raw):
+    """Made behind a busy stream, used on an idle one: after the zeros of dw and status, and the weights' layout."""
+    _log("block first call", raw)
+    wn, x, res, dy, up = _norm_inputs()
+    w, rows = _decoder_inputs()
+    want = _bytes(_norm_calls(_make_norm(wn), x, res, dy, up, None)) + _bytes([_make_decoder(w)(rows)])
+    side = torch.cuda.Stream()
+    arg = side.cuda_stream if raw else side
+    torch.cuda.synchronize()
+    _busy(torch.cuda.current_stream())
+    n = _make_norm(wn)
+    got = _norm_calls(n, x, res, dy, up, arg)
+    _busy(torch.cuda.current_stream())
+    dec = _make_decoder(w)
+    got.append(dec(rows, stream=arg))
+    _same(_bytes(got), want)
+    dec.check_status()
+    with torch.cuda.stream(side):              # the stream as the current one
+        _busy(torch.cuda.default_stream())
+    n = _make_norm(wn)
+    with torch.cuda.stream(side):
+        got = _norm_calls(n, x, res, dy, up, None)
+    _same(_bytes(got), want[:-1])
