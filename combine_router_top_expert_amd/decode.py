@@ -45,6 +45,9 @@ class MoEDecoder(StreamUser):
         self.update_weights(w_gate, w_up, w_down)
         self._ready()
 
+    def _buffers(self):
+        return super()._buffers() + self.weights.tensors
+
     def update_weights(self, w_gate, w_up, w_down, stream=None):
         """Other expert weights of the same sizes in the place of the ones
         there: quantised on `stream` into the same memory, so captured calls

@@ -27,8 +27,10 @@ class StreamUser:
 
     def _enter(self, stream):
         """A call on `stream` begins, with the device current.  The first one on
-        a stream comes after what made the object.  Not in a capture, which
-        waits for nothing outside it."""
+        a stream comes after what made the object, and from then on the memory
+        of its buffers is not given to others before that stream is done with
+        it, though the object goes.  Not in a capture, which waits for nothing
+        outside it and whose owner keeps what it uses."""
         if self._streams is None or self.device.type != "cuda":
             return
         handle = _stream(stream)
@@ -41,6 +43,12 @@ class StreamUser:
         self._streams.add(handle)
         if self._made is not None:
             s.wait_event(self._made)
+        for t in self._buffers():
+            t.record_stream(s)
+
+    def _buffers(self):
+        """The tensors that the object holds."""
+        return [t for t in vars(self).values() if isinstance(t, torch.Tensor)]
 
     def _torch_stream(self, stream):
         """The torch stream of a call's `stream` (None: the current one, or a raw handle)."""

@@ -1,5 +1,5 @@
-"""How the classes around the layer order themselves over streams, on
-the CPU with streams that note what is asked of them."""
+"""How the classes around the layer order themselves over streams and hold
+their memory, on the CPU with streams that note what is asked of them."""
 import pytest
 import torch
 
@@ -7,8 +7,9 @@ import combine_router_top_expert_amd as mok
 import combine_router_top_expert_amd.block as block_mod
 import combine_router_top_expert_amd.decode as decode_mod
 import combine_router_top_expert_amd.streams as streams_mod
-from combine_router_top_expert_amd.block import RMSNorm
+from combine_router_top_expert_amd.block import MoEBlock, RMSNorm
 from combine_router_top_expert_amd.decode import MoEDecoder
+from combine_router_top_expert_amd.layer import MoELayer
 from combine_router_top_expert_amd.streams import StreamUser
 
 BF = torch.bfloat16
@@ -23,6 +24,14 @@ class _Stream:
 
     def wait_event(self, e):
         self.notes.append((self.cuda_stream, "waits for", e))
+
+
+class _Buffer:
+    def __init__(self, notes):
+        self.notes = notes
+
+    def record_stream(self, s):
+        self.notes.append(("held for", s.cuda_stream))
 
 
 @pytest.fixture
@@ -56,13 +65,16 @@ def test_first_call_on_a_stream_comes_after_the_making(gpu):
 
     class User(StreamUser):
         device = torch.device("cuda", 0)
+
+        def _buffers(self):
+            return [_Buffer(notes), _Buffer(notes)]
     u = User()
     u._ready()
     u._enter(None)
     u._enter(streams[0])
     assert not notes
     u._enter(streams[1])
-    first = [(1, "waits for", "event of 0")]
+    first = [(1, "waits for", "event of 0"), ("held for", 1), ("held for", 1)]
     assert notes == first
     u._enter(streams[1])
     with on(streams[1]):
@@ -75,7 +87,7 @@ def test_first_call_on_a_stream_comes_after_the_making(gpu):
     streams[2].captured = False
     with on(streams[2]):
         u._enter(None)
-    assert notes[1:] == [(2, "waits for", "event of 0")]
+    assert notes[3:] == [(2, "waits for", "event of 0"), ("held for", 2), ("held for", 2)]
     # made within a capture: no event to wait for outside it
     notes.clear()
     streams[0].captured = True
@@ -83,7 +95,7 @@ def test_first_call_on_a_stream_comes_after_the_making(gpu):
     u._ready()
     streams[0].captured = False
     u._enter(streams[1])
-    assert not notes
+    assert notes == [("held for", 1), ("held for", 1)]
 
 
 @pytest.fixture
@@ -114,3 +126,18 @@ def test_calls_enter_on_their_stream(entered, gpu):
     entered.clear()
     d.update_weights(*w, stream=s)
     assert entered[0] == ("MoEDecoder", s) and "mok_mxfp4_quantize" in entered
+
+
+def test_buffers_are_all_that_the_calls_name(entered):
+    """Every tensor that a call reads or writes beside its arguments is held."""
+    n = RMSNorm(torch.ones(64, dtype=BF), 4, mx=True, res_type="f32")
+    own = {id(t) for t in n._buffers()}
+    assert all(id(t) in own for t in (n.weight, n.res, n.y, n.codes, n.scales, n.rstd, n.d_r, n.d_x, n.dw, n.ws))
+    w = [torch.zeros(2, 128, 128, dtype=BF)] * 3
+    d = MoEDecoder(torch.zeros(8, 128, dtype=BF), torch.zeros(8), torch.zeros(8, dtype=torch.int32), *w, 2, 4)
+    own = {id(t) for t in d._buffers()}
+    assert all(id(t) in own for t in (d.w_router, d.bias, d.e2l, d.topk_idx, d.topk_gate, d.out, d.ws, d.status,
+                                      *d.weights.tensors))
+    L = MoELayer(1, 4, 64, 4, 2, 64, 4, "bf16", 8, 0, 1, device="cpu", two_streams=False, transposed_weights=False)
+    b = MoEBlock(L, torch.ones(64, dtype=BF))
+    assert id(b.dw_norm) in {id(t) for t in b.norms[0]._buffers()}

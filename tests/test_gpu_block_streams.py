@@ -47,6 +47,11 @@ def _bytes(ts):
     return [t.clone().view(torch.uint8) for t in ts]
 
 
+def _churn(buffers):
+    """New tensors as large as these, so that memory given back too early is written over."""
+    return [torch.full((t.numel() * t.element_size(),), 0xFF, dtype=torch.uint8, device=DEV) for t in buffers for _ in range(2)]
+
+
 @pytest.mark.parametrize("raw", [False, True])
 def test_first_call_on_another_stream(raw):
     """Made behind a busy stream, used on an idle one: after the zeros of dw and status, and the weights' layout."""
@@ -71,3 +76,45 @@ def test_first_call_on_another_stream(raw):
     with torch.cuda.stream(side):
         got = _norm_calls(n, x, res, dy, up, None)
     _same(_bytes(got), want[:-1])
+
+
+@pytest.mark.parametrize("raw", [False, True])
+def test_objects_go_before_their_calls_are_done(raw):
+    """Deleted while their calls wait on a busy stream: the memory serves others only afterwards."""
+    _log("block deleted", raw)
+    wn, x, res, dy, up = _norm_inputs()
+    w, rows = _decoder_inputs()
+    want = _bytes(_norm_calls(_make_norm(wn), x, res, dy, up, None)) + _bytes([_make_decoder(w)(rows)])
+    side = torch.cuda.Stream()
+    arg = side.cuda_stream if raw else side
+    n, dec = _make_norm(wn), _make_decoder(w)
+    torch.cuda.synchronize()
+    _busy(side)
+    got = _norm_calls(n, x, res, dy, up, arg)
+    got.append(dec(rows, stream=arg))
+    sizes = [torch.empty(t.numel() * t.element_size(), dtype=torch.uint8) for t in n._buffers() + dec._buffers()]
+    del n, dec
+    junk = _churn(sizes)
+    _same(_bytes(got), want)
+    assert all(bool((t == 0xFF).all()) for t in junk)
+
+
+def test_weights_of_a_busy_stream():
+    """Other weights, given and let go of while a busy stream has yet to read them."""
+    _log("block weights stream")
+    w, rows = _decoder_inputs()
+    dec = _make_decoder(w)
+    dec.update_weights(2 * w[1], w[2], w[3])
+    want = _bytes([dec(rows)])
+    dec = _make_decoder(w)
+    side = torch.cuda.Stream()
+    new = [2 * w[1], w[2].clone(), w[3].clone()]
+    torch.cuda.synchronize()
+    _busy(side)
+    dec.update_weights(*new, stream=side)
+    sizes = [torch.empty(t.numel() * t.element_size(), dtype=torch.uint8) for t in new]
+    del new
+    junk = _churn(sizes)
+    got = dec(rows, stream=side)
+    _same(_bytes([got]), want)
+    del junk
