@@ -410,8 +410,13 @@ def make_w4(w_gate, w_up, w_down, s_gate, s_up, s_down, stream=None, into=None) 
     w_gate, w_up uint8 [E_local, I, d/2], w_down [E_local, d, I/2], scales
     s_* [..., K/32].  Lays them out as ``mok_decode_ffn`` reads them
     (``mok_mxfp4_tile``), in new tensors that the result holds, or in those of
-    an earlier result of the same sizes (into)."""
+    an earlier result of the same sizes (into).  On `stream` it comes after the
+    current one's work, and the tensors are held for it."""
+    import contextlib
     import torch
+    from .streams import StreamUser
+    user = StreamUser()
+    user.device = w_gate.device
     rows = []
     for w, s in ((w_gate, s_gate), (w_up, s_up), (w_down, s_down)):
         K, n = 2 * w.shape[-1], w.numel() // w.shape[-1]
@@ -427,8 +432,12 @@ def make_w4(w_gate, w_up, w_down, s_gate, s_up, s_down, stream=None, into=None) 
         tensors = into.tensors
         if [t.numel() for t in tensors] != sizes or tensors[0].device != w_gate.device:
             raise ValueError("weights of other sizes, or on another device")
-    for i, (n, K, w, s) in enumerate(rows):
-        mok_mxfp4_tile(n, K, w, s, tensors[2 * i], tensors[2 * i + 1], stream)
+    on_gpu = w_gate.device.type == "cuda"
+    with torch.cuda.device(w_gate.device) if on_gpu else contextlib.nullcontext():
+        if on_gpu:
+            user._after_current(stream, *tensors, *(t for _, _, w, s in rows for t in (w, s)))
+        for i, (n, K, w, s) in enumerate(rows):
+            mok_mxfp4_tile(n, K, w, s, tensors[2 * i], tensors[2 * i + 1], stream)
     r = mok_w4(*(t.data_ptr() for t in tensors[0::2] + tensors[1::2])) if into is None else into
     r.tensors = tensors
     return r

@@ -141,3 +141,48 @@ def test_buffers_are_all_that_the_calls_name(entered):
     L = MoELayer(1, 4, 64, 4, 2, 64, 4, "bf16", 8, 0, 1, device="cpu", two_streams=False, transposed_weights=False)
     b = MoEBlock(L, torch.ones(64, dtype=BF))
     assert id(b.dw_norm) in {id(t) for t in b.norms[0]._buffers()}
+
+
+def test_w4_on_a_stream(gpu, monkeypatch):
+    """The layout runs with the weights' device current, after the current stream's work (which may still write the
+    codes, or use the memory that the new tensors got), and what it reads and writes is held for its stream."""
+    streams, notes, on = gpu
+    seen = []
+
+    class Tensor:
+        """A tensor that calls itself one of a GPU."""
+        dtype, device = torch.uint8, torch.device("cuda", 1)
+
+        def __init__(self, *shape):
+            self.shape, self.t = shape, torch.zeros(*shape, dtype=torch.uint8)
+
+        def numel(self):
+            return self.t.numel()
+
+        def is_contiguous(self):
+            return True
+
+        def data_ptr(self):
+            return self.t.data_ptr()
+
+        def record_stream(self, s):
+            notes.append((id(self), s.cuda_stream))
+    devices = []
+
+    class Device(on):
+        def __enter__(self):
+            devices.append(self.what)
+            super().__enter__()
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    monkeypatch.setattr(torch, "empty", lambda n, dtype, device: Tensor(n))
+    monkeypatch.setattr(_Stream, "wait_stream", lambda self, s: notes.append((self.cuda_stream, "waits for", s.cuda_stream)),
+                        raising=False)
+    monkeypatch.setattr(mok, "mok_mxfp4_tile", lambda *a: seen.append((a, list(notes), list(devices))))
+    w, s = Tensor(2, 16, 64), Tensor(2, 16, 4)
+    r = mok.make_w4(w, w, w, s, s, s, stream=streams[1])
+    for args, before, made_on in seen:
+        assert args[-1] is streams[1] and made_on == [torch.device("cuda", 1)]
+        assert before[0] == (1, "waits for", 0)
+        held = {i for i, h in before[1:] if h == 1}
+        assert held >= {id(t) for t in (*r.tensors, w, s)}
+    assert len(seen) == 3

@@ -4,6 +4,7 @@ stream."""
 import pytest
 import torch
 
+import combine_router_top_expert_amd as mok
 from combine_router_top_expert_amd.block import RMSNorm
 from combine_router_top_expert_amd.decode import MoEDecoder
 from test_gpu_train import DEV, _gen, _log
@@ -117,4 +118,25 @@ def test_weights_of_a_busy_stream():
     junk = _churn(sizes)
     got = dec(rows, stream=side)
     _same(_bytes([got]), want)
+    del junk
+
+
+@pytest.mark.parametrize("raw", [False, True])
+def test_w4_on_a_busy_stream(raw):
+    """Codes that the current stream still writes, laid out on a busy stream and let go of at once."""
+    _log("w4 stream", raw)
+    g = _gen(6)
+    codes = [torch.randint(0, 256, (2, 256, 128), generator=g, dtype=torch.uint8).to(DEV) for _ in range(3)]
+    scales = [torch.randint(118, 123, (2, 256, 8), generator=g, dtype=torch.uint8).to(DEV) for _ in range(3)]
+    want = _bytes(mok.make_w4(*codes, *scales).tensors)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    _busy(side)
+    _busy(torch.cuda.current_stream())
+    mine = [t.clone() for t in codes + scales]
+    w = mok.make_w4(*mine, stream=side.cuda_stream if raw else side)
+    sizes = [torch.empty(t.numel(), dtype=torch.uint8) for t in mine]
+    del mine
+    junk = _churn(sizes)
+    _same(_bytes(w.tensors), want)
     del junk
