@@ -13,8 +13,9 @@ def test_forward(T, d, prec, res):
     norm.test_forward(T, d, prec, res)
 
 
+# and a wave a row, with one unit a thread and many rows, with two units and the most rows of one launch
 @pytest.mark.parametrize("prec,res", norm.TYPES)
-@pytest.mark.parametrize("T,d", [(600, 16448), (1100, 8256), (1025, 16384), (1030, 4160)])
+@pytest.mark.parametrize("T,d", [(600, 16448), (1100, 8256), (1025, 16384), (1030, 4160), (1030, 448), (1024, 1024), (1024, 576)])
 def test_backward(T, d, prec, res):
     norm.test_backward(T, d, prec, res)
 
