@@ -109,6 +109,8 @@ class MoEBlock(StreamUser):
         prec = "f32" if layer.prec == "f32" else "bf16"
         if weight.numel() != layer.d:
             raise ValueError(f"norm weight of {layer.d} elements expected, got {weight.numel()}")
+        if weight.device != layer.status.device:
+            raise ValueError(f"norm weight on {weight.device}, and the layer on {layer.status.device}")
         # (before the norms: their calls come after what made them)
         self.dw_norm = torch.zeros(layer.d, dtype=torch.float32, device=weight.device) if layer.with_bwd else None
         self.norms = [RMSNorm(weight, layer.T_src, prec, res_type, eps, with_bwd=layer.with_bwd) for _ in self.own]

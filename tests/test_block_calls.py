@@ -121,3 +121,10 @@ def test_block_without_own_sources(calls):
     assert b.forward([]) == []
     assert b.backward([torch.zeros(4, 64, dtype=BF)] * 2) == []
     assert (b.dw_norm == 0).all()
+
+
+def test_block_on_one_device(calls):
+    """The layer reads the norms' rows: a weight of another device would put them there."""
+    L = _block().layer
+    with pytest.raises(ValueError, match="meta"):
+        MoEBlock(L, torch.ones(64, dtype=BF, device="meta"))
