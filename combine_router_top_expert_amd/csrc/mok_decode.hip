@@ -2,10 +2,14 @@
 //   out_t = sum over its slots j of gate_tj W_down (silu(W_gate x_t) * W_up x_t)
 // with the matrices of the slot's expert, E2M1 codes with one E8M0 scale per
 // 32 along the contraction (MXFP4).  Two products and a sum:
-//   gate_up   h_n = silu(a) b of every item n = (t, j), rounded to bf16 (the
-//             operand of the second product);
+//   gate_up   h_n = silu(a) b of every item n = (t, j), rounded to bf16;
 //   down      y_n = W_down h_n, fp32;
 //   combine   out_t, fp32 sums over j in order, rounded once.
+// h is the second product's operand, which the matrix cores take in bf16 beside
+// weights that need bf16's range, and is what the layer rounds to as well; as
+// two bf16 parts it would take twice the instructions and LDS.  It makes the
+// output's error 1.4 times that of one rounding at the end (2.3e-3 against
+// 1.7e-3 of the norm).
 //
 // Bound by the weights' bytes.  A workgroup takes some columns of an expert's
 // matrices and all of that expert's items, so a matrix is read once however
@@ -32,10 +36,10 @@
 // kPlanItems on the library's expert-contiguous layout.
 //
 // Measured, us (floor: the bytes at 6.27 TB/s): 1 token, d 2048, I 1408, 64
-// experts, top-6: 12.3 (4.4), two launches; 61 tokens: 61 (47), 39 + 21 + 5 in
-// its launches, of which the weights' stream alone takes 36 + 18; 512 tokens at 8
-// of 256 experts, d 7168, I 2048, top-8: 55 (32), 34 + 17 + 6, the stream alone
-// 31 + 13.
+// experts, top-6: 12.2 (4.4), two launches of 6.6 and 5.8; 61 tokens: 61 (47),
+// 37 + 20 + 5 in its launches, of which the weights' stream alone takes 36 + 18;
+// 512 tokens at 8 of 256 experts, d 7168, I 2048, top-8: 55 (32), 33 + 16 + 6, the
+// stream alone 31 + 13.
 #include <string.h>
 
 #include <type_traits>
@@ -51,9 +55,14 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
 constexpr int kChunk = 128;           // contraction elements of a step: 4 blocks
-// Items that a workgroup looks through itself (61 tokens with room for 1024: 38
-// us, for 4096: 40; 512 tokens at 8 of 256 experts: 34 us with room for 4096, 39
-// with a launch for the search).
+// Items that a workgroup looks through itself: room for them costs registers
+// and LDS whatever their number, a launch for the search (beyond the limit) 3 to
+// 5 us.  First product of 61 tokens with room for 1024 38 us, for 4096 40.  Whole
+// calls, d 7168, 8 of 256 experts, top-8, with a limit of 1024, 2048, 4096 and
+// 8192: 256 tokens 43.2, 40.4, 40.5, 41.1 us; 512 tokens 49.9, 50.0, 46.1, 46.7; 513
+// 51.3, 51.2, 51.3, 48.1; 1000 77, 77, 77, 68; d 2048, 64 experts, top-6: 300
+// tokens 94.0, 88.9, 89.7, 91.0; 682 141, 141, 137, 140; 1000 176, 176, 176, 179.
+// 4096 loses at most 0.8 us below it to a smaller limit; 8192 loses up to 3.
 constexpr int kListItems = 1024, kLongListItems = 4096;
 
 struct DecodeArgs {
@@ -286,8 +295,9 @@ __device__ __forceinline__ void item_operands(const void* row, const uint8_t* sc
 // the order in which a wave reads them: per tile of 16 rows and chunk, 64 lanes
 // of 16 bytes, lane (r, g) with block g of row r; per tile and four chunks, 64
 // lanes of 4 scales, lane (r, g) with block g of row r in each of the four.  A
-// load is one run of memory (row by row, 16 runs of 64 bytes, a wave reaches
-// 4.3 TB/s where this reaches 4.7).
+// load is one run of memory (the stream alone, four chunks ahead with a wait
+// for all of them: 4.7 TB/s, row by row, in 16 runs of 64 bytes, 4.3; the loop as
+// it is reaches 5.4 with the products).
 template <int NM>
 struct Weights {
   const uint8_t* codes[NM];

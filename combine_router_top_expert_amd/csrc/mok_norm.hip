@@ -12,13 +12,13 @@
 // that goes out is written from there.  Short rows go to a wave or a part of one
 // (no barrier between the sum and the outputs), others to a workgroup; rows
 // longer than 16384 elements are read twice.  Workgroups stride over the
-// rows, so the weight is loaded once per workgroup.
+// rows; the weight is read again for every row, from the caches.
 //
 // Measured, bf16 (a copy of the same bytes streams at 5.2 TB/s): 16384 x 2048
 // with y and MX blocks 58 us, 5.2 TB/s; 32749 x 7168 with an fp32 stream 511
 // us, 5.5 TB/s; its backward on 16381 rows 360 us, 5.2 TB/s, 7 of them the
-// second sum of d_w.  1 x 7168 forward 6.5 us, 512 x 256 fp32 backward 5.8, most
-// of both the launch.
+// second sum of d_w.  1 x 7168 forward 6.7 us a call, 3.6 of kernel, 512 x 256
+// fp32 backward 6.0 and 4.5; a call of one wave takes 4.3 and 1.8.
 #include "mok_internal.h"
 #include "mok_lanes.h"
 #include "mok_mx.h"
@@ -418,9 +418,9 @@ __device__ __forceinline__ void norm_dw_columns(const NormBwdArgs& a, int tile) 
 }
 
 // Few rows: d_w needs no row's sum, so its columns are summed in the same
-// launch by workgroups of their own, which read dy and r a second time (512 x
-// 256: 8.6 us in two launches, 5.9 in one; 1024 x 1024 8.5 and 6.0; 1024 x 7168
-// 19.5 and 13.3; 2000 x 2048 11 and 26).
+// launch by workgroups of their own, which read dy and r a second time (us a
+// call, in two launches and in one: 512 x 256 8.6 and 6.0; 1024 x 1024 8.5 and
+// 6.0; 1024 x 7168 19.5 and 13.3; 2000 x 2048 11 and 26).
 template <typename TX, typename TR, int L, int NV>
 __global__ __launch_bounds__(block_of<L>()) void norm_bwd_few_kernel(NormBwdArgs a) {
   const int tiles = a.dw ? a.d / few_columns(block_of<L>()) : 0;
