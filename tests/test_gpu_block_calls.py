@@ -108,3 +108,66 @@ def test_layers_that_checkpoint_with_a_ring_backward(mb, slots):
         C.backward(dout)
         for i, (a, b) in enumerate(zip(g, _grads(C))):
             assert torch.equal(a, b), i
+
+
+@pytest.mark.parametrize("prec", ["f32", "bf16"])
+def test_captured_step_with_balance_losses(prec):
+    """Forward, losses and backward(balance=True) of two sources, captured: every replay gives the eager bytes for
+    the rows that are there then."""
+    _log("captured balance", prec)
+    S, T, d, E, k, I = 2, 70, 128, 8, 2, 192
+    gen, dt = _gen(5), torch.float32 if prec == "f32" else torch.bfloat16
+    rnd = lambda *s, std=1.0: (std * torch.randn(*s, generator=gen)).to(DEV, dt)  # noqa: E731
+    w = [rnd(E, d, std=d ** -0.5), rnd(E, I, d, std=d ** -0.5), rnd(E, I, d, std=d ** -0.5), rnd(E, d, I, std=I ** -0.5)]
+    wn = (1 + 0.2 * torch.randn(d, generator=gen)).to(DEV, dt)
+
+    def build():
+        L = MoELayer(S, T, d, E, k, I, E, prec, S * T * k, 0, S, device=DEV, keep_logits=True, two_streams=False)
+        b = MoEBlock(L, wn, "f32")
+        b.set_inputs(w[0], None, torch.arange(E, dtype=torch.int32, device=DEV), *w[1:])
+        return b
+    rows = [[(2 * torch.randn(T, d, generator=gen)).to(DEV) for _ in range(S)] for _ in range(3)]
+    dout, dl = [rnd(T, d) for _ in range(S)], torch.tensor([300.0, 20.0], device=DEV)
+
+    def step(b, res):
+        out = b.forward(res)
+        loss = b.layer.balance_loss(1.0, 1.0)
+        g = b.backward(dout, balance=True, d_loss=dl)
+        return [*out, loss, *g, b.dw_norm, b.layer.dw_router, b.layer.dw_gate]
+    eager, b = build(), build()
+    slot = [t.clone() for t in rows[0]]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step(b, slot)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step(b, slot)
+    for i in (0, 1, 2, 0):
+        for t, r in zip(slot, rows[i]):
+            t.copy_(r)
+        graph.replay()
+        torch.cuda.synchronize()
+        want = step(eager, rows[i])
+        torch.cuda.synchronize()
+        for j, (a, c) in enumerate(zip(got, want)):
+            assert torch.equal(a, c), (i, j)
+        assert not torch.equal(want[3], torch.zeros_like(want[3]))
+    b.layer.check_status()
+
+
+def test_calls_without_rows():
+    """No tokens: the norm, its backward and the decoder return empty rows, and the weight's gradient is zero."""
+    from combine_router_top_expert_amd.block import RMSNorm
+    n = RMSNorm(torch.ones(128, device=DEV, dtype=torch.bfloat16), 4, "bf16", "f32", mx=True)
+    x = torch.zeros(0, 128, device=DEV, dtype=torch.bfloat16)
+    n.dw.fill_(float("nan"))
+    assert n.forward(x).shape == (0, 128) and n.backward(x).shape == (0, 128)
+    torch.cuda.synchronize()
+    assert (n.dw == 0).all()
+    L, _ = _layer("bf16", 11, d=128, I=128)
+    dec = L.decoder(4)
+    assert dec(x).shape == (0, 128)
+    torch.cuda.synchronize()
+    dec.check_status()
