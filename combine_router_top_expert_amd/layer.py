@@ -42,15 +42,17 @@ class MoELayer(StreamUser):
         """checkpoint: what the backward needs of the expert FFN is kept in 8
         bits after the forward (ck_codes, ck_scales), and ab and h are scratch;
         scratch: a layer of the same sizes whose ab and h this one uses too, so
-        that a stack of layers holds one pair.  (An MXFP8 layer keeps its own h,
-        which holds 8-bit codes already.)"""
+        that a stack of layers holds one pair: their calls on different
+        streams, and replays of captured ones, are ordered by the caller.  (An
+        MXFP8 layer keeps its own h, which holds 8-bit codes already.)"""
         assert S <= MAX_SOURCES
         if checkpoint and not with_bwd:
             raise ValueError("a checkpoint is for the backward: with_bwd")
         if scratch is not None:
-            same = ("S", "T_src", "I", "prec", "R_cap", "device")
-            mine = dict(S=S, T_src=T_src, I=I, prec=prec, R_cap=R_cap, device=torch.device(device))
-            if not (checkpoint and scratch.checkpoint) or any(getattr(scratch, n) != mine[n] for n in same):
+            mine = dict(S=S, T_src=T_src, I=I, prec=prec, R_cap=R_cap)
+            where = torch.empty(0, device=device).device          # with its number ("cuda" names the current one)
+            if not (checkpoint and scratch.checkpoint) or where != scratch.status.device or any(
+                    getattr(scratch, n) != v for n, v in mine.items()):
                 raise ValueError("scratch is shared between checkpointing layers of the same sizes, type and device")
         self.S, self.T_src, self.d, self.E, self.k, self.I = S, T_src, d, E, k, I
         self.E_local, self.prec, self.R_cap = E_local, prec, R_cap

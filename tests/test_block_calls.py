@@ -128,3 +128,13 @@ def test_block_on_one_device(calls):
     L = _block().layer
     with pytest.raises(ValueError, match="meta"):
         MoEBlock(L, torch.ones(64, dtype=BF, device="meta"))
+
+
+def test_scratch_of_the_same_device_by_another_name(calls):
+    """"cuda" and "cuda:0" (here "cpu" and "cpu:0") name one device; another one is refused."""
+    make = lambda device, **kw: MoELayer(1, 4, 64, 4, 2, 64, 4, "bf16", 8, 0, 1, device=device, two_streams=False,  # noqa: E731
+                                         checkpoint=True, **kw)
+    a = make("cpu")
+    assert make("cpu:0", scratch=a).ab is a.ab
+    with pytest.raises(ValueError, match="device"):
+        make("meta", scratch=a)
