@@ -1124,6 +1124,7 @@ mok_status mok_norm_bwd(const mok_config* cfg, int32_t T, const void* dy, const 
       !aligned(d_res, 16) || !aligned(d_r, 16) || !aligned(d_x, 16) || !aligned(d_weight, 4))
     return MOK_EINVAL;
   if (!d_r && !d_x && !d_weight) return MOK_EINVAL;
+  if (d_weight && cfg->d >= 1 << 26) return MOK_EINVAL;  // 1024 threads for 16 columns in one launch
   if (T == 0 && (!d_weight || accumulate != 0)) return MOK_OK;
   trace_mark(cfg->trace, "start", (hipStream_t)stream);
   return launch_norm_bwd(act_prec(cfg), res_type, T, cfg->d, dy, res, weight, rstd, d_res, d_r, d_x,

@@ -574,7 +574,8 @@ size_t mok_norm_bwd_ws_bytes(const mok_config* cfg, int32_t T);
  * overwritten, or with accumulate != 0 added to; without rows it becomes zero
  * (or stays).  It is summed over at most 64 rows in fp32 and then in 64 bits,
  * in a fixed order.  d_r may be d_res; nothing else may overlap.  ws is
- * needed for d_weight.  Pointers 16-byte aligned (rstd and d_weight 4). */
+ * needed for d_weight, and d below 2^26.  Pointers 16-byte aligned (rstd and
+ * d_weight 4). */
 mok_status mok_norm_bwd(const mok_config* cfg, int32_t T, const void* dy, const void* res,
                         int32_t res_type, const void* weight, const float* rstd, const void* d_res,
                         void* d_r, void* d_x, float* d_weight, int32_t accumulate, void* ws,
