@@ -120,12 +120,14 @@ class MoELayer(StreamUser):
             self.dw_up = torch.zeros(E_local, I, d, dtype=torch.float32, device=dev)
             self.dw_down = torch.zeros(E_local, d, I, dtype=torch.float32, device=dev)
             self.dw_router = torch.zeros(E, d, dtype=torch.float32, device=dev)
+        self._ready()
 
     # ---------------------------------------------------------------- inputs
     def set_inputs(self, xs: List[torch.Tensor], w_router, bias, e2l, w_gate, w_up, w_down,
                    other_topk: Optional[List] = None):
         """xs: S device tensors [T_src, d]; other_topk: per non-own source
-        (topk_idx [T_src, k] int32, topk_gate [T_src, k] fp32) numpy arrays."""
+        (topk_idx [T_src, k] int32, topk_gate [T_src, k] fp32) numpy arrays.
+        What the layer forms of the weights is formed on the current stream."""
         self.xs = xs
         self.w_router = w_router
         self.bias = bias
@@ -149,6 +151,7 @@ class MoELayer(StreamUser):
                                         wt_gu=self.wt[1])
         else:
             self.weights = make_weights(w_gate, w_up, w_down)
+        self._ready()
 
     def set_peer_slots(self, s: int, y: torch.Tensor, d_gate: torch.Tensor,
                        dx: Optional[torch.Tensor] = None):
@@ -169,6 +172,7 @@ class MoELayer(StreamUser):
         transposed copies, the MX codes -- in the same buffers.  A layer in
         fp32, or in bf16 without transposed weights, keeps nothing."""
         with torch.cuda.device(self.device):
+            self._enter(stream)
             w = (self.w_gate, self.w_up, self.w_down)
             if self.prec == "mxfp8":
                 for t, (codes, scales) in zip(w, self.wq):
@@ -198,6 +202,7 @@ class MoELayer(StreamUser):
 
     # ---------------------------------------------------------------- passes
     def forward(self, stream=None):
+        self._enter(stream)
         mok_layer_fwd(self.cfg, self.own_lo, self.own_n, self.xs, self.w_router, self.bias,
                       self.e2l, self.weights, self.state, self.staging, self.out, self.ws,
                       self.status, stream)
@@ -221,6 +226,8 @@ class MoELayer(StreamUser):
             need = max(need, mok_workspace_bytes(c))
         if need > self.ws.numel():
             self.ws = torch.zeros(need, dtype=torch.uint8, device=self.device)
+            self._ready()
+        self._enter(stream)
         best, table = mok_tune_fwd(self.cfg, mbs, comms, reps, self.ws.numel(), self.own_lo,
                                    self.own_n, self.xs, self.w_router, self.bias, self.e2l,
                                    self.weights, self.state, self.staging, self.out, self.ws,
@@ -233,6 +240,7 @@ class MoELayer(StreamUser):
 
     def backward(self, d_out: List[torch.Tensor], stream=None, router_grad=True):
         dw_router = self.dw_router if router_grad else None
+        self._enter(stream)
         self._d_x_read = False
         if self.checkpoint and self.prec == "bf16" and not self.cfg.bwd_ring_bytes:
             mok_layer_bwd_checkpoint(self.cfg, self.own_lo, self.own_n, d_out, self.xs, self.w_router, self.e2l,
@@ -292,9 +300,9 @@ class MoELayer(StreamUser):
     def balance_backward(self, d_loss=None, stream=None):
         """Adds the gradient of d_loss[0] * balance loss + d_loss[1] * z-loss
         (d_loss fp32 [2] on the device, None = ones) to d_x and dw_router,
-        after backward() (in a block: MoEBlock.backward(balance=True)).  With a router bias, d_bias [E] becomes these
-        losses' gradient of it; backward() forms none, so the share that comes
-        through the gates is not in it."""
+        after backward() (in a block: MoEBlock.backward(balance=True)).  With a
+        router bias, d_bias [E] becomes these losses' gradient of it; backward()
+        forms none, so the share that comes through the gates is not in it."""
         if getattr(self, "_bal", None) is None or not self.with_bwd:
             raise RuntimeError("balance_backward needs balance_loss and backward before it")
         if self._d_x_read:

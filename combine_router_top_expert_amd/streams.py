@@ -17,7 +17,7 @@ class StreamUser:
         """The object is made: its buffers are filled, or may be memory that
         others used, by work of the current stream, which calls on other
         streams come after (_enter)."""
-        self._streams = set()
+        self._streams, self._made = set(), None
         if self.device.type == "cuda":
             with torch.cuda.device(self.device):
                 s = torch.cuda.current_stream()
@@ -47,8 +47,15 @@ class StreamUser:
             t.record_stream(s)
 
     def _buffers(self):
-        """The tensors that the object holds."""
-        return [t for t in vars(self).values() if isinstance(t, torch.Tensor)]
+        """The tensors that the object holds on its device."""
+        found, more, where = [], list(vars(self).values()), self._where()
+        while more:
+            t = more.pop()
+            if isinstance(t, (list, tuple)):
+                more.extend(t)
+            elif isinstance(t, torch.Tensor) and t.device == where:
+                found.append(t)
+        return found
 
     def _torch_stream(self, stream):
         """The torch stream of a call's `stream` (None: the current one, or a raw handle)."""

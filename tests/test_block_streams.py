@@ -6,6 +6,7 @@ import torch
 import combine_router_top_expert_amd as mok
 import combine_router_top_expert_amd.block as block_mod
 import combine_router_top_expert_amd.decode as decode_mod
+import combine_router_top_expert_amd.layer as layer_mod
 import combine_router_top_expert_amd.streams as streams_mod
 from combine_router_top_expert_amd.block import MoEBlock, RMSNorm
 from combine_router_top_expert_amd.decode import MoEDecoder
@@ -186,3 +187,25 @@ def test_w4_on_a_stream(gpu, monkeypatch):
         held = {i for i, h in before[1:] if h == 1}
         assert held >= {id(t) for t in (*r.tensors, w, s)}
     assert len(seen) == 3
+
+
+def test_layer_enters_on_its_stream(gpu, monkeypatch):
+    """The layer's zeros, 8-bit checkpoint and transposed weights are work of the current stream too."""
+    seen = []
+    monkeypatch.setattr(StreamUser, "_enter", lambda self, s: seen.append(s))
+    for n in ("mok_layer_fwd", "mok_layer_bwd", "mok_layer_bwd_checkpoint", "mok_checkpoint_pack", "mok_prepare_bwd"):
+        monkeypatch.setattr(layer_mod, n, lambda *a, _n=n, **k: seen.append(_n))
+    L = MoELayer(1, 4, 64, 4, 2, 64, 4, "bf16", 8, 0, 1, device="cpu", two_streams=False, checkpoint=True)
+    w = [torch.zeros(4, 64, dtype=BF), None, torch.arange(4, dtype=torch.int32)] + [torch.zeros(4, 64, 64, dtype=BF)] * 3
+    before = L._streams
+    L.set_inputs([torch.zeros(4, 64, dtype=BF)], *w)
+    assert before is not None and L._streams is not before       # made anew on the current stream
+    s = gpu[0][1]
+    seen.clear()
+    L.forward(s)
+    L.backward([torch.zeros(4, 64, dtype=BF)], s)
+    L.update_weights(s)
+    assert seen == [s, "mok_layer_fwd", "mok_checkpoint_pack", s, "mok_layer_bwd_checkpoint", s, "mok_prepare_bwd"]
+    own = {id(t) for t in L._buffers()}
+    assert all(id(t) in own for t in (L.ck_codes, L.ck_scales, L.ab, L.h, L.ws, L.status, *L.staging, *L.out, *L.dx_stage,
+                                      *L.d_x, *L.wt, L.dw_gate, L.dw_up, L.dw_down, L.dw_router, L.w_gate, L.offsets))

@@ -7,6 +7,7 @@ import torch
 import combine_router_top_expert_amd as mok
 from combine_router_top_expert_amd.block import RMSNorm
 from combine_router_top_expert_amd.decode import MoEDecoder
+from combine_router_top_expert_amd.layer import MoELayer
 from test_gpu_train import DEV, _gen, _log
 from test_gpu_train_streams import _busy, _same
 
@@ -140,3 +141,37 @@ def test_w4_on_a_busy_stream(raw):
     junk = _churn(sizes)
     _same(_bytes(w.tensors), want)
     del junk
+
+
+@pytest.mark.parametrize("prec", ["f32", "bf16", "mxfp8"])
+def test_layer_on_another_stream(prec):
+    """A checkpointing layer made behind a busy stream and run at once on another, and deleted before that is done."""
+    _log("layer stream", prec)
+    S, T, d, E, k, I, dt = 1, 64, 128, 4, 2, 128, torch.float32 if prec == "f32" else BF
+    g = _gen(3)
+    rnd = lambda *s: (s[-1] ** -0.5 * torch.randn(*s, generator=g)).to(DEV, dt)  # noqa: E731
+    x, dout, w = rnd(T, d), rnd(T, d), [rnd(E, d), rnd(E, I, d), rnd(E, I, d), rnd(E, d, I)]
+    e2l = torch.arange(E, dtype=torch.int32, device=DEV)
+
+    def run(side):
+        torch.cuda.synchronize()
+        if side is not None:
+            _busy(torch.cuda.current_stream())
+        L = MoELayer(S, T, d, E, k, I, E, prec, T * k, 0, 1, device=DEV, checkpoint=True, two_streams=False)
+        L.set_inputs([x], w[0], None, e2l, *w[1:])
+        if side is not None:
+            L.forward(side)
+            _busy(side)
+        else:
+            L.forward()
+        L.backward([dout], side)
+        out = [L.out[0], L.d_x[0], L.dw_gate, L.dw_router, L.ck_codes]
+        if side is not None:
+            keep = {t.data_ptr() for t in (*out, x, *w, e2l)}
+            large = [torch.empty(t.numel() * t.element_size(), dtype=torch.uint8) for t in L._buffers() if t.data_ptr() not in keep]
+            del L
+            junk = _churn(large)
+            del junk
+        return _bytes(out)
+    want = run(None)
+    _same(run(torch.cuda.Stream()), want)
