@@ -241,6 +241,7 @@ class MoELayer(StreamUser):
     def backward(self, d_out: List[torch.Tensor], stream=None, router_grad=True):
         dw_router = self.dw_router if router_grad else None
         self._enter(stream)
+        self._hold(stream, *d_out)
         self._d_x_read = False
         if self.checkpoint and self.prec == "bf16" and not self.cfg.bwd_ring_bytes:
             mok_layer_bwd_checkpoint(self.cfg, self.own_lo, self.own_n, d_out, self.xs, self.w_router, self.e2l,

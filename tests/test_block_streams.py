@@ -209,3 +209,14 @@ def test_layer_enters_on_its_stream(gpu, monkeypatch):
     own = {id(t) for t in L._buffers()}
     assert all(id(t) in own for t in (L.ck_codes, L.ck_scales, L.ab, L.h, L.ws, L.status, *L.staging, *L.out, *L.dx_stage,
                                       *L.d_x, *L.wt, L.dw_gate, L.dw_up, L.dw_down, L.dw_router, L.w_gate, L.offsets))
+
+
+def test_backward_holds_the_gradients_it_is_given(gpu, monkeypatch):
+    """d_out is read by work on the call's stream, though its owner lets it go."""
+    streams, notes, _ = gpu
+    for n in ("mok_layer_bwd",):
+        monkeypatch.setattr(layer_mod, n, lambda *a, **k: notes.append("backward"))
+    L = MoELayer(2, 4, 64, 4, 2, 64, 4, "bf16", 8, 0, 2, device="cpu", two_streams=False, transposed_weights=False)
+    L.xs, L.w_router, L.bias, L.e2l, L.weights = [], None, None, None, None
+    L.backward([_Buffer(notes), None], streams[1])
+    assert notes == [("held for", 1), "backward"]
