@@ -193,6 +193,7 @@ def test_layer_enters_on_its_stream(gpu, monkeypatch):
     """The layer's zeros, 8-bit checkpoint and transposed weights are work of the current stream too."""
     seen = []
     monkeypatch.setattr(StreamUser, "_enter", lambda self, s: seen.append(s))
+    monkeypatch.setattr(StreamUser, "_hold", lambda self, s, *t: None)
     for n in ("mok_layer_fwd", "mok_layer_bwd", "mok_layer_bwd_checkpoint", "mok_checkpoint_pack", "mok_prepare_bwd"):
         monkeypatch.setattr(layer_mod, n, lambda *a, _n=n, **k: seen.append(_n))
     L = MoELayer(1, 4, 64, 4, 2, 64, 4, "bf16", 8, 0, 1, device="cpu", two_streams=False, checkpoint=True)
